@@ -29,6 +29,7 @@ STATUS = {
 # name -> (restype, argtypes) for every symbol of include/w4q.h
 _P, _I64, _INT, _SZ, _U32P = (ctypes.c_void_p, ctypes.c_int64, ctypes.c_int, ctypes.c_size_t,
                               ctypes.POINTER(ctypes.c_uint32))
+_F = ctypes.c_float
 SIGNATURES = {
     "w4q_status_string": (ctypes.c_char_p, [_INT]),
     "w4_packed_bytes": (_SZ, [_I64, _I64, _INT]),
@@ -57,6 +58,13 @@ SIGNATURES = {
     "w4_pack_weights_compact": (_INT, [_P, _I64, _I64, _INT, _P, _P]),
     "w4_unpack_weights_compact": (_INT, [_P, _I64, _I64, _INT, _P, _P, _P, _P, _P]),
     "w4a16_gemm_compact": (_INT, [_P, _P, _P, _I64, _I64, _I64, _INT, _P]),
+    "qk_norm_rope": (_INT, [_P, _P, _I64, _INT, _INT, _INT, _I64, _I64, _P, _P, _F, _P, _I64, _INT,
+                            _INT, _P, _P, _P, _P]),
+    "kv8_append": (_INT, [_P, _P, _P, _I64, _I64, _I64, _P, _P, _I64, _INT, _P, _P, _P, _F, _P, _I64,
+                          _INT, _INT, _P]),
+    "kv8_read": (_INT, [_P, _P, _I64, _P, _P, _P]),
+    "kv8_attention": (_INT, [_P, _P, _I64, _P, _P, _INT, _INT, _F, _I64, _P, _SZ, _P]),
+    "kv8_workspace_bytes": (_SZ, [_I64, _INT, _INT, _INT, _INT]),
     "w4q_device_error": (_INT, [_U32P]),
     "w4q_selftest_wait_expiry": (_INT, [ctypes.c_uint, _P]),
 }
@@ -348,6 +356,187 @@ def w8_gemm(x, W, scales, out=None, workspace=None, stream=None):
     pws = _cuda(workspace, torch.uint8, "workspace") if workspace is not None else None
     nbytes = workspace.numel() if workspace is not None else 0
     _check("w8_gemm", lib().w8_gemm(px, pw, ps, po, M, N, K, pws, nbytes, _stream(stream)))
+    return out
+
+
+# ------------------------------------------------ between the linear layers
+
+class _Kv8Cache(ctypes.Structure):
+    """w4q_kv8_cache of include/w4q.h."""
+    _fields_ = [("k", _P), ("v", _P), ("k_scale", _P), ("v_scale", _P), ("block_table", _P),
+                ("seq_lens", _P), ("blocks", _I64), ("seqs", ctypes.c_int32),
+                ("width", ctypes.c_int32), ("kv_heads", ctypes.c_int32),
+                ("head_dim", ctypes.c_int32), ("page", ctypes.c_int32), ("format", ctypes.c_int32)]
+
+
+def _new(make, shape, dtype, device, stream):
+    """make(shape) (torch.empty or torch.zeros) on the stream that the call
+    runs on, so that its memory belongs to that stream and a fill comes first."""
+    if stream is None:
+        return make(shape, dtype=dtype, device=device)
+    if not hasattr(stream, "cuda_stream"):
+        stream = torch.cuda.ExternalStream(int(stream))
+    with torch.cuda.stream(stream):
+        return make(shape, dtype=dtype, device=device)
+
+
+def _heads(t: torch.Tensor, name: str, tokens=None, heads=None, dim=None):
+    """(pointer, row stride) of head rows bf16 [tokens, heads, head_dim]: a
+    token's heads lie one after the other, tokens may lie further apart."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise ValueError("%s must be a CUDA tensor" % name)
+    if t.dtype != torch.bfloat16 or t.dim() != 3:
+        raise ValueError("%s must be bfloat16 [tokens, heads, head_dim]" % name)
+    n, h, d = t.shape
+    if (tokens is not None and n != tokens) or (heads is not None and h != heads) or \
+            (dim is not None and d != dim):
+        raise ValueError("%s must be [%s, %s, %s], got %s" % (
+            name, "*" if tokens is None else tokens, "*" if heads is None else heads,
+            "*" if dim is None else dim, tuple(t.shape)))
+    s0, s1, s2 = t.stride()
+    if (d > 1 and s2 != 1) or (h > 1 and s1 != d):
+        raise ValueError("a token's heads must lie one after the other in %s" % name)
+    return t.data_ptr(), s0 if n > 1 else h * d
+
+
+def _optional(t, dtype, name, numel=None):
+    if t is None:
+        return None
+    p = _cuda(t, dtype, name)
+    if numel is not None and t.numel() != numel:
+        raise ValueError("%s must have %d elements, got %d" % (name, numel, t.numel()))
+    return p
+
+
+def _table(cos_sin):
+    if cos_sin is None:
+        return None, 0, 0
+    if cos_sin.dim() != 2:
+        raise ValueError("cos_sin must be [positions, rot]")
+    return _cuda(cos_sin, torch.float32, "cos_sin"), cos_sin.shape[0], cos_sin.shape[1]
+
+
+def qk_norm_rope(q, k=None, q_weight=None, k_weight=None, cos_sin=None, positions=None, eps=1e-6,
+                 interleaved=False, q_out=None, k_out=None, stream=None):
+    """(q, k) normed per head and rotated, bf16 [tokens, heads, head_dim]
+    (k may be None).  cos_sin: fp32 [positions, rot], the cosines of the
+    rot / 2 angles of a position, then the sines; positions: int32 [tokens]."""
+    pq, sq = _heads(q, "q")
+    n, hq, d = q.shape
+    pk, sk, hk = None, 0, 0
+    if k is not None:
+        pk, sk = _heads(k, "k", n, None, d)
+        hk = k.shape[1]
+    pt, npos, rot = _table(cos_sin)
+    if q_out is None:
+        q_out = _new(torch.empty, (n, hq, d), torch.bfloat16, q.device, stream)
+    po = _optional(q_out, torch.bfloat16, "q_out", n * hq * d)
+    if k is not None and k_out is None:
+        k_out = _new(torch.empty, (n, hk, d), torch.bfloat16, q.device, stream)
+    pko = _optional(k_out, torch.bfloat16, "k_out", n * hk * d)
+    _check("qk_norm_rope", lib().qk_norm_rope(
+        pq, pk, n, hq, hk, d, sq, sk, _optional(q_weight, torch.bfloat16, "q_weight", d),
+        _optional(k_weight, torch.bfloat16, "k_weight", d), eps, pt, npos, rot, bool(interleaved),
+        _optional(positions, torch.int32, "positions", n), po, pko, _stream(stream)))
+    return q_out, k_out
+
+
+def _kv8(k_cache, v_cache, k_scale, v_scale, block_table, seq_lens):
+    blocks, kv_heads, page, d = k_cache.shape
+    if k_cache.dtype not in (torch.int8, torch.float8_e4m3fn):
+        raise ValueError("k_cache must be int8 or float8_e4m3fn, got %s" % k_cache.dtype)
+    if v_cache.shape != k_cache.shape:
+        raise ValueError("k_cache and v_cache must have one shape")
+    if block_table.dim() != 2 or seq_lens.dim() != 1 or block_table.shape[0] != seq_lens.shape[0]:
+        raise ValueError("block_table must be [seqs, width], seq_lens [seqs]")
+    n = blocks * kv_heads
+    return _Kv8Cache(
+        _cuda(k_cache, k_cache.dtype, "k_cache"), _cuda(v_cache, k_cache.dtype, "v_cache"),
+        _optional(k_scale, torch.float32, "k_scale", n), _optional(v_scale, torch.float32, "v_scale", n),
+        _cuda(block_table, torch.int32, "block_table"), _cuda(seq_lens, torch.int32, "seq_lens"),
+        blocks, block_table.shape[0], block_table.shape[1], kv_heads, d, page,
+        0 if k_cache.dtype == torch.int8 else 1)
+
+
+def _cu(cu_tokens, seqs):
+    return _optional(cu_tokens, torch.int32, "cu_tokens", seqs + 1)
+
+
+def kv8_append(k, v, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, cu_tokens=None,
+               q=None, q_out=None, q_weight=None, k_weight=None, cos_sin=None, eps=1e-6,
+               interleaved=False, stream=None):
+    """Write the step's keys and values bf16 [tokens, kv_heads, head_dim] into
+    the 8-bit cache (k_cache, v_cache: int8 or float8_e4m3fn [blocks,
+    kv_heads, page, head_dim]; scales fp32 [blocks, kv_heads]), the keys normed
+    and rotated first where k_weight / cos_sin are given.  seq_lens counts the
+    new tokens; cu_tokens int32 [seqs + 1], or None: one token each.  With q,
+    returns the queries normed and rotated too (q_out), else None."""
+    c = _kv8(k_cache, v_cache, k_scale, v_scale, block_table, seq_lens)
+    n, d = k.shape[0], c.head_dim
+    pk, sk = _heads(k, "k", None, c.kv_heads, d)
+    pv, sv = _heads(v, "v", n, c.kv_heads, d)
+    pq, sq, hq, po = None, 0, 0, None
+    if q is not None:
+        pq, sq = _heads(q, "q", n, None, d)
+        hq = q.shape[1]
+        if q_out is None:
+            q_out = _new(torch.empty, (n, hq, d), torch.bfloat16, q.device, stream)
+        po = _optional(q_out, torch.bfloat16, "q_out", n * hq * d)
+    pt, npos, rot = _table(cos_sin)
+    _check("kv8_append", lib().kv8_append(
+        ctypes.byref(c), pk, pv, sk, sv, n, _cu(cu_tokens, c.seqs), pq, sq, hq, po,
+        _optional(q_weight, torch.bfloat16, "q_weight", d),
+        _optional(k_weight, torch.bfloat16, "k_weight", d), eps, pt, npos, rot, bool(interleaved),
+        _stream(stream)))
+    return q_out
+
+
+def kv8_read(k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, cu_tokens=None, tokens=None,
+             stream=None):
+    """(k, v) bf16 [tokens, kv_heads, head_dim]: what the cache holds of the
+    last cu_tokens[b + 1] - cu_tokens[b] positions of each sequence (None: the
+    last one).  tokens: cu_tokens' last value, known on the host."""
+    c = _kv8(k_cache, v_cache, k_scale, v_scale, block_table, seq_lens)
+    if tokens is None:
+        if cu_tokens is not None:
+            raise ValueError("tokens must be given with cu_tokens")
+        tokens = c.seqs
+    k = _new(torch.empty, (tokens, c.kv_heads, c.head_dim), torch.bfloat16, k_cache.device, stream)
+    v = _new(torch.empty, k.shape, torch.bfloat16, k_cache.device, stream)
+    _check("kv8_read", lib().kv8_read(ctypes.byref(c), _cu(cu_tokens, c.seqs), tokens, k.data_ptr(),
+                                      v.data_ptr(), _stream(stream)))
+    return k, v
+
+
+def kv8_workspace_bytes(seqs: int, queries: int, heads: int, kv_heads: int, head_dim: int) -> int:
+    return int(lib().kv8_workspace_bytes(seqs, queries, heads, kv_heads, head_dim))
+
+
+def kv8_attention(q, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, scale=None,
+                  window=0, out=None, lse=None, workspace=None, stream=None):
+    """Attention of q bf16 [seqs, queries, heads, head_dim], the last tokens of
+    their sequences, over the 8-bit cache; scale None: head_dim ** -0.5.
+    window > 0: each query sees the last `window` positions up to its own.
+    lse: fp32 [seqs, queries, heads] to be written, or None.  workspace:
+    kv8_workspace_bytes bytes, zero before the first use (one is made if it is
+    None)."""
+    c = _kv8(k_cache, v_cache, k_scale, v_scale, block_table, seq_lens)
+    if q.dim() != 4 or q.shape[0] != c.seqs or q.shape[3] != c.head_dim:
+        raise ValueError("q must be [%d, queries, heads, %d]" % (c.seqs, c.head_dim))
+    n, m, hq, d = q.shape
+    if n > 1 and m > 1 and q.stride(0) != m * q.stride(1):
+        raise ValueError("the query tokens must lie at one stride in q")
+    pq, sq = _heads(q[:, 0] if m == 1 else q.flatten(0, 1), "q")
+    if out is None:
+        out = _new(torch.empty, (n, m, hq, d), torch.bfloat16, q.device, stream)
+    po = _optional(out, torch.bfloat16, "out", n * m * hq * d)
+    if workspace is None:
+        workspace = _new(torch.zeros, (max(16, kv8_workspace_bytes(n, m, hq, c.kv_heads, d)),), torch.uint8,
+                         q.device, stream)
+    _check("kv8_attention", lib().kv8_attention(
+        ctypes.byref(c), pq, sq, po, _optional(lse, torch.float32, "lse", n * m * hq), m, hq,
+        d ** -0.5 if scale is None else scale, window, _cuda(workspace, workspace.dtype, "workspace"),
+        workspace.numel() * workspace.element_size(), _stream(stream)))
     return out
 
 

@@ -376,6 +376,117 @@ size_t w8_workspace_bytes(int64_t M, int64_t N, int64_t K);
  * invalid sizes. */
 int w8_kernel_launches(int64_t M, int64_t N, int64_t K);
 
+/* ------------------------- between the linear layers of a decode step --- */
+
+/* Head rows: bf16 [tokens][heads][head_dim], the heads of a token one after
+ * the other, `stride` elements from token to token (a multiple of 8), so the
+ * parts of a fused query / key / value projection can be given as they lie.
+ * head_dim is 64, 128 or 256. */
+
+/* Norm and rotation of the query and key heads, in one pass and in fp32:
+ *   y = x / sqrt(mean(x^2) + eps) * weight     (where a weight is given)
+ *   (y_a, y_b) = (y_a c - y_b s, y_b c + y_a s) (where a table is given)
+ * for the rot / 2 pairs (a, b) = (i, i + rot / 2), or (2i, 2i + 1) with
+ * interleaved != 0; c = cos_sin[pos][i], s = cos_sin[pos][rot / 2 + i];
+ * elements from rot on are not rotated; one rounding to bf16 at the end.
+ *   q, k        device, bf16 [tokens][q_heads | k_heads][head_dim], rows
+ *               q_stride, k_stride apart; k may be NULL with k_heads = 0
+ *   q_weight, k_weight  device, bf16 [head_dim], or NULL: no norm
+ *   cos_sin     device, fp32 [positions][rot], or NULL: no rotation; rot a
+ *               multiple of 16, at most head_dim
+ *   pos         device, int32 [tokens], or NULL: token i has position i.
+ *               Positions outside the table use its nearest row.
+ *   q_out, k_out  device, bf16 [tokens][heads][head_dim] (written)
+ * One launch; tokens = 0 launches nothing. */
+int qk_norm_rope(const void *q, const void *k, int64_t tokens, int q_heads,
+                 int k_heads, int head_dim, int64_t q_stride, int64_t k_stride,
+                 const void *q_weight, const void *k_weight, float eps,
+                 const float *cos_sin, int64_t positions, int rot,
+                 int interleaved, const int32_t *pos, void *q_out, void *k_out,
+                 void *stream);
+
+/* A paged key / value cache in 8 bits.  A page holds `page` consecutive
+ * positions of one sequence; its codes are row-major bytes
+ *   k, v               [blocks][kv_heads][page][head_dim]
+ * and stand for code * scale with one fp32 scale per (page, kv head):
+ *   k_scale, v_scale   [blocks][kv_heads].
+ * format 0: int8 codes in [-127, 127]; format 1: e4m3.
+ *   block_table  int32 [seqs][width]: the page of positions
+ *                [page i, page i + page) of a sequence.  An entry outside
+ *                [0, blocks) is a hole: nothing is written to it, the
+ *                attention leaves its positions out.
+ *   seq_lens     int32 [seqs]: the sequences' lengths, the tokens of the
+ *                current step among them; 0 (or less) is an idle sequence;
+ *                a length beyond width * page counts as width * page.
+ * All device pointers.  page is 16, 32, 64 or 128; seqs <= 4096; a page
+ * that a call appends to belongs to one sequence alone. */
+typedef struct {
+    void *k, *v;
+    float *k_scale, *v_scale;
+    const int32_t *block_table;
+    const int32_t *seq_lens;
+    int64_t blocks;
+    int32_t seqs, width, kv_heads, head_dim, page, format;
+} w4q_kv8_cache;
+
+/* Write the step's new keys and values into the cache.  Sequence b has the
+ * new tokens cu_tokens[b] .. cu_tokens[b + 1] - 1 of k and v (cu_tokens NULL:
+ * token b alone, tokens == seqs), and they are its last positions.  The keys
+ * are normed and rotated first as by qk_norm_rope (k_weight and cos_sin may
+ * be NULL), at their own positions and without being rounded to bf16.
+ * For every page and kv head, over the new rows y that fall into it, with
+ * top = 127 (int8) or 448 (e4m3), in IEEE fp32:
+ *   s' = max(s, max|y| / top)  (s = 0 if the page held no earlier token);
+ *   code = rint(y / s') clamped to [-127, 127], or e4m3(y / s') (to nearest
+ *   even, saturating); all codes 0 where s' = 0;
+ *   where s' > s, earlier tokens' codes become the code of code * (s / s').
+ *   k, v        device, bf16 [tokens][kv_heads][head_dim]
+ *   cu_tokens   device, int32 [seqs + 1], ascending from 0, or NULL
+ *   q, q_out    optional (q_heads = 0, NULL): the queries of the same
+ *               tokens, normed and rotated into q_out in the same launch
+ * One launch. */
+int kv8_append(const w4q_kv8_cache *cache, const void *k, const void *v,
+               int64_t k_stride, int64_t v_stride, int64_t tokens,
+               const int32_t *cu_tokens, const void *q, int64_t q_stride,
+               int q_heads, void *q_out, const void *q_weight,
+               const void *k_weight, float eps, const float *cos_sin,
+               int64_t positions, int rot, int interleaved, void *stream);
+
+/* The values that the last cu_tokens[b + 1] - cu_tokens[b] positions of each
+ * sequence stand for (cu_tokens NULL: the last one, tokens == seqs),
+ * bf16(code * scale), as k_out, v_out bf16 [tokens][kv_heads][head_dim];
+ * zeros for a hole and for positions before the first.  One launch. */
+int kv8_read(const w4q_kv8_cache *cache, const int32_t *cu_tokens,
+             int64_t tokens, void *k_out, void *v_out, void *stream);
+
+/* Attention of the last `queries` tokens of every sequence over the cache:
+ * query i of sequence b has position seq_lens[b] - queries + i and sees the
+ * positions up to its own, the last `window` of them if window > 0.
+ *   o = sum_p softmax_p(scale * q . k_p) v_p,  k_p, v_p the cache's values;
+ * heads = group * kv_heads, query head h reads kv head h / group.  A query
+ * that sees nothing (an idle sequence, a negative position) gives zeros and
+ * lse = -inf.
+ *   q    device, bf16 [seqs * queries][heads][head_dim], rows q_stride apart
+ *   out  device, bf16 [seqs][queries][heads][head_dim] (written)
+ *   lse  device, fp32 [seqs][queries][heads], natural log of the softmax's
+ *        sum (written), or NULL
+ *   workspace  device, >= kv8_workspace_bytes(...) bytes, zero-filled before
+ *        its first use; every call leaves its counters zero again, so one
+ *        buffer serves any calls of at most its size, one after the other
+ *        on the GPU (not two at a time).
+ * Sums, the running reference and the softmax's sum in fp32; the softmax's
+ * weights enter the second product with 11 bits.  queries * group <= 64,
+ * width * page < 2^31 - 128.  One launch. */
+int kv8_attention(const w4q_kv8_cache *cache, const void *q, int64_t q_stride,
+                  void *out, float *lse, int queries, int heads, float scale,
+                  int64_t window, void *workspace, size_t workspace_bytes,
+                  void *stream);
+
+/* Workspace bytes of kv8_attention on the current device; 0 for unsupported
+ * sizes. */
+size_t kv8_workspace_bytes(int64_t seqs, int queries, int heads, int kv_heads,
+                           int head_dim);
+
 /* ------------------------------------------------------------ status --- */
 
 /* Read and clear the device-side error word of the current device (set by
