@@ -77,6 +77,16 @@ int check_cache(const w4q_kv8_cache *c, w4q::Kv8 *out)
     return W4Q_OK;
 }
 
+int check_moe(int64_t tokens, int64_t hidden, int64_t inter, int64_t experts, int topk)
+{
+    if (tokens <= 0 || hidden <= 0 || inter <= 0 || experts <= 0 || topk <= 0 || topk > experts)
+        return W4Q_ERR_INVALID_ARG;
+    if (tokens > 64 || hidden % 256 != 0 || inter % 256 != 0 || hidden > 32768 || inter > 32768 || experts > 512 ||
+        topk > 16)
+        return W4Q_ERR_UNSUPPORTED;
+    return W4Q_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -194,6 +204,37 @@ int kv8_attention(const w4q_kv8_cache *cache, const void *q, int64_t q_stride, v
     const int win = window >= ((int64_t)c.width << c.page_log2) ? 0 : (int)window;
     return status(w4q::launch_kv8_attention(c, q, q_stride, out, lse, queries, heads, scale, win, sms, workspace,
                                             static_cast<cudaStream_t>(stream)));
+}
+
+size_t moe_workspace_bytes(int64_t tokens, int64_t hidden, int64_t inter, int64_t experts, int topk)
+{
+    if (check_moe(tokens, hidden, inter, experts, topk) != W4Q_OK)
+        return 0;
+    return w4q::moe_workspace((int)tokens, (int)hidden, (int)inter, topk);
+}
+
+int moe_w4a16(const void *x, const void *router, const float *bias, const void *w13, const void *w2, void *out,
+              int64_t tokens, int64_t hidden, int64_t inter, int64_t experts, int topk, int sigmoid, int renormalize,
+              float scale, int32_t *ids_out, float *weights_out, void *workspace, size_t workspace_bytes, void *stream)
+{
+    if (x == nullptr || router == nullptr || w13 == nullptr || w2 == nullptr || out == nullptr || !(scale == scale))
+        return W4Q_ERR_INVALID_ARG;
+    const int st = check_moe(tokens, hidden, inter, experts, topk);
+    if (st != W4Q_OK)
+        return st;
+    if (bias != nullptr && !sigmoid)
+        return W4Q_ERR_INVALID_ARG;
+    if (!aligned16(x) || !aligned16(router) || !aligned16(bias) || !aligned16(w13) || !aligned16(w2) ||
+        !aligned16(out) || !aligned16(ids_out) || !aligned16(weights_out) || !aligned16(workspace))
+        return W4Q_ERR_MISALIGNED;
+    if (workspace == nullptr || workspace_bytes < w4q::moe_workspace((int)tokens, (int)hidden, (int)inter, topk))
+        return W4Q_ERR_WORKSPACE;
+    const int sms = device_sms();
+    if (sms < 0)
+        return W4Q_ERR_CUDA;
+    const w4q::Moe a = {x, router, bias, w13, w2, out, ids_out, weights_out, (int)tokens, (int)hidden, (int)inter,
+                        (int)experts, topk, sigmoid != 0, renormalize != 0, scale};
+    return status(w4q::launch_moe(a, sms, workspace, static_cast<cudaStream_t>(stream)));
 }
 
 }  // extern "C"

@@ -65,4 +65,19 @@ cudaError_t launch_kv8_append(const Kv8 &c, const void *k, const void *v, int64_
 cudaError_t launch_kv8_read(const Kv8 &c, const int32_t *cu, int64_t tokens, void *k_out, void *v_out,
                             cudaStream_t stream);
 
+// --- mixture of experts (moe_w4.cu)
+struct Moe {
+    const void *x, *router;
+    const float *bias;
+    const void *w13, *w2;
+    void *out;
+    int32_t *ids_out;
+    float *weights_out;
+    int tokens, hidden, inter, experts, topk;
+    bool sigmoid, renormalize;
+    float scale;
+};
+size_t moe_workspace(int tokens, int hidden, int inter, int topk);
+cudaError_t launch_moe(const Moe &a, int sm_count, void *workspace, cudaStream_t stream);
+
 }  // namespace w4q

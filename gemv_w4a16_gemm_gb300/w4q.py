@@ -64,6 +64,9 @@ SIGNATURES = {
                           _INT, _INT, _P]),
     "kv8_read": (_INT, [_P, _P, _I64, _P, _P, _P]),
     "kv8_attention": (_INT, [_P, _P, _I64, _P, _P, _INT, _INT, _F, _I64, _P, _SZ, _P]),
+    "moe_w4a16": (_INT, [_P, _P, _P, _P, _P, _P, _I64, _I64, _I64, _I64, _INT, _INT, _INT, _F, _P, _P,
+                         _P, _SZ, _P]),
+    "moe_workspace_bytes": (_SZ, [_I64, _I64, _I64, _I64, _INT]),
     "kv8_workspace_bytes": (_SZ, [_I64, _INT, _INT, _INT, _INT]),
     "w4q_device_error": (_INT, [_U32P]),
     "w4q_selftest_wait_expiry": (_INT, [ctypes.c_uint, _P]),
@@ -537,6 +540,40 @@ def kv8_attention(q, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, 
         ctypes.byref(c), pq, sq, po, _optional(lse, torch.float32, "lse", n * m * hq), m, hq,
         d ** -0.5 if scale is None else scale, window, _cuda(workspace, workspace.dtype, "workspace"),
         workspace.numel() * workspace.element_size(), _stream(stream)))
+    return out
+
+
+def moe_workspace_bytes(tokens: int, hidden: int, inter: int, experts: int, topk: int) -> int:
+    return int(lib().moe_workspace_bytes(tokens, hidden, inter, experts, topk))
+
+
+def moe_w4a16(x, router, w13, w2, inter, topk, bias=None, sigmoid=False, renormalize=True, scale=1.0,
+              out=None, ids=None, weights=None, workspace=None, stream=None):
+    """A mixture-of-experts layer for x bf16 [tokens, hidden] (1..64 tokens):
+    router bf16 [experts, hidden]; w13 = w4_pack_weights of [experts * 2 *
+    inter, hidden] (an expert's gate rows, then its up rows); w2 =
+    w4_pack_weights of [experts * hidden, inter].  sigmoid: sigmoid scores, the
+    choice by score + bias (fp32 [experts] or None); else softmax.  ids, weights:
+    int32 / fp32 [tokens, topk] to be written, or None."""
+    if x.dim() != 2 or router.dim() != 2 or router.shape[1] != x.shape[1]:
+        raise ValueError("x must be [tokens, hidden], router [experts, hidden]")
+    m, h = x.shape
+    e = router.shape[0]
+    px, pr = _cuda(x, torch.bfloat16, "x"), _cuda(router, torch.bfloat16, "router")
+    p13, p2 = _cuda(w13, torch.uint8, "w13"), _cuda(w2, torch.uint8, "w2")
+    if w13.numel() != packed_bytes(e * 2 * inter, h) or w2.numel() != packed_bytes(e * h, inter):
+        raise ValueError("w13 and w2 must be packed from [%d, %d] and [%d, %d]" % (e * 2 * inter, h, e * h, inter))
+    if out is None:
+        out = _new(torch.empty, (m, h), torch.bfloat16, x.device, stream)
+    if workspace is None:
+        workspace = _new(torch.empty, (max(16, moe_workspace_bytes(m, h, inter, e, topk)),), torch.uint8,
+                         x.device, stream)
+    _check("moe_w4a16", lib().moe_w4a16(
+        px, pr, _optional(bias, torch.float32, "bias", e), p13, p2, _optional(out, torch.bfloat16, "out", m * h),
+        m, h, inter, e, topk, bool(sigmoid), bool(renormalize), scale,
+        _optional(ids, torch.int32, "ids", m * topk), _optional(weights, torch.float32, "weights", m * topk),
+        _cuda(workspace, workspace.dtype, "workspace"), workspace.numel() * workspace.element_size(),
+        _stream(stream)))
     return out
 
 

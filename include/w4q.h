@@ -487,6 +487,38 @@ int kv8_attention(const w4q_kv8_cache *cache, const void *q, int64_t q_stride,
 size_t kv8_workspace_bytes(int64_t seqs, int queries, int heads, int kv_heads,
                            int head_dim);
 
+/* A mixture-of-experts layer for 1..64 tokens, experts in the packed W4
+ * format of w4_pack_weights:
+ *   l = x . router^T (fp32 sums);  score = softmax(l), or sigmoid(l);
+ *   the topk experts with the largest l (softmax) or score + bias (sigmoid),
+ *   equal ones by the lower number;
+ *   weight = scale * score, divided by the chosen scores' sum if renormalize;
+ *   out[m] = bf16( sum_k weight * W2_e . bf16(silu(gate_e . x) * up_e . x) ),
+ * the sum over the choices in their order.  Weights are exact, sums fp32.
+ *   x        device, bf16 [tokens][hidden]
+ *   router   device, bf16 [experts][hidden]
+ *   bias     device, fp32 [experts], or NULL; only with sigmoid != 0
+ *   w13      device, w4_pack_weights of [experts * 2 * inter][hidden]: each
+ *            expert's gate rows, then its up rows
+ *   w2       device, w4_pack_weights of [experts * hidden][inter]
+ *   out      device, bf16 [tokens][hidden] (written)
+ *   ids_out, weights_out  device, int32 / fp32 [tokens][topk] (written), or
+ *            NULL: the choice and its weights
+ *   workspace  device, >= moe_workspace_bytes(...) bytes; contents are
+ *            clobbered
+ * hidden and inter are multiples of 256 up to 32768, experts <= 512,
+ * topk <= 16.  Only the chosen experts' weights are read.  Four launches. */
+int moe_w4a16(const void *x, const void *router, const float *bias,
+              const void *w13, const void *w2, void *out, int64_t tokens,
+              int64_t hidden, int64_t inter, int64_t experts, int topk,
+              int sigmoid, int renormalize, float scale, int32_t *ids_out,
+              float *weights_out, void *workspace, size_t workspace_bytes,
+              void *stream);
+
+/* Workspace bytes of moe_w4a16; 0 for unsupported sizes. */
+size_t moe_workspace_bytes(int64_t tokens, int64_t hidden, int64_t inter,
+                           int64_t experts, int topk);
+
 /* ------------------------------------------------------------ status --- */
 
 /* Read and clear the device-side error word of the current device (set by

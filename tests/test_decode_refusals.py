@@ -131,3 +131,28 @@ def test_refused_calls_write_nothing(cuda):
         w4q.qk_norm_rope(q[:, 0].transpose(0, 1))
     torch.cuda.synchronize()
     assert (out == 7.0).all() and (kc == 0).all()
+
+
+def moe(**changes):
+    a = dict(x=FAKE, router=FAKE, bias=None, w13=FAKE, w2=FAKE, out=FAKE, tokens=4, hidden=512, inter=256, experts=8, topk=2,
+             sigmoid=0, renormalize=1, scale=1.0, ids=None, weights=None, workspace=None, bytes=0, stream=None)
+    a.update(changes)
+    return w4q.lib().moe_w4a16(*a.values())
+
+
+@pytest.mark.parametrize("changes,status", [
+    (dict(x=None), 1), (dict(w2=None), 1), (dict(out=None), 1), (dict(tokens=0), 1), (dict(topk=0), 1), (dict(topk=9), 1),
+    (dict(inter=-256), 1), (dict(bias=FAKE), 1), (dict(scale=float("nan")), 1),
+    (dict(tokens=65), 2), (dict(hidden=300), 2), (dict(inter=128), 2), (dict(experts=513), 2), (dict(experts=40, topk=17), 2),
+    (dict(hidden=1 << 16), 2),
+    (dict(x=FAKE + 2), 3), (dict(w13=FAKE + 8), 3), (dict(ids=FAKE + 4), 3), (dict(workspace=FAKE + 4), 3),
+    (dict(), 4), (dict(workspace=FAKE, bytes=100), 4),
+])
+def test_moe(changes, status):
+    assert moe(**changes) == status
+
+
+def test_moe_workspace():
+    assert w4q.moe_workspace_bytes(4, 512, 256, 8, 2) > 4 * 512 * 2
+    assert w4q.moe_workspace_bytes(65, 512, 256, 8, 2) == 0
+    assert w4q.moe_workspace_bytes(4, 512, 100, 8, 2) == 0
