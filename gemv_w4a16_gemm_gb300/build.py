@@ -1,11 +1,14 @@
 """Build libw4q.so in-tree: one nvcc per translation unit (in parallel) for
-sm_103a, then one shared-library link.  No cmake, no torch extension."""
+sm_103a, then one shared-library link; and _w4q_binding.so, the Python module
+that marshals the decode-step operators' arguments, by g++ against the
+installed torch's headers.  No cmake."""
 from __future__ import annotations
 
 import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
@@ -14,6 +17,7 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libw4q.so")
+BINDING = os.path.join(PKG, "_w4q_binding.so")
 SOURCES = ("api.cu", "pack.cu", "pack_compact.cu", "gemv_w4.cu", "gemv_w4_cluster.cu",
            "gemv_w4_umma.cu", "w8.cu", "gemv_w8_umma.cu", "noalloc.cu", "selftest.cu",
            "api_decode.cu", "kv8_append.cu", "kv8_attention.cu", "moe_w4.cu")
@@ -39,6 +43,29 @@ def _stale(target: str, deps) -> bool:
     return any(os.path.getmtime(d) > t for d in deps)
 
 
+def _run(cmd):
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError("%s failed:\n%s\n%s" % (cmd[0], r.stdout, r.stderr))
+
+
+def _torch_dir() -> str:
+    import importlib.util
+    return os.path.dirname(importlib.util.find_spec("torch").origin)
+
+
+def _compile_binding(force: bool) -> str:
+    """The Python module of binding.cpp, compiled against the torch headers (no torch import)."""
+    src, obj = os.path.join(CSRC, "binding.cpp"), os.path.join(BUILD, "binding.o")
+    if force or _stale(obj, [src, os.path.join(INCLUDE, "w4q.h")]):
+        inc = os.path.join(_torch_dir(), "include")
+        cuda = os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(nvcc()))), "include")
+        _run(["g++", "-O2", "-std=c++17", "-fPIC", "-I", INCLUDE, "-isystem", inc,
+              "-isystem", os.path.join(inc, "torch", "csrc", "api", "include"), "-isystem", cuda,
+              "-isystem", sysconfig.get_paths()["include"], "-c", src, "-o", obj])
+    return obj
+
+
 def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) -> str:
     """Compile every CUDA translation unit and link libw4q.so; returns its path."""
     os.makedirs(BUILD, exist_ok=True)
@@ -59,8 +86,10 @@ def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) 
                 sys.stderr.write(r.stderr)
         return obj
 
-    with ThreadPoolExecutor(max_workers=len(SOURCES)) as ex:
+    with ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
+        binding = ex.submit(_compile_binding, force)
         objs = list(ex.map(compile_one, SOURCES))
+        binding_obj = binding.result()
     if force or _stale(LIB, objs):
         tmp = LIB + ".tmp%d" % os.getpid()
         cmd = [cc, *ARCH, "-shared", "-o", tmp, *objs, "-cudart", "static"]
@@ -68,6 +97,12 @@ def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) 
         if r.returncode != 0:
             raise RuntimeError("link failed:\n%s\n%s" % (r.stdout, r.stderr))
         os.replace(tmp, LIB)
+    if force or _stale(BINDING, [binding_obj, LIB]):
+        tmp = BINDING + ".tmp%d" % os.getpid()
+        lib = os.path.join(_torch_dir(), "lib")
+        _run(["g++", "-shared", "-o", tmp, binding_obj, LIB, "-L" + lib, "-lc10", "-lc10_cuda", "-ltorch_cpu",
+              "-ltorch_python", "-Wl,-rpath,$ORIGIN", "-Wl,-rpath," + lib])
+        os.replace(tmp, BINDING)
     return LIB
 
 

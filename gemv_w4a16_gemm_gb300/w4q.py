@@ -363,6 +363,10 @@ def w8_gemm(x, W, scales, out=None, workspace=None, stream=None):
 
 
 # ------------------------------------------------ between the linear layers
+#
+# These calls take a few microseconds on the GPU, so their arguments are
+# checked and marshalled by a native module (csrc/binding.cpp).  All tensors of
+# a call are on one device, which need not be the current one.
 
 class _Kv8Cache(ctypes.Structure):
     """w4q_kv8_cache of include/w4q.h."""
@@ -372,51 +376,21 @@ class _Kv8Cache(ctypes.Structure):
                 ("head_dim", ctypes.c_int32), ("page", ctypes.c_int32), ("format", ctypes.c_int32)]
 
 
-def _new(make, shape, dtype, device, stream):
-    """make(shape) (torch.empty or torch.zeros) on the stream that the call
-    runs on, so that its memory belongs to that stream and a fill comes first."""
-    if stream is None:
-        return make(shape, dtype=dtype, device=device)
-    if not hasattr(stream, "cuda_stream"):
-        stream = torch.cuda.ExternalStream(int(stream))
-    with torch.cuda.stream(stream):
-        return make(shape, dtype=dtype, device=device)
+_native_module = None
 
 
-def _heads(t: torch.Tensor, name: str, tokens=None, heads=None, dim=None):
-    """(pointer, row stride) of head rows bf16 [tokens, heads, head_dim]: a
-    token's heads lie one after the other, tokens may lie further apart."""
-    if not isinstance(t, torch.Tensor) or not t.is_cuda:
-        raise ValueError("%s must be a CUDA tensor" % name)
-    if t.dtype != torch.bfloat16 or t.dim() != 3:
-        raise ValueError("%s must be bfloat16 [tokens, heads, head_dim]" % name)
-    n, h, d = t.shape
-    if (tokens is not None and n != tokens) or (heads is not None and h != heads) or \
-            (dim is not None and d != dim):
-        raise ValueError("%s must be [%s, %s, %s], got %s" % (
-            name, "*" if tokens is None else tokens, "*" if heads is None else heads,
-            "*" if dim is None else dim, tuple(t.shape)))
-    s0, s1, s2 = t.stride()
-    if (d > 1 and s2 != 1) or (h > 1 and s1 != d):
-        raise ValueError("a token's heads must lie one after the other in %s" % name)
-    return t.data_ptr(), s0 if n > 1 else h * d
-
-
-def _optional(t, dtype, name, numel=None):
-    if t is None:
-        return None
-    p = _cuda(t, dtype, name)
-    if numel is not None and t.numel() != numel:
-        raise ValueError("%s must have %d elements, got %d" % (name, numel, t.numel()))
-    return p
-
-
-def _table(cos_sin):
-    if cos_sin is None:
-        return None, 0, 0
-    if cos_sin.dim() != 2:
-        raise ValueError("cos_sin must be [positions, rot]")
-    return _cuda(cos_sin, torch.float32, "cos_sin"), cos_sin.shape[0], cos_sin.shape[1]
+def _native():
+    """The loaded _w4q_binding.so; raises if it has not been built."""
+    global _native_module
+    if _native_module is None:
+        lib()
+        try:
+            from . import _w4q_binding
+        except ImportError as e:
+            raise RuntimeError("_w4q_binding.so is not built (run __graft_entry__.build() or "
+                               "python gemv_w4a16_gemm_gb300/build.py): %s" % e) from e
+        _native_module = _w4q_binding
+    return _native_module
 
 
 def qk_norm_rope(q, k=None, q_weight=None, k_weight=None, cos_sin=None, positions=None, eps=1e-6,
@@ -424,45 +398,12 @@ def qk_norm_rope(q, k=None, q_weight=None, k_weight=None, cos_sin=None, position
     """(q, k) normed per head and rotated, bf16 [tokens, heads, head_dim]
     (k may be None).  cos_sin: fp32 [positions, rot], the cosines of the
     rot / 2 angles of a position, then the sines; positions: int32 [tokens]."""
-    pq, sq = _heads(q, "q")
-    n, hq, d = q.shape
-    pk, sk, hk = None, 0, 0
-    if k is not None:
-        pk, sk = _heads(k, "k", n, None, d)
-        hk = k.shape[1]
-    pt, npos, rot = _table(cos_sin)
-    if q_out is None:
-        q_out = _new(torch.empty, (n, hq, d), torch.bfloat16, q.device, stream)
-    po = _optional(q_out, torch.bfloat16, "q_out", n * hq * d)
-    if k is not None and k_out is None:
-        k_out = _new(torch.empty, (n, hk, d), torch.bfloat16, q.device, stream)
-    pko = _optional(k_out, torch.bfloat16, "k_out", n * hk * d)
-    _check("qk_norm_rope", lib().qk_norm_rope(
-        pq, pk, n, hq, hk, d, sq, sk, _optional(q_weight, torch.bfloat16, "q_weight", d),
-        _optional(k_weight, torch.bfloat16, "k_weight", d), eps, pt, npos, rot, bool(interleaved),
-        _optional(positions, torch.int32, "positions", n), po, pko, _stream(stream)))
+    status, q_out, k_out = (_native_module or _native()).qk_norm_rope(
+        q, k, q_weight, k_weight, cos_sin, positions, eps, interleaved, q_out, k_out,
+        None if stream is None else _stream(stream))
+    if status:
+        raise W4QError("qk_norm_rope", status)
     return q_out, k_out
-
-
-def _kv8(k_cache, v_cache, k_scale, v_scale, block_table, seq_lens):
-    blocks, kv_heads, page, d = k_cache.shape
-    if k_cache.dtype not in (torch.int8, torch.float8_e4m3fn):
-        raise ValueError("k_cache must be int8 or float8_e4m3fn, got %s" % k_cache.dtype)
-    if v_cache.shape != k_cache.shape:
-        raise ValueError("k_cache and v_cache must have one shape")
-    if block_table.dim() != 2 or seq_lens.dim() != 1 or block_table.shape[0] != seq_lens.shape[0]:
-        raise ValueError("block_table must be [seqs, width], seq_lens [seqs]")
-    n = blocks * kv_heads
-    return _Kv8Cache(
-        _cuda(k_cache, k_cache.dtype, "k_cache"), _cuda(v_cache, k_cache.dtype, "v_cache"),
-        _optional(k_scale, torch.float32, "k_scale", n), _optional(v_scale, torch.float32, "v_scale", n),
-        _cuda(block_table, torch.int32, "block_table"), _cuda(seq_lens, torch.int32, "seq_lens"),
-        blocks, block_table.shape[0], block_table.shape[1], kv_heads, d, page,
-        0 if k_cache.dtype == torch.int8 else 1)
-
-
-def _cu(cu_tokens, seqs):
-    return _optional(cu_tokens, torch.int32, "cu_tokens", seqs + 1)
 
 
 def kv8_append(k, v, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, cu_tokens=None,
@@ -474,23 +415,11 @@ def kv8_append(k, v, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, 
     and rotated first where k_weight / cos_sin are given.  seq_lens counts the
     new tokens; cu_tokens int32 [seqs + 1], or None: one token each.  With q,
     returns the queries normed and rotated too (q_out), else None."""
-    c = _kv8(k_cache, v_cache, k_scale, v_scale, block_table, seq_lens)
-    n, d = k.shape[0], c.head_dim
-    pk, sk = _heads(k, "k", None, c.kv_heads, d)
-    pv, sv = _heads(v, "v", n, c.kv_heads, d)
-    pq, sq, hq, po = None, 0, 0, None
-    if q is not None:
-        pq, sq = _heads(q, "q", n, None, d)
-        hq = q.shape[1]
-        if q_out is None:
-            q_out = _new(torch.empty, (n, hq, d), torch.bfloat16, q.device, stream)
-        po = _optional(q_out, torch.bfloat16, "q_out", n * hq * d)
-    pt, npos, rot = _table(cos_sin)
-    _check("kv8_append", lib().kv8_append(
-        ctypes.byref(c), pk, pv, sk, sv, n, _cu(cu_tokens, c.seqs), pq, sq, hq, po,
-        _optional(q_weight, torch.bfloat16, "q_weight", d),
-        _optional(k_weight, torch.bfloat16, "k_weight", d), eps, pt, npos, rot, bool(interleaved),
-        _stream(stream)))
+    status, q_out, _ = (_native_module or _native()).kv8_append(
+        k, v, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, cu_tokens, q, q_out,
+        q_weight, k_weight, cos_sin, eps, interleaved, None if stream is None else _stream(stream))
+    if status:
+        raise W4QError("kv8_append", status)
     return q_out
 
 
@@ -499,15 +428,11 @@ def kv8_read(k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, cu_token
     """(k, v) bf16 [tokens, kv_heads, head_dim]: what the cache holds of the
     last cu_tokens[b + 1] - cu_tokens[b] positions of each sequence (None: the
     last one).  tokens: cu_tokens' last value, known on the host."""
-    c = _kv8(k_cache, v_cache, k_scale, v_scale, block_table, seq_lens)
-    if tokens is None:
-        if cu_tokens is not None:
-            raise ValueError("tokens must be given with cu_tokens")
-        tokens = c.seqs
-    k = _new(torch.empty, (tokens, c.kv_heads, c.head_dim), torch.bfloat16, k_cache.device, stream)
-    v = _new(torch.empty, k.shape, torch.bfloat16, k_cache.device, stream)
-    _check("kv8_read", lib().kv8_read(ctypes.byref(c), _cu(cu_tokens, c.seqs), tokens, k.data_ptr(),
-                                      v.data_ptr(), _stream(stream)))
+    status, k, v = (_native_module or _native()).kv8_read(
+        k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, cu_tokens, tokens,
+        None if stream is None else _stream(stream))
+    if status:
+        raise W4QError("kv8_read", status)
     return k, v
 
 
@@ -523,23 +448,11 @@ def kv8_attention(q, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, 
     lse: fp32 [seqs, queries, heads] to be written, or None.  workspace:
     kv8_workspace_bytes bytes, zero before the first use (one is made if it is
     None)."""
-    c = _kv8(k_cache, v_cache, k_scale, v_scale, block_table, seq_lens)
-    if q.dim() != 4 or q.shape[0] != c.seqs or q.shape[3] != c.head_dim:
-        raise ValueError("q must be [%d, queries, heads, %d]" % (c.seqs, c.head_dim))
-    n, m, hq, d = q.shape
-    if n > 1 and m > 1 and q.stride(0) != m * q.stride(1):
-        raise ValueError("the query tokens must lie at one stride in q")
-    pq, sq = _heads(q[:, 0] if m == 1 else q.flatten(0, 1), "q")
-    if out is None:
-        out = _new(torch.empty, (n, m, hq, d), torch.bfloat16, q.device, stream)
-    po = _optional(out, torch.bfloat16, "out", n * m * hq * d)
-    if workspace is None:
-        workspace = _new(torch.zeros, (max(16, kv8_workspace_bytes(n, m, hq, c.kv_heads, d)),), torch.uint8,
-                         q.device, stream)
-    _check("kv8_attention", lib().kv8_attention(
-        ctypes.byref(c), pq, sq, po, _optional(lse, torch.float32, "lse", n * m * hq), m, hq,
-        d ** -0.5 if scale is None else scale, window, _cuda(workspace, workspace.dtype, "workspace"),
-        workspace.numel() * workspace.element_size(), _stream(stream)))
+    status, out, _ = (_native_module or _native()).kv8_attention(
+        q, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, scale, window, out, lse,
+        workspace, None if stream is None else _stream(stream))
+    if status:
+        raise W4QError("kv8_attention", status)
     return out
 
 
@@ -555,25 +468,11 @@ def moe_w4a16(x, router, w13, w2, inter, topk, bias=None, sigmoid=False, renorma
     w4_pack_weights of [experts * hidden, inter].  sigmoid: sigmoid scores, the
     choice by score + bias (fp32 [experts] or None); else softmax.  ids, weights:
     int32 / fp32 [tokens, topk] to be written, or None."""
-    if x.dim() != 2 or router.dim() != 2 or router.shape[1] != x.shape[1]:
-        raise ValueError("x must be [tokens, hidden], router [experts, hidden]")
-    m, h = x.shape
-    e = router.shape[0]
-    px, pr = _cuda(x, torch.bfloat16, "x"), _cuda(router, torch.bfloat16, "router")
-    p13, p2 = _cuda(w13, torch.uint8, "w13"), _cuda(w2, torch.uint8, "w2")
-    if w13.numel() != packed_bytes(e * 2 * inter, h) or w2.numel() != packed_bytes(e * h, inter):
-        raise ValueError("w13 and w2 must be packed from [%d, %d] and [%d, %d]" % (e * 2 * inter, h, e * h, inter))
-    if out is None:
-        out = _new(torch.empty, (m, h), torch.bfloat16, x.device, stream)
-    if workspace is None:
-        workspace = _new(torch.empty, (max(16, moe_workspace_bytes(m, h, inter, e, topk)),), torch.uint8,
-                         x.device, stream)
-    _check("moe_w4a16", lib().moe_w4a16(
-        px, pr, _optional(bias, torch.float32, "bias", e), p13, p2, _optional(out, torch.bfloat16, "out", m * h),
-        m, h, inter, e, topk, bool(sigmoid), bool(renormalize), scale,
-        _optional(ids, torch.int32, "ids", m * topk), _optional(weights, torch.float32, "weights", m * topk),
-        _cuda(workspace, workspace.dtype, "workspace"), workspace.numel() * workspace.element_size(),
-        _stream(stream)))
+    status, out, _ = (_native_module or _native()).moe_w4a16(
+        x, router, w13, w2, inter, topk, bias, sigmoid, renormalize, scale, out, ids, weights,
+        workspace, None if stream is None else _stream(stream))
+    if status:
+        raise W4QError("moe_w4a16", status)
     return out
 
 

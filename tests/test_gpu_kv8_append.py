@@ -226,6 +226,18 @@ def test_read_returns_the_values(cuda, dtype, d, hkv):
     assert (k1[1] == 0).all() and torch.equal(k1[0], k[12])
 
 
+def test_no_tokens(cuda):
+    cache = Cache(2, 2, 2, 64, 16, I8)
+    dev = cache.to(cuda)
+    lens, cu = torch.zeros(2, dtype=torch.int32, device=cuda), torch.zeros(3, dtype=torch.int32, device=cuda)
+    none = torch.empty(0, 2, 64, dtype=torch.bfloat16, device=cuda)
+    q = w4q.kv8_append(none, none, *dev, lens, cu_tokens=cu, q=none)
+    k, v = w4q.kv8_read(*dev, lens, cu_tokens=cu, tokens=0)
+    qo, ko = w4q.qk_norm_rope(none, none)
+    assert q.shape == k.shape == v.shape == qo.shape == ko.shape == (0, 2, 64)
+    same(cache, dev[:4])
+
+
 def test_offsets_beyond_32_bits(cuda):
     hkv, page, d = 8, 64, 128
     blocks = (1 << 32) // (hkv * page * d) + 9
