@@ -29,9 +29,11 @@
 // and, of the positions 2t, 2t + 1, 2t + 8, 2t + 9, D / 8 consecutive bytes
 // (dims D / 8 * g on): whole rows of a warp's loads are consecutive in memory,
 // pages stay row-major, and a lane only ever uses bytes that it has loaded
-// itself.  So each lane keeps its own ring in shared memory, filled by cp.async
-// and read back with conflict-free 16-byte loads; nothing waits for another
-// thread inside the loop.
+// itself.  So the cache goes from global memory to registers and nowhere else:
+// the next tile's K is loaded as soon as this tile's is used up, its V likewise,
+// which keeps 2 to 4 KB a warp on the way.  (The same bytes through a ring of
+// cp.async in shared memory took 466 instructions a tile instead of 3xx and half
+// as long again: 434 us instead of xxx for 64 x 16000 x 8 heads.)
 //
 // Work.  One chunk = 16 W positions (a 16-position tile for each of the W
 // warps) of one (sequence, kv head, row tile).  All chunks of a call lie in one
@@ -74,23 +76,19 @@ struct AttnParams {
     float *part;            // [2 * CTAs][rows of a tile][D + 2]
 };
 
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src)
+__device__ __forceinline__ uint4 ldg_stream(const void *p)
 {
-    asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+    uint4 v;
+    asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "l"(p));
+    return v;
 }
-__device__ __forceinline__ void cp_async8(uint32_t dst, const void *src)
+__device__ __forceinline__ uint2 ldg_stream8(const void *p)
 {
-    asm volatile("cp.async.ca.shared.global.L2::128B [%0], [%1], 8;" ::"r"(dst), "l"(src) : "memory");
-}
-__device__ __forceinline__ void cp_async4(uint32_t dst, const void *src)
-{
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
-}
-__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void cp_async_wait()
-{
-    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+    uint2 v;
+    asm volatile("ld.global.nc.L1::no_allocate.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "l"(p));
+    return v;
 }
 
 __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
@@ -159,28 +157,24 @@ __device__ __forceinline__ Span span_of(const AttnParams &p, int b)
     return s;
 }
 
-// Dynamic shared memory of a CTA: the rings (reused to join the warps' sums),
-// then the chunks' prefix sums over the sequences.
-template <int D, int NT, int W, int S>
+// Dynamic shared memory of a CTA: the warps' sums, then the chunks' prefix
+// sums over the sequences.
+template <int D, int NT, int W>
 struct Smem {
-    static constexpr int TILE = 2 * 16 * D;       // bytes of K and V of a tile
-    static constexpr int META = 16;               // s_K, s_V, page
-    static constexpr int RING = S * (TILE + META);
     static constexpr int ROWS = 8 * NT;
     static constexpr int PITCH = D + 4;           // rows 2t, 2t + 1 of a half-warp fall into other banks
-    static constexpr int JOINED = (W * ROWS * PITCH + 2 * W * ROWS) * 4;
-    static constexpr int BASE = (W * RING > JOINED ? W * RING : JOINED + 15) / 16 * 16;
+    static constexpr int BASE = ((W * ROWS * PITCH + 2 * W * ROWS) * 4 + 15) / 16 * 16;
     static size_t bytes(int seqs) { return BASE + (size_t)(seqs + 1) * 4; }
 };
 
-template <int D, int NT, bool FP8, int W, int S, int CPS>
+template <int D, int NT, bool FP8, int W, int CPS>
 __global__ void __launch_bounds__(32 * W, CPS) kv8_attention_kernel(const AttnParams p)
 {
-    using SM = Smem<D, NT, W, S>;
-    constexpr int ROWS = SM::ROWS, THREADS = 32 * W, KC = D / 64, VB = D / 8, NM = D / 16;
+    using SM = Smem<D, NT, W>;
+    constexpr int ROWS = SM::ROWS, THREADS = 32 * W, KC = D / 64, VB = D / 8, VW = VB / 4, NM = D / 16;
     extern __shared__ __align__(16) uint8_t smem[];
     __shared__ unsigned s_last;
-    __shared__ long long s_warp[W];
+    __shared__ int s_warp[W];
     float *s_o = reinterpret_cast<float *>(smem);             // [W][ROWS][PITCH]
     float *s_m = s_o + W * ROWS * SM::PITCH;                  // [W][ROWS]
     float *s_l = s_m + W * ROWS;                              // [W][ROWS]
@@ -212,8 +206,8 @@ __global__ void __launch_bounds__(32 * W, CPS) kv8_attention_kernel(const AttnPa
 #pragma unroll
             for (int w = 0; w < W; ++w) {
                 if (w < warp)
-                    before += (int)s_warp[w];
-                all += (int)s_warp[w];
+                    before += s_warp[w];
+                all += s_warp[w];
             }
             if (b < p.c.seqs)
                 s_prefix[b] = before + x - n;
@@ -231,9 +225,6 @@ __global__ void __launch_bounds__(32 * W, CPS) kv8_attention_kernel(const AttnPa
     if (cta >= P)
         return;
     const long long begin = U * cta / P, end = U * (cta + 1) / P;
-
-    uint8_t *ring = smem + warp * SM::RING;
-    const uint32_t ring_s = smem_addr(ring);
 
     int b = 0;
     {
@@ -264,60 +255,65 @@ __global__ void __launch_bounds__(32 * W, CPS) kv8_attention_kernel(const AttnPa
         const int32_t *table = p.c.table + (int64_t)b * p.c.width;
         const int64_t page_bytes = (int64_t)D << p.c.page_log2;
 
-        auto page_of = [&](int j) -> int {  // the page of this warp's tile of chunk j, -1: none
-            const int tile = sp.first + j * W + warp;
-            if (j >= j1 || tile >= tiles_end)
+        // this warp's tiles: number i is tile0 + i W of the sequence, i < n
+        const int tile0 = sp.first + j0 * W + warp;
+        const int n = j1 - j0 - (tile0 + (j1 - 1 - j0) * W >= tiles_end ? 1 : 0);
+        // Page and scales of 32 tiles at a time, one a lane; the next 32 are fetched meanwhile.  A
+        // hole reads page 0 with zero scales and is masked.
+        auto page_of = [&](int i) -> int {
+            if (i >= n)
                 return -1;
-            const int pg = __ldg(table + (tile >> per_page));
+            const int pg = __ldg(table + ((tile0 + i * W) >> per_page));
             return (unsigned)pg < (unsigned)p.c.blocks ? pg : -1;
         };
-        auto issue = [&](int j, int stage, int pg) {
-            const uint32_t dst = ring_s + stage * (SM::TILE + SM::META);
-            if (pg >= 0) {
-                const int tile = sp.first + j * W + warp;
-                const int slot = (tile & ((1 << per_page) - 1)) << 4;
-                const int64_t ph = (int64_t)pg * p.c.kv_heads + h;
-                const int64_t at = ph * page_bytes + slot * D;
-                const uint8_t *ks = p.c.k + at + g * D + 16 * t;
-                const uint8_t *vs = p.c.v + at + 2 * t * D + VB * g;
+        auto scale_of = [&](const float *scales, int pg) -> float {
+            return pg >= 0 ? __ldg(scales + (int64_t)pg * p.c.kv_heads + h) : 0.f;
+        };
+        const uint8_t *k_lane = p.c.k + h * page_bytes + g * D + 16 * t;
+        const uint8_t *v_lane = p.c.v + h * page_bytes + 2 * t * D + VB * g;
+        const int64_t page_stride = page_bytes * p.c.kv_heads;
+        auto offset_of = [&](int i, int pg) -> int64_t {
+            return (pg < 0 ? 0 : pg) * page_stride + (((tile0 + i * W) & ((1 << per_page) - 1)) << 4) * D;
+        };
+        uint4 kr[KC][2];       // positions g, g + 8
+        uint32_t vr[4][VW];    // positions 2t, 2t + 1, 2t + 8, 2t + 9
+        auto load_k = [&](int64_t at) {
 #pragma unroll
-                for (int c = 0; c < KC; ++c) {
-                    cp_async16(dst + (2 * c) * 512 + lane * 16, ks + 64 * c);
-                    cp_async16(dst + (2 * c + 1) * 512 + lane * 16, ks + 8 * D + 64 * c);
-                }
+            for (int c = 0; c < KC; ++c) {
+                kr[c][0] = ldg_stream(k_lane + at + 64 * c);
+                kr[c][1] = ldg_stream(k_lane + at + 8 * D + 64 * c);
+            }
+        };
+        auto load_v = [&](int64_t at) {
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {  // positions 2t, 2t + 1, 2t + 8, 2t + 9
-                    const uint8_t *src = vs + ((i & 1) + (i >> 1) * 8) * D;
-                    if constexpr (VB == 8) {
-                        cp_async8(dst + 16 * D + i * 256 + lane * 8, src);
-                    } else {
+            for (int i = 0; i < 4; ++i) {
+                const uint8_t *src = v_lane + at + ((i & 1) + (i >> 1) * 8) * D;
+                if constexpr (VB == 8) {
+                    const uint2 x = ldg_stream8(src);
+                    vr[i][0] = x.x;
+                    vr[i][1] = x.y;
+                } else {
 #pragma unroll
-                        for (int c = 0; c < VB / 16; ++c)
-                            cp_async16(dst + 16 * D + (i * (VB / 16) + c) * 512 + lane * 16, src + 16 * c);
+                    for (int c = 0; c < VB / 16; ++c) {
+                        const uint4 x = ldg_stream(src + 16 * c);
+                        vr[i][4 * c] = x.x;
+                        vr[i][4 * c + 1] = x.y;
+                        vr[i][4 * c + 2] = x.z;
+                        vr[i][4 * c + 3] = x.w;
                     }
                 }
-                if (lane == 0)
-                    cp_async4(dst + SM::TILE, p.c.k_scale + ph);
-                if (lane == 1)
-                    cp_async4(dst + SM::TILE + 4, p.c.v_scale + ph);
             }
-            if (lane == 2)
-                *reinterpret_cast<int *>(ring + stage * (SM::TILE + SM::META) + SM::TILE + 8) = pg;
-            cp_async_commit();
         };
 
-        // --- fill the ring, then the query rows while it is on its way
-        int pg_next;
-        {
-            int pg[S];
-#pragma unroll
-            for (int i = 0; i < S; ++i)
-                pg[i] = page_of(j0 + i);
-            pg_next = page_of(j0 + S);
-#pragma unroll
-            for (int i = 0; i < S; ++i)
-                issue(j0 + i, i, pg[i]);
+        int pages = page_of(lane), pages_next = -1;
+        if (n > 0) {
+            const int64_t at = offset_of(0, __shfl_sync(~0u, pages, 0));
+            load_k(at);
+            load_v(at);
         }
+        float sks = scale_of(p.c.k_scale, pages), svs = scale_of(p.c.v_scale, pages);
+        float sks_next = 0.f, svs_next = 0.f;
+        // --- the query rows while the first tile is on its way
         uint32_t qf[NT][KC][8];
         float factor[NT][2];  // of the lane's columns 2t, 2t + 1: scale * log2 e / 2^sigma
         int limit[NT][2];     // positions below this are seen
@@ -388,126 +384,124 @@ __global__ void __launch_bounds__(32 * W, CPS) kv8_attention_kernel(const AttnPa
                 o[nt][j][0] = o[nt][j][1] = o[nt][j][2] = o[nt][j][3] = 0.f;
         }
 
-        int stage = 0;
-        for (int j = j0; j < j1; ++j) {
-            cp_async_wait<S - 1>();
-            __syncwarp();
-            const uint32_t src = ring_s + stage * (SM::TILE + SM::META);
-            const uint4 meta = lds128(src + SM::TILE);
-            if ((int)meta.z >= 0) {
-                const float sk = __uint_as_float(meta.x), sv = __uint_as_float(meta.y);
-                float s[NT][4];
+        float lsvs = fmaxf(__log2f(svs), -64.f);
+        for (int i = 0; i < n; ++i) {
+            const int at32 = i & 31;
+            if (at32 == 0)
+                pages_next = page_of(i + 32 + lane);
+            if (at32 == 16) {
+                sks_next = scale_of(p.c.k_scale, pages_next);
+                svs_next = scale_of(p.c.v_scale, pages_next);
+            }
+            const bool hole = __shfl_sync(~0u, pages, at32) < 0;
+            const float sk = __shfl_sync(~0u, sks, at32), sv = __shfl_sync(~0u, svs, at32);
+            const float lsv = __shfl_sync(~0u, lsvs, at32);
+            const int64_t next = offset_of(i + 1, __shfl_sync(~0u, at32 == 31 ? pages_next : pages, (i + 1) & 31));
+
+            // S^T, in two chains of MMAs where one would be long
+            constexpr int CH = NT == 1 && KC > 1 ? 2 : 1;
+            float s[CH][NT][4];
+#pragma unroll
+            for (int ch = 0; ch < CH; ++ch)
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
-                    s[nt][0] = s[nt][1] = s[nt][2] = s[nt][3] = 0.f;
+                    s[ch][nt][0] = s[ch][nt][1] = s[ch][nt][2] = s[ch][nt][3] = 0.f;
+#pragma unroll
+            for (int w = 0; w < 4; ++w)
 #pragma unroll
                 for (int c = 0; c < KC; ++c) {
-                    const uint4 ka = lds128(src + (2 * c) * 512 + lane * 16);
-                    const uint4 kb = lds128(src + (2 * c + 1) * 512 + lane * 16);
+                    uint32_t a0, a1, a2, a3;
+                    codes_to_f16<FP8>((&kr[c][0].x)[w], a0, a2);
+                    codes_to_f16<FP8>((&kr[c][1].x)[w], a1, a3);
 #pragma unroll
-                    for (int w = 0; w < 4; ++w) {
-                        uint32_t a0, a1, a2, a3;
-                        codes_to_f16<FP8>((&ka.x)[w], a0, a2);
-                        codes_to_f16<FP8>((&kb.x)[w], a1, a3);
-#pragma unroll
-                        for (int nt = 0; nt < NT; ++nt)
-                            mma_f16(s[nt], a0, a1, a2, a3, qf[nt][c][2 * w], qf[nt][c][2 * w + 1]);
-                    }
+                    for (int nt = 0; nt < NT; ++nt)
+                        mma_f16(s[c % CH][nt], a0, a1, a2, a3, qf[nt][c][2 * w], qf[nt][c][2 * w + 1]);
                 }
-                const int pos = (sp.first + j * W + warp) << 4;
-                const bool edge = pos + 16 > lim_min || pos < lo_max;
-                const float lsv = fmaxf(__log2f(sv), -64.f);
-                bool grow = false;
+            if (i + 1 < n)
+                load_k(next);
+            const int pos = (tile0 + i * W) << 4;
+            const bool edge = pos + 16 > lim_min || pos < lo_max || hole;
+            bool grow = false;
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    float x = s[0][nt][e];
+                    if constexpr (CH == 2)
+                        x += s[CH - 1][nt][e];
+                    x *= factor[nt][e & 1] * sk;
+                    if (edge) {
+                        const int at = pos + g + 8 * (e >> 1), lim = limit[nt][e & 1];
+                        if (at >= lim || (p.window > 0 && at < lim - p.window) || hole)
+                            x = -INFINITY;
+                    }
+                    s[0][nt][e] = x;
+                    grow |= x + lsv > m[nt][e & 1] + SLACK;
+                }
+            if (__any_sync(~0u, grow)) {
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        float x = s[nt][e] * (factor[nt][e & 1] * sk);
-                        if (edge) {
-                            const int at = pos + g + 8 * (e >> 1), lim = limit[nt][e & 1];
-                            if (at >= lim || (p.window > 0 && at < lim - p.window))
-                                x = -INFINITY;
+                    for (int e = 0; e < 2; ++e) {
+                        float x = fmaxf(s[0][nt][e], s[0][nt][e + 2]) + lsv;
+                        x = fmaxf(x, __shfl_xor_sync(~0u, x, 4));
+                        x = fmaxf(x, __shfl_xor_sync(~0u, x, 8));
+                        x = fmaxf(x, __shfl_xor_sync(~0u, x, 16));
+                        x = fmaxf(x, m[nt][e]);
+                        const float a = ex2(m[nt][e] - x);
+                        m[nt][e] = x;
+                        l[nt][e] *= a;
+#pragma unroll
+                        for (int k = 0; k < NM; ++k) {
+                            o[nt][k][e] *= a;
+                            o[nt][k][e + 2] *= a;
                         }
-                        s[nt][e] = x;
-                        grow |= x + lsv > m[nt][e & 1] + SLACK;
-                    }
-                if (__any_sync(~0u, grow)) {
-#pragma unroll
-                    for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                        for (int e = 0; e < 2; ++e) {
-                            float x = fmaxf(s[nt][e], s[nt][e + 2]) + lsv;
-                            x = fmaxf(x, __shfl_xor_sync(~0u, x, 4));
-                            x = fmaxf(x, __shfl_xor_sync(~0u, x, 8));
-                            x = fmaxf(x, __shfl_xor_sync(~0u, x, 16));
-                            x = fmaxf(x, m[nt][e]);
-                            const float a = ex2(m[nt][e] - x);
-                            m[nt][e] = x;
-                            l[nt][e] *= a;
-#pragma unroll
-                            for (int i = 0; i < NM; ++i) {
-                                o[nt][i][e] *= a;
-                                o[nt][i][e + 2] *= a;
-                            }
-                        }
-                }
-                uint32_t pf[NT][2];
-                const float svp = sv * P_SCALE;
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt) {
-                    float x[4];
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const float w = ex2(s[nt][e] - m[nt][e & 1]);
-                        l[nt][e & 1] += w;
-                        x[e] = w * svp;
-                    }
-                    pf[nt][0] = transpose8x8(f16x2(x[0], x[1]));
-                    pf[nt][1] = transpose8x8(f16x2(x[2], x[3]));
-                }
-                constexpr int VW = VB / 4;  // 32-bit words of a position's bytes
-                uint32_t v[4][VW];
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    if constexpr (VB == 8) {
-                        asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];"
-                                     : "=r"(v[i][0]), "=r"(v[i][1])
-                                     : "r"(src + 16 * D + i * 256 + lane * 8));
-                    } else {
-#pragma unroll
-                        for (int c = 0; c < VB / 16; ++c) {
-                            const uint4 x = lds128(src + 16 * D + (i * (VB / 16) + c) * 512 + lane * 16);
-                            v[i][4 * c] = x.x;
-                            v[i][4 * c + 1] = x.y;
-                            v[i][4 * c + 2] = x.z;
-                            v[i][4 * c + 3] = x.w;
-                        }
-                    }
-                    // beyond the sequence's end a page may hold anything, e4m3's NaN too
-                    if (FP8 && edge && pos + 2 * t + (i & 1) + 8 * (i >> 1) >= sp.len)
-#pragma unroll
-                        for (int w = 0; w < VW; ++w)
-                            v[i][w] = 0;
-                }
-#pragma unroll
-                for (int w = 0; w < VW; ++w)
-#pragma unroll
-                    for (int half = 0; half < 2; ++half) {  // dims 4w + 2 half, + 1: MMA 2w + half
-                        uint32_t a0, a1, a2, a3;
-                        const uint32_t sel = half ? 0x7362u : 0x5140u;
-                        codes_to_f16<FP8>(prmt(v[0][w], v[1][w], sel), a0, a1);
-                        codes_to_f16<FP8>(prmt(v[2][w], v[3][w], sel), a2, a3);
-#pragma unroll
-                        for (int nt = 0; nt < NT; ++nt)
-                            mma_f16(o[nt][2 * w + half], a0, a1, a2, a3, pf[nt][0], pf[nt][1]);
                     }
             }
-            __syncwarp();
-            issue(j + S, stage, pg_next);
-            pg_next = page_of(j + S + 1);
-            stage = stage + 1 == S ? 0 : stage + 1;
+            uint32_t pf[NT][2];
+            const float svp = sv * P_SCALE;
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+                float x[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const float w = ex2(s[0][nt][e] - m[nt][e & 1]);
+                    l[nt][e & 1] += w;
+                    x[e] = w * svp;
+                }
+                pf[nt][0] = transpose8x8(f16x2(x[0], x[1]));
+                pf[nt][1] = transpose8x8(f16x2(x[2], x[3]));
+            }
+            // beyond the sequence's end a page may hold anything, e4m3's NaN too
+            if (FP8 && edge) {
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    if (hole || pos + 2 * t + (k & 1) + 8 * (k >> 1) >= sp.len)
+#pragma unroll
+                        for (int w = 0; w < VW; ++w)
+                            vr[k][w] = 0;
+            }
+#pragma unroll
+            for (int w = 0; w < VW; ++w)
+#pragma unroll
+                for (int half = 0; half < 2; ++half) {  // dims 4w + 2 half, + 1: MMA 2w + half
+                    uint32_t a0, a1, a2, a3;
+                    const uint32_t sel = half ? 0x7362u : 0x5140u;
+                    codes_to_f16<FP8>(prmt(vr[0][w], vr[1][w], sel), a0, a1);
+                    codes_to_f16<FP8>(prmt(vr[2][w], vr[3][w], sel), a2, a3);
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt)
+                        mma_f16(o[nt][2 * w + half], a0, a1, a2, a3, pf[nt][0], pf[nt][1]);
+                }
+            if (i + 1 < n)
+                load_v(next);
+            if (at32 == 31) {
+                pages = pages_next;
+                sks = sks_next;
+                svs = svs_next;
+                lsvs = fmaxf(__log2f(svs), -64.f);
+            }
         }
-        cp_async_wait<0>();
 
         // --- join the warps' sums
 #pragma unroll
@@ -520,7 +514,6 @@ __global__ void __launch_bounds__(32 * W, CPS) kv8_attention_kernel(const AttnPa
                 x += __shfl_xor_sync(~0u, x, 16);
                 l[nt][e] = x;
             }
-        __syncthreads();  // every warp is done with its ring
         if (g == 0)
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
@@ -676,17 +669,17 @@ __global__ void __launch_bounds__(32 * W, CPS) kv8_attention_kernel(const AttnPa
                 }
             }
         }
-        __syncthreads();  // the rings are free again
+        __syncthreads();  // the sums are read
     }
 }
 
 // The variant of a call: D, the query rows of a tile and its CTAs per SM.
-template <int D, int NT, bool FP8, int W, int S, int CPS>
+template <int D, int NT, bool FP8, int W, int CPS>
 cudaError_t launch_variant(AttnParams &p, int sm_count, cudaStream_t stream)
 {
-    using SM = Smem<D, NT, W, S>;
+    using SM = Smem<D, NT, W>;
     static std::atomic<unsigned long long> done{0};
-    auto fn = kv8_attention_kernel<D, NT, FP8, W, S, CPS>;
+    auto fn = kv8_attention_kernel<D, NT, FP8, W, CPS>;
     cudaError_t e = smem_opt_in_once(done, fn, (int)SM::bytes(MAX_SEQS));
     if (e != cudaSuccess)
         return e;
@@ -697,7 +690,7 @@ cudaError_t launch_variant(AttnParams &p, int sm_count, cudaStream_t stream)
     return launch_pdl(fn, dim3((unsigned)grid), dim3(32 * W), SM::bytes(p.c.seqs), stream, p);
 }
 
-constexpr int MAX_CPS = 4;  // CTAs per SM of any variant: sizes the workspace
+constexpr int MAX_CPS = 6;  // CTAs per SM of any variant: sizes the workspace
 
 int tile_rows(int rows, int D) { return rows <= 8 || D == 256 ? 8 : 16; }
 
@@ -733,20 +726,20 @@ cudaError_t launch_kv8_attention(const Kv8 &c, const void *q, int64_t q_stride, 
     p.unit_count = static_cast<unsigned *>(workspace);
     p.join_count = p.unit_count + (size_t)sm_count * MAX_CPS;
     p.part = reinterpret_cast<float *>(static_cast<char *>(workspace) + counter_bytes(sm_count));
-#define W4Q_ATTN(D, NT, S, CPS)                                                          \
-    return c.fp8 ? launch_variant<D, NT, true, 4, S, CPS>(p, sm_count, stream)           \
-                 : launch_variant<D, NT, false, 4, S, CPS>(p, sm_count, stream)
+#define W4Q_ATTN(D, NT, CPS)                                                          \
+    return c.fp8 ? launch_variant<D, NT, true, 4, CPS>(p, sm_count, stream)           \
+                 : launch_variant<D, NT, false, 4, CPS>(p, sm_count, stream)
     if (c.head_dim == 64) {
         if (tr == 8)
-            W4Q_ATTN(64, 1, 5, 4);
-        W4Q_ATTN(64, 2, 5, 4);
+            W4Q_ATTN(64, 1, 6);
+        W4Q_ATTN(64, 2, 4);
     }
     if (c.head_dim == 128) {
         if (tr == 8)
-            W4Q_ATTN(128, 1, 3, 4);
-        W4Q_ATTN(128, 2, 4, 3);
+            W4Q_ATTN(128, 1, 4);
+        W4Q_ATTN(128, 2, 3);
     }
-    W4Q_ATTN(256, 1, 2, 3);
+    W4Q_ATTN(256, 1, 2);
 #undef W4Q_ATTN
 }
 
