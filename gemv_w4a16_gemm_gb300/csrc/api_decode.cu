@@ -64,9 +64,7 @@ int check_cache(const w4q_kv8_cache *c, w4q::Kv8 *out)
         ++log2;
     if (log2 == 8)
         return W4Q_ERR_UNSUPPORTED;
-    // positions are 32-bit, and so is the count of 64-position pieces of all sequences
-    if (((int64_t)c->width << log2) >= 0x7fffffffLL - 127 ||
-        (((int64_t)c->width << log2) / 64 + 1) * c->seqs >= 0x7fffffffLL)
+    if (((int64_t)c->width << log2) >= 0x7fffffffLL - 127)  // positions are 32-bit
         return W4Q_ERR_UNSUPPORTED;
     if (!aligned16(c->k) || !aligned16(c->v) || !aligned16(c->k_scale) || !aligned16(c->v_scale) ||
         !aligned16(c->block_table) || !aligned16(c->seq_lens))
@@ -188,6 +186,10 @@ int kv8_attention(const w4q_kv8_cache *cache, const void *q, int64_t q_stride, v
     if (q == nullptr || out == nullptr || queries <= 0 || heads <= 0 || window < 0 || !(scale == scale))
         return W4Q_ERR_INVALID_ARG;
     if (heads % c.kv_heads != 0 || queries > MAX_ROWS || (int64_t)queries * (heads / c.kv_heads) > MAX_ROWS)
+        return W4Q_ERR_UNSUPPORTED;
+    // the pieces of 64 positions of all (sequence, kv head, 8 query rows) are counted in 32 bits
+    const int64_t tiles = ((int64_t)queries * (heads / c.kv_heads) + 7) / 8;
+    if ((((int64_t)c.width << c.page_log2) / 64 + 2) * c.seqs * c.kv_heads * tiles >= 0x7fffffffLL)
         return W4Q_ERR_UNSUPPORTED;
     st = check_stride(q_stride, heads, c.head_dim);
     if (st != W4Q_OK)

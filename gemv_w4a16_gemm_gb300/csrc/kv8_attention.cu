@@ -35,14 +35,16 @@
 // cp.async in shared memory took 466 instructions a tile instead of 3xx and half
 // as long again: 434 us instead of xxx for 64 x 16000 x 8 heads.)
 //
-// Work.  One chunk = 16 W positions (a 16-position tile for each of the W
-// warps) of one (sequence, kv head, row tile).  All chunks of a call lie in one
-// line, which is cut into P equal ranges, one per resident CTA, whatever the
-// sequences' lengths are; each CTA finds its range from the lengths on the
-// device.  A unit (sequence, kv head, row tile) that is cut leaves partial sums
-// in the workspace, joined by the last CTA of every 16 to arrive and then by
-// the last of those, in a fixed order: results do not depend on the order of
-// arrival.
+// Work.  One chunk = 64 positions (a 16-position tile for each of 4 warps) of
+// one (sequence, kv head, row tile), its unit.  All chunks of a call lie in one
+// line, which is cut into equal ranges, one per CTA (one CTA per SM), whatever
+// the sequences' lengths are; each CTA finds its range from the lengths on the
+// device, and cuts it again among its G groups of 4 warps.  A cut does not fall
+// into a unit of at most SNAP chunks.  A unit that groups of one CTA share is
+// joined in shared memory; one that CTAs share leaves partial sums in the
+// workspace, joined by the last CTA to arrive (for many parts, first among
+// every JOIN neighbours), in the order of the line: results do not depend on
+// the order of arrival.
 #include <cuda_fp16.h>
 
 #include <atomic>
@@ -58,7 +60,10 @@ namespace {
 constexpr float NEG = -1e30f;      // the reference before any position was seen
 constexpr float SLACK = 8.f;       // the reference may lag this far (log2) behind the largest term
 constexpr float P_SCALE = 128.f;   // 2^7: P <= 2^8 becomes at most 2^15 in f16
-constexpr int JOIN = 16;           // partial sums joined by one CTA
+constexpr int W = 4;               // warps of a group
+constexpr int SNAP = 16;           // units up to this many chunks stay in one CTA
+constexpr int JOIN = 16;           // neighbours whose partial sums are joined first ...
+constexpr int JOIN_ONCE = 48;      // ... where a unit has more parts than this
 constexpr int MAX_SEQS = 4096;
 
 struct AttnParams {
@@ -138,50 +143,60 @@ __device__ __forceinline__ void codes_to_f16(uint32_t w, uint32_t &lo, uint32_t 
     }
 }
 
-// The chunks of a sequence: its first 16-position tile that some query sees
-// and the number of chunks of W tiles from there, at least one.
+// The chunks of a sequence of that length: its first 16-position tile that
+// some query sees and the number of chunks from there, at least one.
 struct Span {
-    int len, first, chunks;
+    int first, chunks;
 };
-template <int W>
-__device__ __forceinline__ Span span_of(const AttnParams &p, int b)
+__device__ __forceinline__ Span span_of(const AttnParams &p, int len)
 {
     Span s;
-    const long long cap = (long long)p.c.width << p.c.page_log2;
-    const long long len = p.c.lens[b];
-    s.len = (int)(len < 0 ? 0 : (len > cap ? cap : len));
-    const int lo = p.window > 0 ? s.len - p.queries - p.window + 1 : 0;
+    const int lo = p.window > 0 ? len - p.queries - p.window + 1 : 0;
     s.first = lo > 0 ? lo >> 4 : 0;
-    const int tiles = ((s.len + 15) >> 4) - s.first;
+    const int tiles = ((len + 15) >> 4) - s.first;
     s.chunks = tiles > 0 ? (tiles + W - 1) / W : 1;
     return s;
 }
 
-// Dynamic shared memory of a CTA: the warps' sums, then the chunks' prefix
-// sums over the sequences.
-template <int D, int NT, int W>
+// Dynamic shared memory of a CTA: the warps' sums, the groups' sums of the two
+// units that a group's range can cut (0: the one that it continues, 1: the one
+// that it begins), then the sequences' lengths and their chunks' prefix sums.
+template <int D, int NT, int G>
 struct Smem {
     static constexpr int ROWS = 8 * NT;
     static constexpr int PITCH = D + 4;           // rows 2t, 2t + 1 of a half-warp fall into other banks
-    static constexpr int BASE = ((W * ROWS * PITCH + 2 * W * ROWS) * 4 + 15) / 16 * 16;
-    static size_t bytes(int seqs) { return BASE + (size_t)(seqs + 1) * 4; }
+    static constexpr int PART = ROWS * (D + 2);   // a part: O [ROWS][D], m [ROWS], l [ROWS]
+    static constexpr int GROUP = W * ROWS * PITCH + 2 * W * ROWS + 2 * PART;
+    static constexpr int BASE = (G * GROUP * 4 + 15) / 16 * 16;
+    static size_t bytes(int seqs) { return BASE + (size_t)(2 * seqs + 1) * 4; }
 };
 
-template <int D, int NT, bool FP8, int W, int CPS>
-__global__ void __launch_bounds__(32 * W, CPS) kv8_attention_kernel(const AttnParams p)
+// A unit of the line.
+struct Unit {
+    int begin, end;  // its chunks in the line; begin < 0: none
+    int b, hr;
+};
+
+template <int D, int NT, bool FP8, int G>
+__global__ void __launch_bounds__(32 * W * G, 1) kv8_attention_kernel(const AttnParams p)
 {
-    using SM = Smem<D, NT, W>;
-    constexpr int ROWS = SM::ROWS, THREADS = 32 * W, KC = D / 64, VB = D / 8, VW = VB / 4, NM = D / 16;
+    using SM = Smem<D, NT, G>;
+    constexpr int ROWS = SM::ROWS, THREADS = 32 * W * G, KC = D / 64, VB = D / 8, VW = VB / 4, NM = D / 16;
     extern __shared__ __align__(16) uint8_t smem[];
     __shared__ unsigned s_last;
-    __shared__ int s_warp[W];
-    float *s_o = reinterpret_cast<float *>(smem);             // [W][ROWS][PITCH]
-    float *s_m = s_o + W * ROWS * SM::PITCH;                  // [W][ROWS]
-    float *s_l = s_m + W * ROWS;                              // [W][ROWS]
-    int *s_prefix = reinterpret_cast<int *>(smem + SM::BASE); // [seqs + 1] chunks before a sequence
+    __shared__ int s_warp[W * G];
+    __shared__ Unit s_cut[2 * G];
+    int *s_len = reinterpret_cast<int *>(smem + SM::BASE);  // [seqs]
+    int *s_prefix = s_len + p.c.seqs;                       // [seqs + 1] chunks before a sequence
 
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int tid = threadIdx.x, lane = tid & 31, grp = tid / (32 * W), warp = (tid >> 5) % W;
     const int g = lane >> 2, t = lane & 3;
+    float *s_o = reinterpret_cast<float *>(smem) + grp * SM::GROUP;  // [W][ROWS][PITCH]
+    float *s_m = s_o + W * ROWS * SM::PITCH;                         // [W][ROWS]
+    float *s_l = s_m + W * ROWS;                                     // [W][ROWS]
+    auto part_of = [&](int cut) {  // group cut / 2's part cut % 2
+        return reinterpret_cast<float *>(smem) + (cut >> 1) * SM::GROUP + (SM::GROUP - 2 * SM::PART) + (cut & 1) * SM::PART;
+    };
 
     pdl_wait();
     pdl_launch_dependents();
@@ -191,7 +206,12 @@ __global__ void __launch_bounds__(32 * W, CPS) kv8_attention_kernel(const AttnPa
         int base = 0;
         for (int b0 = 0; b0 < p.c.seqs; b0 += THREADS) {
             const int b = b0 + tid;
-            const int n = b < p.c.seqs ? span_of<W>(p, b).chunks : 0;
+            int n = 0;
+            if (b < p.c.seqs) {
+                const int len = min(max(p.c.lens[b], 0), p.c.width << p.c.page_log2);
+                s_len[b] = len;
+                n = span_of(p, len).chunks;
+            }
             int x = n;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
@@ -200,12 +220,12 @@ __global__ void __launch_bounds__(32 * W, CPS) kv8_attention_kernel(const AttnPa
                     x += y;
             }
             if (lane == 31)
-                s_warp[warp] = x;
+                s_warp[tid >> 5] = x;
             __syncthreads();
             int before = base, all = base;
 #pragma unroll
-            for (int w = 0; w < W; ++w) {
-                if (w < warp)
+            for (int w = 0; w < W * G; ++w) {
+                if (w < (tid >> 5))
                     before += s_warp[w];
                 all += s_warp[w];
             }
@@ -216,41 +236,80 @@ __global__ void __launch_bounds__(32 * W, CPS) kv8_attention_kernel(const AttnPa
         }
         if (tid == 0)
             s_prefix[p.c.seqs] = base;
+        if (tid < 2 * G)
+            s_cut[tid].begin = -1;
         __syncthreads();
     }
     const int HR = p.c.kv_heads * p.row_tiles;
-    const long long U = (long long)s_prefix[p.c.seqs] * HR;
-    const long long P = U < (long long)gridDim.x ? U : (long long)gridDim.x;
-    const long long cta = blockIdx.x;
+    const int U = s_prefix[p.c.seqs] * HR, P = min(U, (int)gridDim.x), cta = blockIdx.x;
     if (cta >= P)
         return;
-    const long long begin = U * cta / P, end = U * (cta + 1) / P;
 
-    int b = 0;
-    {
-        int hi = p.c.seqs;  // the last b with prefix[b] * HR <= begin
-        while (hi - b > 1) {
-            const int mid = (b + hi) >> 1;
-            if ((long long)s_prefix[mid] * HR <= begin)
-                b = mid;
+    auto sequence_at = [&](int u) -> int {  // the last b with prefix[b] * HR <= u
+        int lo = 0, hi = p.c.seqs;
+        while (hi - lo > 1) {
+            const int mid = (lo + hi) >> 1;
+            if (s_prefix[mid] * HR <= u)
+                lo = mid;
             else
                 hi = mid;
         }
-    }
+        return lo;
+    };
+    auto snapped = [&](int u) -> int {  // a cut at u, out of a short unit
+        if (u >= U)
+            return U;
+        const int b = sequence_at(u), seq0 = s_prefix[b] * HR;
+        const unsigned chunks = s_prefix[b + 1] - s_prefix[b];
+        return chunks <= SNAP ? seq0 + (unsigned)(u - seq0) / chunks * chunks : u;
+    };
+    const int begin = snapped((int)((long long)U * cta / P)), end = snapped((int)((long long)U * (cta + 1) / P));
+    if (begin >= end)
+        return;
+    const int from = begin + (int)((long long)(end - begin) * grp / G);
+    const int to = begin + (int)((long long)(end - begin) * (grp + 1) / G);
 
-    for (long long u = begin; u < end;) {
-        while ((long long)s_prefix[b + 1] * HR <= u)
+    // row r of a unit, permuted index at (see where the sums are stored), of the joined sums
+    auto finish = [&](const Unit &x, int r, int at, float2 v, float mm, float ll) {
+        const int h = x.hr / p.row_tiles, rr = (x.hr % p.row_tiles) * ROWS + r;
+        if (rr >= p.rows)
+            return;
+        const int qi = rr / p.group, head = h * p.group + rr % p.group;
+        const int d = VB * ((at & 15) >> 1) + 2 * (at >> 4);
+        const float inv = ll > 0.f ? 1.f / ll * (1.f / P_SCALE) : 0.f;
+        const int64_t row = ((int64_t)x.b * p.queries + qi) * p.heads + head;
+        *reinterpret_cast<__nv_bfloat162 *>(p.out + row * D + d) = __floats2bfloat162_rn(v.x * inv, v.y * inv);
+        if (at == 0 && p.lse != nullptr)
+            p.lse[row] = ll > 0.f ? (mm + log2f(ll)) * 0.6931471805599453f : -INFINITY;
+    };
+
+    int b = from < to ? sequence_at(from) : 0;
+    for (int u = from; u < to;) {
+        while (s_prefix[b + 1] * HR <= u)
             ++b;
-        const Span sp = span_of<W>(p, b);
-        const long long seq0 = (long long)s_prefix[b] * HR;
-        const int hr = (int)((u - seq0) / sp.chunks);
-        const long long unit0 = seq0 + (long long)hr * sp.chunks, unit1 = unit0 + sp.chunks;
-        const int j0 = (int)(u - unit0);
-        const int j1 = (int)((end < unit1 ? end : unit1) - unit0);
-        const int h = hr / p.row_tiles, row0 = (hr % p.row_tiles) * ROWS;
-        u = unit0 + j1;
+        const int len = s_len[b], seq0 = s_prefix[b] * HR;
+        const Span sp = span_of(p, len);
+        const int hr = (int)((unsigned)(u - seq0) / (unsigned)sp.chunks);
+        const Unit unit = {seq0 + hr * sp.chunks, seq0 + (hr + 1) * sp.chunks, b, hr};
+        const int j0 = u - unit.begin, j1 = min(to, unit.end) - unit.begin;
+        const int h = (int)((unsigned)hr / (unsigned)p.row_tiles), row0 = (hr - h * p.row_tiles) * ROWS;
+        u = unit.begin + j1;
 
-        const int tiles_end = (sp.len + 15) >> 4;
+        // --- the query rows' loads: rows beyond the last are its copies, and are dropped at the end
+        uint4 raw[NT][KC][2];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+            const unsigned r = min(row0 + nt * 8 + g, p.rows - 1), qi = r / (unsigned)p.group;
+            const __nv_bfloat16 *src = p.q + ((int64_t)b * p.queries + qi) * p.q_stride +
+                                       (int64_t)(h * p.group + (r - qi * p.group)) * D + 16 * t;
+#pragma unroll
+            for (int c = 0; c < KC; ++c) {
+                raw[nt][c][0] = __ldg(reinterpret_cast<const uint4 *>(src + 64 * c));
+                raw[nt][c][1] = __ldg(reinterpret_cast<const uint4 *>(src + 64 * c) + 1);
+            }
+        }
+
+        const int tiles_end = (len + 15) >> 4;
         const int per_page = p.c.page_log2 - 4;
         const int32_t *table = p.c.table + (int64_t)b * p.c.width;
         const int64_t page_bytes = (int64_t)D << p.c.page_log2;
@@ -320,27 +379,12 @@ __global__ void __launch_bounds__(32 * W, CPS) kv8_attention_kernel(const AttnPa
         int lim_min = 0x7fffffff;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
-            const int r = row0 + nt * 8 + g;
             float top = 0.f;
-            uint4 raw[KC][2];
-            if (r < p.rows) {
-                const int qi = r / p.group, head = h * p.group + r % p.group;
-                const __nv_bfloat16 *src = p.q + ((int64_t)b * p.queries + qi) * p.q_stride + (int64_t)head * D + 16 * t;
-#pragma unroll
-                for (int c = 0; c < KC; ++c) {
-                    raw[c][0] = __ldg(reinterpret_cast<const uint4 *>(src + 64 * c));
-                    raw[c][1] = __ldg(reinterpret_cast<const uint4 *>(src + 64 * c) + 1);
-                }
-            } else {
-#pragma unroll
-                for (int c = 0; c < KC; ++c)
-                    raw[c][0] = raw[c][1] = make_uint4(0, 0, 0, 0);
-            }
 #pragma unroll
             for (int c = 0; c < KC; ++c)
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
-                    const uint32_t w = (&raw[c][i >> 2].x)[i & 3];
+                    const uint32_t w = (&raw[nt][c][i >> 2].x)[i & 3];
                     top = fmaxf(top, fmaxf(fabsf(bf16lo_to_f32(w)), fabsf(bf16hi_to_f32(w))));
                 }
             top = fmaxf(top, __shfl_xor_sync(~0u, top, 1));
@@ -355,7 +399,7 @@ __global__ void __launch_bounds__(32 * W, CPS) kv8_attention_kernel(const AttnPa
             for (int c = 0; c < KC; ++c)
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
-                    const uint32_t w = (&raw[c][i >> 2].x)[i & 3];
+                    const uint32_t w = (&raw[nt][c][i >> 2].x)[i & 3];
                     qf[nt][c][i] = f16x2(bf16lo_to_f32(w) * u1 * u2, bf16hi_to_f32(w) * u1 * u2);
                 }
 #pragma unroll
@@ -364,15 +408,14 @@ __global__ void __launch_bounds__(32 * W, CPS) kv8_attention_kernel(const AttnPa
                 const int upc = __shfl_sync(~0u, up, (2 * t + e) * 4);
                 factor[nt][e] = p.scale_log2 * __uint_as_float((uint32_t)(127 - upc / 2) << 23) *
                                 __uint_as_float((uint32_t)(127 - (upc - upc / 2)) << 23);
-                limit[nt][e] = rr < p.rows ? sp.len - p.queries + rr / p.group + 1 : 0x7fffffff;
-                if (rr < p.rows)
-                    lim_min = min(lim_min, limit[nt][e]);
+                limit[nt][e] = len - p.queries + min(rr, p.rows - 1) / p.group + 1;
+                lim_min = min(lim_min, limit[nt][e]);
             }
         }
         lim_min = min(lim_min, __shfl_xor_sync(~0u, lim_min, 1));
         lim_min = min(lim_min, __shfl_xor_sync(~0u, lim_min, 2));
         // tiles from here on are seen from their first position by every row
-        const int lo_max = p.window > 0 ? sp.len - p.window : 0;
+        const int lo_max = p.window > 0 ? len - p.window : 0;
 
         float o[NT][NM][4], m[NT][2], l[NT][2];
 #pragma unroll
@@ -476,7 +519,7 @@ __global__ void __launch_bounds__(32 * W, CPS) kv8_attention_kernel(const AttnPa
             if (FP8 && edge) {
 #pragma unroll
                 for (int k = 0; k < 4; ++k)
-                    if (hole || pos + 2 * t + (k & 1) + 8 * (k >> 1) >= sp.len)
+                    if (hole || pos + 2 * t + (k & 1) + 8 * (k >> 1) >= len)
 #pragma unroll
                         for (int w = 0; w < VW; ++w)
                             vr[k][w] = 0;
@@ -503,7 +546,7 @@ __global__ void __launch_bounds__(32 * W, CPS) kv8_attention_kernel(const AttnPa
             }
         }
 
-        // --- join the warps' sums
+        // --- join the group's warps
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -531,29 +574,12 @@ __global__ void __launch_bounds__(32 * W, CPS) kv8_attention_kernel(const AttnPa
                 for (int i = 0; i < NM; ++i)
                     *reinterpret_cast<float2 *>(s_o + (warp * ROWS + nt * 8 + 2 * t + e) * SM::PITCH + 16 * i + 2 * g) =
                         make_float2(o[nt][i][e], o[nt][i][e + 2]);
-        __syncthreads();
-
-        const bool whole = j0 == 0 && j1 == sp.chunks;
-        const long long c0 = whole ? cta : ((unit0 + 1) * P - 1) / U, c1 = whole ? cta : (unit1 * P - 1) / U;
-        // a CTA's slot 1 holds the unit that starts in it, slot 0 the one that it continues
-        auto slot_of = [&](long long c) { return 2 * c + (c == c0 ? 1 : 0); };
-        constexpr int PART = ROWS * (D + 2);
-
-        auto finish = [&](int r, int at, float2 x, float mm, float ll) {  // row r, permuted index at
-            const int rr = row0 + r;
-            if (rr >= p.rows)
-                return;
-            const int qi = rr / p.group, head = h * p.group + rr % p.group;
-            const int d = VB * ((at & 15) >> 1) + 2 * (at >> 4);
-            const float inv = ll > 0.f ? 1.f / ll * (1.f / P_SCALE) : 0.f;
-            const int64_t row = ((int64_t)b * p.queries + qi) * p.heads + head;
-            *reinterpret_cast<__nv_bfloat162 *>(p.out + row * D + d) =
-                __floats2bfloat162_rn(x.x * inv, x.y * inv);
-            if (at == 0 && p.lse != nullptr)
-                p.lse[row] = ll > 0.f ? (mm + log2f(ll)) * 0.6931471805599453f : -INFINITY;
-        };
-
-        for (int i = tid; i < ROWS * (D / 2); i += THREADS) {
+        asm volatile("bar.sync %0, %1;" ::"r"(1 + grp), "n"(32 * W) : "memory");
+        const bool whole = j0 == 0 && u == unit.end;
+        const int cut = 2 * grp + (j0 == 0 ? 1 : 0);
+#pragma unroll
+        for (int it = 0; it < ROWS * (D / 2) / (32 * W); ++it) {
+            const int i = tid % (32 * W) + it * 32 * W;
             const int r = i / (D / 2), at = 2 * (i % (D / 2));
             float mm = NEG, ll = 0.f;
             float2 x = make_float2(0.f, 0.f);
@@ -569,9 +595,9 @@ __global__ void __launch_bounds__(32 * W, CPS) kv8_attention_kernel(const AttnPa
                 x.y += a * y.y;
             }
             if (whole) {
-                finish(r, at, x, mm, ll);
+                finish(unit, r, at, x, mm, ll);
             } else {
-                float *dst = p.part + slot_of(cta) * PART;
+                float *dst = part_of(cut);
                 *reinterpret_cast<float2 *>(dst + r * D + at) = x;
                 if (at == 0) {
                     dst[ROWS * D + r] = mm;
@@ -579,130 +605,179 @@ __global__ void __launch_bounds__(32 * W, CPS) kv8_attention_kernel(const AttnPa
                 }
             }
         }
-        if (!whole) {
-            // Two levels: the last CTA of each JOIN neighbours joins their sums into the first
-            // one's slot, the last of those joins the unit's.
-            const long long n = c1 - c0 + 1, mine = (cta - c0) / JOIN;
-            const long long f0 = c0 + mine * JOIN;
-            const int members = (int)(n - mine * JOIN < JOIN ? n - mine * JOIN : JOIN);
-            const int joins = (int)((n + JOIN - 1) / JOIN);
-            auto arrive = [&](unsigned *count, int of) -> bool {
-                __syncthreads();
-                if (tid == 0) {
-                    __threadfence();
-                    const unsigned before = atomic_add_acq_rel(count, 1u);
-                    s_last = before + 1 == (unsigned)of;
-                    if (s_last)
-                        *count = 0;  // as the next call expects it
-                    __threadfence();
+        if (!whole && tid % (32 * W) == 0)
+            s_cut[cut] = unit;
+        asm volatile("bar.sync %0, %1;" ::"r"(1 + grp), "n"(32 * W) : "memory");  // the sums are read
+    }
+
+    // --- join the units that the CTA's groups, or CTAs, share
+    __syncthreads();
+    for (int k = 0; k < 2 * G;) {
+        const Unit unit = s_cut[k];
+        if (unit.begin < 0) {
+            ++k;
+            continue;
+        }
+        const int k0 = k;  // this unit's parts in the CTA: those of its cuts k0 .. k - 1
+        while (k < 2 * G && (s_cut[k].begin < 0 || s_cut[k].begin == unit.begin))
+            ++k;
+        const bool whole = unit.begin >= begin && unit.end <= end;
+        // a CTA's slot 1 in the workspace holds the unit that begins in it, slot 0 the one that it continues
+        const int c0 = whole ? cta : (int)(((long long)(unit.begin + 1) * P - 1) / U);
+        const int c1 = whole ? cta : (int)(((long long)unit.end * P - 1) / U);
+        auto slot_of = [&](int c) { return p.part + (int64_t)(2 * c + (c == c0 ? 1 : 0)) * SM::PART; };
+        for (int i = tid; i < ROWS * (D / 2); i += THREADS) {
+            const int r = i / (D / 2), at = 2 * (i % (D / 2));
+            float mm = NEG, ll = 0.f;
+            float2 x = make_float2(0.f, 0.f);
+            for (int q = k0; q < k; ++q)
+                if (s_cut[q].begin >= 0)
+                    mm = fmaxf(mm, part_of(q)[ROWS * D + r]);
+            for (int q = k0; q < k; ++q)
+                if (s_cut[q].begin >= 0) {
+                    const float *src = part_of(q);
+                    const float a = ex2(src[ROWS * D + r] - mm);
+                    const float2 y = *reinterpret_cast<const float2 *>(src + r * D + at);
+                    ll += a * src[ROWS * D + ROWS + r];
+                    x.x += a * y.x;
+                    x.y += a * y.y;
                 }
-                __syncthreads();
-                return s_last != 0;
-            };
-            // joins `of` slots, `step` CTAs apart from CTA f on
-            auto join = [&](long long f, int step, int of, bool last) {
-                for (int i = tid; i < ROWS * (D / 4); i += THREADS) {
-                    const int r = i / (D / 4), at = 4 * (i % (D / 4));
-                    float pm[JOIN], mm = NEG, ll = 0.f;
-                    float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-                    for (int k = 0; k < JOIN; ++k) {
-                        pm[k] = NEG;
-                        if (k < of)
-                            pm[k] = __ldcg(p.part + slot_of(f + (long long)k * step) * PART + ROWS * D + r);
-                        mm = fmaxf(mm, pm[k]);
-                    }
-#pragma unroll
-                    for (int k = 0; k < JOIN; ++k)
-                        if (k < of) {
-                            const float *src = p.part + slot_of(f + (long long)k * step) * PART;
-                            const float a = ex2(pm[k] - mm);
-                            const float4 y = __ldcg(reinterpret_cast<const float4 *>(src + r * D + at));
-                            ll += a * __ldcg(src + ROWS * D + ROWS + r);
-                            x.x += a * y.x;
-                            x.y += a * y.y;
-                            x.z += a * y.z;
-                            x.w += a * y.w;
-                        }
-                    if (last) {
-                        finish(r, at, make_float2(x.x, x.y), mm, ll);
-                        finish(r, at + 2, make_float2(x.z, x.w), mm, ll);
-                    } else {
-                        // the first slot's other readers of m and l are this row's threads: all
-                        // of a row lie in one warp's reach only if D / 4 <= 32, so they go to a
-                        // copy that is written after the barrier below
-                        float *dst = p.part + slot_of(f) * PART;
-                        *reinterpret_cast<float4 *>(dst + r * D + at) = x;
-                        if (at == 0) {
-                            s_m[r] = mm;
-                            s_l[r] = ll;
-                        }
-                    }
-                }
-                if (!last) {
-                    __syncthreads();
-                    float *dst = p.part + slot_of(f) * PART;
-                    for (int r = tid; r < ROWS; r += THREADS) {
-                        dst[ROWS * D + r] = s_m[r];
-                        dst[ROWS * D + ROWS + r] = s_l[r];
-                    }
-                }
-            };
-            unsigned *unit_count = p.unit_count + c0;
-            if (joins == 1) {
-                if (arrive(unit_count, members))
-                    join(f0, 1, members, true);
-            } else if (arrive(p.join_count + slot_of(f0), members)) {
-                join(f0, 1, members, false);
-                if (arrive(unit_count, joins)) {
-                    // more than JOIN * JOIN parts: fold the join's slots JOIN at a time
-                    int left = joins, step = JOIN;
-                    while (left > JOIN) {
-                        for (int k = 0; k < left; k += JOIN) {
-                            join(c0 + (long long)k * step, step, left - k < JOIN ? left - k : JOIN, false);
-                            __syncthreads();
-                        }
-                        left = (left + JOIN - 1) / JOIN;
-                        step *= JOIN;
-                    }
-                    join(c0, step, left, true);
+            if (whole) {
+                finish(unit, r, at, x, mm, ll);
+            } else {
+                float *dst = slot_of(cta);
+                *reinterpret_cast<float2 *>(dst + r * D + at) = x;
+                if (at == 0) {
+                    dst[ROWS * D + r] = mm;
+                    dst[ROWS * D + ROWS + r] = ll;
                 }
             }
         }
-        __syncthreads();  // the sums are read
+        if (whole)
+            continue;
+
+        auto arrive = [&](unsigned *count, int of) -> bool {
+            __syncthreads();
+            if (tid == 0) {
+                __threadfence();
+                const unsigned before = atomic_add_acq_rel(count, 1u);
+                s_last = before + 1 == (unsigned)of;
+                if (s_last)
+                    *count = 0;  // as the next call expects it
+                __threadfence();
+            }
+            __syncthreads();
+            return s_last != 0;
+        };
+        // joins `of` slots, `step` CTAs apart from CTA f on, into the first of them or the result
+        auto join = [&](int f, int step, int of, bool last) {
+            constexpr int ITEMS = (ROWS * (D / 2) + THREADS - 1) / THREADS, AT_ONCE = 16;
+            float row_m[ITEMS], row_l[ITEMS];
+#pragma unroll
+            for (int it = 0; it < ITEMS; ++it) {
+                const int i = tid + it * THREADS;
+                if (i >= ROWS * (D / 2))
+                    continue;
+                const int r = i / (D / 2), at = 2 * (i % (D / 2));
+                float mm = NEG, ll = 0.f;
+                float2 x = make_float2(0.f, 0.f);
+                for (int q0 = 0; q0 < of; q0 += AT_ONCE) {
+                    float pm[AT_ONCE], pl[AT_ONCE];
+                    float2 y[AT_ONCE];
+#pragma unroll
+                    for (int q = 0; q < AT_ONCE; ++q) {  // all loads before any use
+                        const float *src = slot_of(f + min(q0 + q, of - 1) * step);
+                        pm[q] = __ldcg(src + ROWS * D + r);
+                        pl[q] = __ldcg(src + ROWS * D + ROWS + r);
+                        y[q] = __ldcg(reinterpret_cast<const float2 *>(src + r * D + at));
+                    }
+                    float top = mm;
+#pragma unroll
+                    for (int q = 0; q < AT_ONCE; ++q)
+                        top = fmaxf(top, pm[q]);
+                    const float keep = ex2(mm - top);
+                    ll *= keep;
+                    x.x *= keep;
+                    x.y *= keep;
+                    mm = top;
+#pragma unroll
+                    for (int q = 0; q < AT_ONCE; ++q) {
+                        const float a = q0 + q < of ? ex2(pm[q] - mm) : 0.f;
+                        ll += a * pl[q];
+                        x.x += a * y[q].x;
+                        x.y += a * y[q].y;
+                    }
+                }
+                if (last)
+                    finish(unit, r, at, x, mm, ll);
+                else
+                    *reinterpret_cast<float2 *>(slot_of(f) + r * D + at) = x;
+                row_m[it] = mm;
+                row_l[it] = ll;
+            }
+            if (!last) {
+                __syncthreads();  // every thread has read the first slot's m and l
+#pragma unroll
+                for (int it = 0; it < ITEMS; ++it) {
+                    const int i = tid + it * THREADS;
+                    if (i < ROWS * (D / 2) && i % (D / 2) == 0) {
+                        slot_of(f)[ROWS * D + i / (D / 2)] = row_m[it];
+                        slot_of(f)[ROWS * D + ROWS + i / (D / 2)] = row_l[it];
+                    }
+                }
+            }
+        };
+        const int parts = c1 - c0 + 1;
+        unsigned *unit_count = p.unit_count + c0;
+        if (parts <= JOIN_ONCE) {
+            if (arrive(unit_count, parts))
+                join(c0, 1, parts, true);
+        } else {
+            const int mine0 = (cta - c0) / JOIN * JOIN;
+            const int members = min(JOIN, parts - mine0);
+            const int f = c0 + mine0;
+            if (arrive(p.join_count + 2 * f + (f == c0 ? 1 : 0), members)) {
+                join(f, 1, members, false);
+                const int joins = (parts + JOIN - 1) / JOIN;
+                if (arrive(unit_count, joins))
+                    join(c0, JOIN, joins, true);
+            }
+        }
     }
 }
 
-// The variant of a call: D, the query rows of a tile and its CTAs per SM.
-template <int D, int NT, bool FP8, int W, int CPS>
+template <int D, int NT, bool FP8, int G>
 cudaError_t launch_variant(AttnParams &p, int sm_count, cudaStream_t stream)
 {
-    using SM = Smem<D, NT, W>;
+    using SM = Smem<D, NT, G>;
     static std::atomic<unsigned long long> done{0};
-    auto fn = kv8_attention_kernel<D, NT, FP8, W, CPS>;
+    auto fn = kv8_attention_kernel<D, NT, FP8, G>;
     cudaError_t e = smem_opt_in_once(done, fn, (int)SM::bytes(MAX_SEQS));
     if (e != cudaSuccess)
         return e;
     // no more CTAs than the longest sequences that the table can hold give chunks
     const long long most = (((long long)p.c.width << p.c.page_log2) + 16 * W - 1) / (16 * W);
     const long long units = (long long)p.c.seqs * p.c.kv_heads * p.row_tiles * (most > 0 ? most : 1);
-    const long long grid = units < (long long)sm_count * CPS ? units : (long long)sm_count * CPS;
-    return launch_pdl(fn, dim3((unsigned)grid), dim3(32 * W), SM::bytes(p.c.seqs), stream, p);
+    const long long grid = units < (long long)sm_count ? units : (long long)sm_count;
+    return launch_pdl(fn, dim3((unsigned)grid), dim3(32 * W * G), SM::bytes(p.c.seqs), stream, p);
 }
 
-constexpr int MAX_CPS = 6;  // CTAs per SM of any variant: sizes the workspace
-
-int tile_rows(int rows, int D) { return rows <= 8 || D == 256 ? 8 : 16; }
+// Query rows of a tile: the accumulators (D / 4 registers per 8 rows) have to fit.
+int tile_rows(int rows, int D)
+{
+    if (rows <= 8 || D == 256)
+        return 8;
+    return rows <= 16 || D == 128 ? 16 : 32;
+}
 
 }  // namespace
 
 // Workspace: the counters, in the same place for every call on a device, then the partial sums.
-static size_t counter_bytes(int sm_count) { return ((size_t)3 * sm_count * MAX_CPS * 4 + 255) / 256 * 256; }
+static size_t counter_bytes(int sm_count) { return ((size_t)3 * sm_count * 4 + 255) / 256 * 256; }
 
 size_t kv8_attention_workspace(int queries, int group, int head_dim, int sm_count)
 {
-    return counter_bytes(sm_count) +
-           (size_t)2 * sm_count * MAX_CPS * tile_rows(queries * group, head_dim) * (head_dim + 2) * 4;
+    return counter_bytes(sm_count) + (size_t)2 * sm_count * tile_rows(queries * group, head_dim) * (head_dim + 2) * 4;
 }
 
 cudaError_t launch_kv8_attention(const Kv8 &c, const void *q, int64_t q_stride, void *out, float *lse,
@@ -724,15 +799,18 @@ cudaError_t launch_kv8_attention(const Kv8 &c, const void *q, int64_t q_stride, 
     p.window = window;
     p.scale_log2 = scale * 1.4426950408889634f;
     p.unit_count = static_cast<unsigned *>(workspace);
-    p.join_count = p.unit_count + (size_t)sm_count * MAX_CPS;
+    p.join_count = p.unit_count + sm_count;
     p.part = reinterpret_cast<float *>(static_cast<char *>(workspace) + counter_bytes(sm_count));
-#define W4Q_ATTN(D, NT, CPS)                                                          \
-    return c.fp8 ? launch_variant<D, NT, true, 4, CPS>(p, sm_count, stream)           \
-                 : launch_variant<D, NT, false, 4, CPS>(p, sm_count, stream)
+// Groups per CTA: as many as the registers allow (128 a thread with 4 groups, 96 with 5, 168 with 3, 255 with 2).
+#define W4Q_ATTN(D, NT, G)                                                        \
+    return c.fp8 ? launch_variant<D, NT, true, G>(p, sm_count, stream)           \
+                 : launch_variant<D, NT, false, G>(p, sm_count, stream)
     if (c.head_dim == 64) {
         if (tr == 8)
-            W4Q_ATTN(64, 1, 6);
-        W4Q_ATTN(64, 2, 4);
+            W4Q_ATTN(64, 1, 5);
+        if (tr == 16)
+            W4Q_ATTN(64, 2, 4);
+        W4Q_ATTN(64, 4, 3);
     }
     if (c.head_dim == 128) {
         if (tr == 8)

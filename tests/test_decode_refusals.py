@@ -54,7 +54,7 @@ def test_norm_rope(changes, status):
 @pytest.mark.parametrize("changes,status", [
     (dict(k=None), 1), (dict(seq_lens=None), 1), (dict(blocks=0), 1), (dict(seqs=0), 1), (dict(width=-1), 1), (dict(kv_heads=0), 1),
     (dict(head_dim=80), 2), (dict(page=48), 2), (dict(page=8), 2), (dict(page=256), 2), (dict(format=2), 2), (dict(seqs=5000), 2),
-    (dict(width=1 << 25), 2), (dict(blocks=1 << 31), 2), (dict(seqs=4096, width=1 << 20), 2),
+    (dict(width=1 << 25), 2), (dict(blocks=1 << 31), 2),
     (dict(v=FAKE + 8), 3), (dict(k_scale=FAKE + 4), 3), (dict(block_table=FAKE + 4), 3),
 ])
 def test_cache(changes, status):
@@ -87,6 +87,10 @@ def test_append(changes, status):
 ])
 def test_attention(changes, status):
     assert attend(**changes) == status
+
+
+def test_attention_over_too_many_positions():
+    assert attend(cache(seqs=4096, width=1 << 20)) == 2
 
 
 @pytest.mark.parametrize("args", [(0, 1, 8, 2, 128), (5000, 1, 8, 2, 128), (1, 0, 8, 2, 128), (1, 1, 7, 2, 128), (1, 65, 2, 2, 128),
