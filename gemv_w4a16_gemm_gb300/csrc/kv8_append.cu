@@ -15,11 +15,12 @@
 // and the codes rnd(y / s'); where s' > s the earlier codes become
 // rnd(code * (s / s')).  Every quotient is the correctly rounded fp32 one.
 //
-// What bounds it: each element is read and written once, a few dozen
-// instructions an element; HBM for prompts, one launch for single tokens.
-// Layout: D / 8 lanes hold a head row, 8 elements (one 16-byte load) each, so
-// the norm's sum and the rotation's partners are a few shuffles away and
-// nothing goes through shared memory.
+// What bounds it: each element is read and written once, some fifty
+// instructions for a lane's 8 of them; HBM for prompts, one launch for single
+// tokens.  Layout: D / 8 lanes hold a head row.  A lane has two groups of 4
+// elements, one from each half of the rotated part (or 8 beyond it), so both
+// partners of its pairs and their 4 angles are its own: the norm's sum is the
+// only thing that lanes exchange.
 #include <cuda_fp16.h>
 
 #include "common.cuh"
@@ -32,7 +33,6 @@ namespace {
 
 struct Row {
     const __nv_bfloat16 *weight;  // null: no norm
-    bool norm;                    // some row of the warp has a weight: all join the norm's shuffles
     const float *cos_sin;         // null: no rotation
     int64_t positions;
     int rot;
@@ -40,66 +40,84 @@ struct Row {
     float eps;
 };
 
-__device__ __forceinline__ void unpack8(uint4 raw, float (&y)[8])
-{
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        y[2 * i] = bf16lo_to_f32((&raw.x)[i]);
-        y[2 * i + 1] = bf16hi_to_f32((&raw.x)[i]);
-    }
-}
-
-__device__ __forceinline__ uint4 pack8(const float (&y)[8])
-{
-    uint4 r;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const __nv_bfloat162 h = __floats2bfloat162_rn(y[2 * i], y[2 * i + 1]);
-        (&r.x)[i] = *reinterpret_cast<const uint32_t *>(&h);
-    }
-    return r;
-}
-
-__device__ __forceinline__ void load8(const float *src, float (&y)[8])
-{
-    const float4 a = __ldg(reinterpret_cast<const float4 *>(src));
-    const float4 b = __ldg(reinterpret_cast<const float4 *>(src) + 1);
-    y[0] = a.x, y[1] = a.y, y[2] = a.z, y[3] = a.w;
-    y[4] = b.x, y[5] = b.y, y[6] = b.z, y[7] = b.w;
-}
-
-// What a lane needs of the table for its 8 elements, whatever the head.
-struct Angles {
-    float c[8], s[8];  // interleaved: 4 of each
+// A lane's elements of a row: a[0..3] from offset first on, a[4..7] from second on.
+struct Where {
+    int first, second;
 };
 
 template <int D>
-__device__ __forceinline__ void load_angles(const Row &p, int64_t pos, int sub, Angles &a)
+__device__ __forceinline__ Where elements_of(const Row &p, int sub)
 {
-    if (p.cos_sin == nullptr || 8 * sub >= p.rot)
-        return;
-    pos = pos < 0 ? 0 : (pos >= p.positions ? p.positions - 1 : pos);
-    const float *t = p.cos_sin + pos * p.rot;
-    const int half = p.rot / 2;
-    if (p.interleaved) {
-        const float4 c = __ldg(reinterpret_cast<const float4 *>(t + 4 * sub));
-        const float4 s = __ldg(reinterpret_cast<const float4 *>(t + half + 4 * sub));
-        a.c[0] = c.x, a.c[1] = c.y, a.c[2] = c.z, a.c[3] = c.w;
-        a.s[0] = s.x, a.s[1] = s.y, a.s[2] = s.z, a.s[3] = s.w;
-    } else {
-        const int i = 8 * sub < half ? 8 * sub : 8 * sub - half;
-        load8(t + i, a.c);
-        load8(t + half + i, a.s);
+    if (p.interleaved)
+        return {8 * sub, 8 * sub + 4};
+    const int turned = p.rot / 8;  // lanes of the rotated part
+    if (sub < turned)
+        return {4 * sub, p.rot / 2 + 4 * sub};
+    return {8 * sub, 8 * sub + 4};
+}
+
+struct Raw {
+    uint2 a, b;
+};
+
+__device__ __forceinline__ Raw load_raw(const __nv_bfloat16 *row, Where w)
+{
+    return {__ldg(reinterpret_cast<const uint2 *>(row + w.first)), __ldg(reinterpret_cast<const uint2 *>(row + w.second))};
+}
+
+__device__ __forceinline__ void unpack8(Raw r, float (&y)[8])
+{
+    y[0] = bf16lo_to_f32(r.a.x), y[1] = bf16hi_to_f32(r.a.x), y[2] = bf16lo_to_f32(r.a.y), y[3] = bf16hi_to_f32(r.a.y);
+    y[4] = bf16lo_to_f32(r.b.x), y[5] = bf16hi_to_f32(r.b.x), y[6] = bf16lo_to_f32(r.b.y), y[7] = bf16hi_to_f32(r.b.y);
+}
+
+__device__ __forceinline__ uint32_t bf16_pair(float lo, float hi)
+{
+    const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t *>(&h);
+}
+
+__device__ __forceinline__ void store_row(__nv_bfloat16 *row, Where w, const float (&y)[8])
+{
+    *reinterpret_cast<uint2 *>(row + w.first) = make_uint2(bf16_pair(y[0], y[1]), bf16_pair(y[2], y[3]));
+    *reinterpret_cast<uint2 *>(row + w.second) = make_uint2(bf16_pair(y[4], y[5]), bf16_pair(y[6], y[7]));
+}
+
+// What a lane needs for every row of a kind and a position: the norm's weights
+// and the angles of its pairs.
+struct Weights {
+    float w[8];
+};
+__device__ __forceinline__ Weights load_weights(const Row &p, Where at)
+{
+    Weights v = {};
+    if (p.weight != nullptr)
+        unpack8(load_raw(p.weight, at), v.w);
+    return v;
+}
+
+struct Angles {
+    float4 c, s;
+};
+__device__ __forceinline__ Angles load_angles(const Row &p, int64_t pos, int sub)
+{
+    Angles a = {};
+    if (p.cos_sin != nullptr && 8 * sub < p.rot) {
+        pos = pos < 0 ? 0 : (pos >= p.positions ? p.positions - 1 : pos);
+        const float *t = p.cos_sin + pos * p.rot + 4 * sub;
+        a.c = __ldg(reinterpret_cast<const float4 *>(t));
+        a.s = __ldg(reinterpret_cast<const float4 *>(t + p.rot / 2));
     }
+    return a;
 }
 
 // The lane's 8 elements of a head row, normed and rotated.  All lanes of the
 // warp call it together.
 template <int D>
-__device__ __forceinline__ void turn(const Row &p, const Angles &a, int sub, float (&y)[8])
+__device__ __forceinline__ void turn(const Row &p, const Weights &w, const Angles &a, int sub, float (&y)[8])
 {
     constexpr int LANES = D / 8;
-    if (p.norm) {
+    if (p.weight != nullptr) {
         float ss = 0.f;
 #pragma unroll
         for (int i = 0; i < 8; ++i)
@@ -107,53 +125,51 @@ __device__ __forceinline__ void turn(const Row &p, const Angles &a, int sub, flo
 #pragma unroll
         for (int o = LANES / 2; o > 0; o >>= 1)
             ss += __shfl_xor_sync(~0u, ss, o);
-        if (p.weight != nullptr) {
-            const float f = rsqrtf(ss * (1.f / D) + p.eps);
-            float w[8];
-            unpack8(__ldg(reinterpret_cast<const uint4 *>(p.weight) + sub), w);
+        const float f = rsqrtf(ss * (1.f / D) + p.eps);
 #pragma unroll
-            for (int i = 0; i < 8; ++i)
-                y[i] = y[i] * f * w[i];
-        }
+        for (int i = 0; i < 8; ++i)
+            y[i] = y[i] * f * w.w[i];
     }
-    if (p.cos_sin != nullptr) {
+    if (p.cos_sin != nullptr && 8 * sub < p.rot) {
+        const float c[4] = {a.c.x, a.c.y, a.c.z, a.c.w}, s[4] = {a.s.x, a.s.y, a.s.z, a.s.w};
         if (p.interleaved) {
-            if (8 * sub < p.rot) {
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const float u = y[2 * i], v = y[2 * i + 1];
-                    y[2 * i] = u * a.c[i] - v * a.s[i];
-                    y[2 * i + 1] = v * a.c[i] + u * a.s[i];
-                }
+            for (int i = 0; i < 4; ++i) {
+                const float u = y[2 * i], v = y[2 * i + 1];
+                y[2 * i] = u * c[i] - v * s[i];
+                y[2 * i + 1] = v * c[i] + u * s[i];
             }
         } else {
-            const int half = p.rot / 16;  // lanes of half the rotated elements
-            const bool first = sub < half;
-            const int other = first ? sub + half : (sub < 2 * half ? sub - half : sub);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const float v = __shfl_sync(~0u, y[i], other, LANES);
-                if (sub < 2 * half)
-                    y[i] = first ? y[i] * a.c[i] - v * a.s[i] : y[i] * a.c[i] + v * a.s[i];
+            for (int i = 0; i < 4; ++i) {
+                const float u = y[i], v = y[4 + i];
+                y[i] = u * c[i] - v * s[i];
+                y[4 + i] = v * c[i] + u * s[i];
             }
         }
     }
 }
 
-// The last b with cu[b] <= x for 0 <= x < cu[seqs] (a warp's lanes search
-// together); the owner of token x.
-__device__ __forceinline__ int owner_of(const int32_t *cu, int seqs, int64_t x, int lane)
+// The last b in [0, seqs) with key(b) <= x, for a rising key with key(0) <= x;
+// a warp's lanes search together.
+template <class Key>
+__device__ __forceinline__ int last_at_most(Key key, int seqs, int64_t x, int lane)
 {
-    int lo = 0, hi = seqs;  // cu[lo] <= x < cu[hi]
+    int lo = 0, hi = seqs;  // key(lo) <= x < key(hi)
     while (hi - lo > 1) {
         const int step = (hi - lo + 31) / 32;
         const int at = lo + (lane + 1) * step;
-        const bool le = at < hi && __ldg(cu + at) <= x;
-        const int n = __popc(__ballot_sync(~0u, le));
-        lo += n * step;
+        const bool le = at < hi && key(at) <= x;
+        lo += __popc(__ballot_sync(~0u, le)) * step;
         hi = min(hi, lo + step);
     }
     return lo;
+}
+
+// The sequence that token x of those laid out by the prefix sums cu belongs to.
+__device__ __forceinline__ int owner_of(const int32_t *cu, int seqs, int64_t x, int lane)
+{
+    return last_at_most([cu](int b) { return (int64_t)__ldg(cu + b); }, seqs, x, lane);
 }
 
 // --- rows of heads: [tokens][heads] strided in, contiguous out
@@ -166,59 +182,65 @@ struct HeadsIn {
     Row qrow, krow;
 };
 
-// One warp's task: R rows for each of its 32 / LANES groups of lanes, all of
-// one token, whose angles it loads once.  `chunk` counts a token's tasks.
+// One warp's task: R rows for each of its 32 / LANES groups of lanes, heads of
+// one kind and one token, whose weights and angles it loads once.  A token has
+// q_chunks tasks of query heads, then those of the key heads.
 template <int D, int R>
-__device__ __forceinline__ void heads_task(const HeadsIn &p, int64_t token, int chunk, int64_t pos, int lane)
-{
-    constexpr int LANES = D / 8, GROUPS = 32 / LANES;
-    const int sub = lane % LANES, grp = lane / LANES;
-    const int heads = p.q_heads + p.k_heads;
-    uint4 raw[R];
-    int head[R];
+struct HeadsTask {
+    static constexpr int LANES = D / 8, GROUPS = 32 / LANES, ROWS = R * GROUPS;
+    Raw raw[R];
+    const __nv_bfloat16 *weight;
+    __nv_bfloat16 *out;
+    int head0, heads;
+
+    // the rows' loads; what follows may wait for the position meanwhile
+    __device__ __forceinline__ void load(const HeadsIn &p, int64_t token, int chunk, int q_chunks, int lane)
+    {
+        const bool q = chunk < q_chunks;
+        heads = q ? p.q_heads : p.k_heads;
+        head0 = (q ? chunk : chunk - q_chunks) * ROWS + lane / LANES;
+        const Where at = elements_of<D>(p.qrow, lane % LANES);
+        const __nv_bfloat16 *row = q ? p.q + token * p.q_stride : p.k + token * p.k_stride;
+        out = q ? p.q_out + token * heads * D : p.k_out + token * heads * D;
+        weight = q ? p.qrow.weight : p.krow.weight;
 #pragma unroll
-    for (int i = 0; i < R; ++i) {
-        head[i] = chunk * (R * GROUPS) + i * GROUPS + grp;
-        raw[i] = make_uint4(0, 0, 0, 0);
-        if (head[i] < heads) {
-            const bool q = head[i] < p.q_heads;
-            const __nv_bfloat16 *src = q ? p.q + token * p.q_stride + (int64_t)head[i] * D
-                                         : p.k + token * p.k_stride + (int64_t)(head[i] - p.q_heads) * D;
-            raw[i] = __ldcs(reinterpret_cast<const uint4 *>(src) + sub);
-        }
+        for (int i = 0; i < R; ++i)  // heads past the last are its copies, and are not stored
+            raw[i] = load_raw(row + (int64_t)min(head0 + i * GROUPS, heads - 1) * D, at);
     }
-    Angles a;
-    load_angles<D>(p.qrow, pos, sub, a);
-#pragma unroll
-    for (int i = 0; i < R; ++i) {
-        const bool q = head[i] < p.q_heads;
+    __device__ __forceinline__ void store(const HeadsIn &p, int64_t pos, int lane)
+    {
+        const int sub = lane % LANES;
         Row row = p.qrow;
-        row.weight = q ? p.qrow.weight : p.krow.weight;
-        row.norm = p.qrow.norm || p.krow.norm;
-        float y[8];
-        unpack8(raw[i], y);
-        turn<D>(row, a, sub, y);
-        if (head[i] < heads) {
-            __nv_bfloat16 *dst = q ? p.q_out + (token * p.q_heads + head[i]) * D
-                                   : p.k_out + (token * p.k_heads + head[i] - p.q_heads) * D;
-            reinterpret_cast<uint4 *>(dst)[sub] = pack8(y);
+        row.weight = weight;
+        const Where at = elements_of<D>(row, sub);
+        const Angles a = load_angles(row, pos, sub);
+        const Weights w = load_weights(row, at);
+#pragma unroll
+        for (int i = 0; i < R; ++i) {
+            float y[8];
+            unpack8(raw[i], y);
+            turn<D>(row, w, a, sub, y);
+            if (head0 + i * GROUPS < heads)
+                store_row(out + (int64_t)(head0 + i * GROUPS) * D, at, y);
         }
     }
-}
+};
 
 constexpr int HEAD_WARPS = 4;
 
 template <int D, int R>
 __global__ void __launch_bounds__(32 * HEAD_WARPS) qk_norm_rope_kernel(const HeadsIn p, const int32_t *pos,
-                                                                       int chunks)
+                                                                       int q_chunks, int chunks)
 {
+    const int64_t task = (int64_t)blockIdx.x * HEAD_WARPS + (threadIdx.x >> 5);
+    const unsigned token = (unsigned)task / (unsigned)chunks;
     pdl_wait();
     pdl_launch_dependents();
-    const int64_t task = (int64_t)blockIdx.x * HEAD_WARPS + (threadIdx.x >> 5);
-    const int64_t token = task / chunks;
     if (token >= p.tokens)
         return;
-    heads_task<D, R>(p, token, (int)(task % chunks), pos ? pos[token] : token, threadIdx.x & 31);
+    HeadsTask<D, R> t;
+    t.load(p, token, (int)(task - (int64_t)token * chunks), q_chunks, threadIdx.x & 31);
+    t.store(p, pos ? (int64_t)__ldg(pos + token) : (int64_t)token, threadIdx.x & 31);
 }
 
 // --- codes
@@ -304,24 +326,54 @@ struct AppendParams {
     int head_blocks;
 };
 
+// A lane's codes of a row of D, where its elements are.
+__device__ __forceinline__ void store_codes(uint8_t *row, Where w, uint2 c)
+{
+    *reinterpret_cast<uint32_t *>(row + w.first) = c.x;
+    *reinterpret_cast<uint32_t *>(row + w.second) = c.y;
+}
+
+// Rewrites n 16-byte groups of codes under the page's new scale, 4 KB at a
+// time, so that their loads wait for memory together.
+template <bool FP8>
+__device__ __forceinline__ void recode(uint4 *held, int n, int lane, float r)
+{
+    constexpr int BATCH = 8;
+    for (int i0 = lane; i0 < n; i0 += 32 * BATCH) {
+        uint4 c[BATCH];
+#pragma unroll
+        for (int i = 0; i < BATCH; ++i)
+            if (i0 + 32 * i < n)
+                c[i] = held[i0 + 32 * i];
+#pragma unroll
+        for (int i = 0; i < BATCH; ++i)
+            if (i0 + 32 * i < n) {
+                const uint2 lo = recode8<FP8>(make_uint2(c[i].x, c[i].y), r);
+                const uint2 hi = recode8<FP8>(make_uint2(c[i].z, c[i].w), r);
+                held[i0 + 32 * i] = make_uint4(lo.x, lo.y, hi.x, hi.y);
+            }
+    }
+}
+
 // One new token per sequence: a warp writes one (sequence, kv head) row of K or
 // V, its groups of D / 8 lanes computing the same row; the first blocks take
 // the query heads.  A page whose scale grows (one token in n + 1 with n before
-// it, on gaussian rows) is read and written back 4 KB at a time, so that its
-// loads wait for memory together.
+// it, on gaussian rows) is read and written back.
 template <int D, bool FP8>
 __global__ void __launch_bounds__(32 * HEAD_WARPS) kv8_append_one_kernel(const AppendParams p)
 {
-    constexpr int LANES = D / 8, BATCH = 8;
-    pdl_wait();
-    pdl_launch_dependents();
+    constexpr int LANES = D / 8;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int sub = lane % LANES;
+    pdl_wait();
+    pdl_launch_dependents();
     if ((int)blockIdx.x < p.head_blocks) {
-        const int64_t task = (int64_t)blockIdx.x * HEAD_WARPS + warp;
-        const int64_t token = task / p.head_chunks;
-        if (token < p.tokens)
-            heads_task<D, 1>(p.heads, token, (int)(task % p.head_chunks), (int64_t)p.c.lens[token] - 1, lane);
+        const unsigned task = blockIdx.x * HEAD_WARPS + warp, token = task / (unsigned)p.head_chunks;
+        if (token < p.tokens) {
+            HeadsTask<D, 1> t;
+            t.load(p.heads, token, (int)(task - token * p.head_chunks), p.head_chunks, lane);
+            t.store(p.heads, (int64_t)p.c.lens[token] - 1, lane);
+        }
         return;
     }
     int unit = (int)(blockIdx.x - p.head_blocks) * HEAD_WARPS + warp;
@@ -330,12 +382,12 @@ __global__ void __launch_bounds__(32 * HEAD_WARPS) kv8_append_one_kernel(const A
     unit -= value ? per : 0;
     if (unit >= per)
         return;
-    const int b = unit / p.c.kv_heads, h = unit % p.c.kv_heads;
+    const int b = (int)((unsigned)unit / (unsigned)p.c.kv_heads), h = unit - b * p.c.kv_heads;
     const int64_t pos = (int64_t)p.c.lens[b] - 1;
+    const Where at = elements_of<D>(p.krow, sub);
+    const Raw raw = load_raw((value ? p.v + b * p.v_stride : p.k + b * p.k_stride) + (int64_t)h * D, at);
     if (pos < 0 || (pos >> p.c.page_log2) >= p.c.width)
         return;
-    const uint4 raw = __ldcs(reinterpret_cast<const uint4 *>((value ? p.v + b * p.v_stride : p.k + b * p.k_stride) +
-                                                             (int64_t)h * D) + sub);
     const int page = __ldg(p.c.table + (int64_t)b * p.c.width + (pos >> p.c.page_log2));
     if ((unsigned)page >= (unsigned)p.c.blocks)
         return;
@@ -347,192 +399,183 @@ __global__ void __launch_bounds__(32 * HEAD_WARPS) kv8_append_one_kernel(const A
         old = *scale;
     float y[8];
     unpack8(raw, y);
-    if (!value) {
-        Angles a;
-        load_angles<D>(p.krow, pos, sub, a);
-        turn<D>(p.krow, a, sub, y);
-    }
+    if (!value)
+        turn<D>(p.krow, load_weights(p.krow, at), load_angles(p.krow, pos, sub), sub, y);
     old = __shfl_sync(~0u, old, 0);
     const float s = fmaxf(__fdiv_rn(max_abs<LANES>(y), FP8 ? 448.f : 127.f), old);
     uint8_t *codes = (value ? p.c.v : p.c.k) + ((ph << p.c.page_log2) * D);
     if (lane < LANES)
-        reinterpret_cast<uint2 *>(codes + (int64_t)slot * D)[lane] = encode8<FP8>(y, s);
+        store_codes(codes + (int64_t)slot * D, at, encode8<FP8>(y, s));
     if (lane == 0)
         *scale = s;
-    if (slot > 0 && s > old) {
-        const float r = __fdiv_rn(old, s);
-        uint4 *held = reinterpret_cast<uint4 *>(codes);
-        const int n = slot * (D / 16);
-        for (int i0 = lane; i0 < n; i0 += 32 * BATCH) {
-            uint4 c[BATCH];
-#pragma unroll
-            for (int i = 0; i < BATCH; ++i)
-                if (i0 + 32 * i < n)
-                    c[i] = held[i0 + 32 * i];
-#pragma unroll
-            for (int i = 0; i < BATCH; ++i)
-                if (i0 + 32 * i < n) {
-                    const uint2 lo = recode8<FP8>(make_uint2(c[i].x, c[i].y), r);
-                    const uint2 hi = recode8<FP8>(make_uint2(c[i].z, c[i].w), r);
-                    held[i0 + 32 * i] = make_uint4(lo.x, lo.y, hi.x, hi.y);
-                }
-        }
-    }
+    if (slot > 0 && s > old)
+        recode<FP8>(reinterpret_cast<uint4 *>(codes), slot * (D / 16), lane, __fdiv_rn(old, s));
 }
 
-// Any number of new tokens per sequence: one CTA writes the part of one page
-// (of one kv head, K or V) that they fill.  Page j of the new tokens of
-// sequence b is number cu[b] / page + 2 b + j: at least as many numbers lie
-// between one sequence's first and the next one's as it can touch pages, so
-// tokens / page + 2 seqs CTAs per head cover every case and the ones without
-// a page leave.
-constexpr int PAGE_THREADS = 256;
+// Any number of new tokens per sequence: WARPS warps write the part of one
+// page (of one kv head, K or V) that they fill, each up to 2048 elements of
+// it in registers.  Page j of the new tokens of sequence b is number
+// cu[b] / page + 2 b + j: at least as many numbers lie between one sequence's
+// first and the next one's as it can touch pages, so tokens / page + 2 seqs
+// numbers cover every case and the ones without a page are left.
+template <int D, int PL>
+struct PageUnit {
+    static constexpr int WARPS = (D << PL) > 2048 ? (D << PL) / 2048 : 1;
+    static constexpr int CTA_WARPS = WARPS > 8 ? WARPS : 8;
+};
 
 template <int D, int PL, bool FP8>
-__global__ void __launch_bounds__(PAGE_THREADS) kv8_append_kernel(const AppendParams p)
+__global__ void __launch_bounds__(32 * PageUnit<D, PL>::CTA_WARPS) kv8_append_kernel(const AppendParams p)
 {
-    constexpr int LANES = D / 8, AT_ONCE = PAGE_THREADS / LANES, PAGE = 1 << PL;
-    constexpr int R = PAGE > AT_ONCE ? PAGE / AT_ONCE : 1;
-    __shared__ float s_max[PAGE_THREADS / 32];
+    constexpr int PAGE = 1 << PL, LANES = D / 8, GROUPS = 32 / LANES;
+    constexpr int WARPS = PageUnit<D, PL>::WARPS, CTA_WARPS = PageUnit<D, PL>::CTA_WARPS;
+    constexpr int R = (PAGE + WARPS * GROUPS - 1) / (WARPS * GROUPS);  // rows of a group of lanes
+    __shared__ float s_max[CTA_WARPS];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, sub = lane % LANES;
     pdl_wait();
     pdl_launch_dependents();
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, sub = lane % LANES;
     if ((int)blockIdx.x < p.head_blocks) {
-        const int64_t task = (int64_t)blockIdx.x * (PAGE_THREADS / 32) + warp;
-        const int64_t token = task / p.head_chunks;
+        const int64_t task = (int64_t)blockIdx.x * CTA_WARPS + warp;
+        const unsigned token = (unsigned)task / (unsigned)p.head_chunks;
         if (token < p.tokens) {
+            HeadsTask<D, 4> t;
+            t.load(p.heads, token, (int)(task - (int64_t)token * p.head_chunks), p.head_chunks, lane);
             const int b = owner_of(p.cu, p.c.seqs, token, lane);
-            const int64_t pos = (int64_t)p.c.lens[b] - p.cu[b + 1] + token;
-            heads_task<D, 2>(p.heads, token, (int)(task % p.head_chunks), pos, lane);
+            t.store(p.heads, (int64_t)p.c.lens[b] - p.cu[b + 1] + token, lane);
         }
         return;
     }
-    int64_t unit = blockIdx.x - p.head_blocks;
-    const bool value = unit % 2;
-    unit /= 2;
-    const int h = (int)(unit % p.c.kv_heads);
-    unit /= p.c.kv_heads;
-    int b = -1;
-    for (int i0 = 0; i0 < p.c.seqs; i0 += PAGE_THREADS) {
-        const int i = i0 + tid;
-        b += __syncthreads_count(i < p.c.seqs && (int64_t)(__ldg(p.cu + i) >> PL) + 2 * i <= unit);
-    }
-    if (b < 0)
-        return;
-    const int64_t first = __ldg(p.cu + b), count = __ldg(p.cu + b + 1) - first;
+    // the unit of this warp and its place among the unit's warps; K and V of a page, then its heads
+    int64_t unit = (int64_t)(blockIdx.x - p.head_blocks) * (CTA_WARPS / WARPS) + warp / WARPS;
+    const int part = warp % WARPS;
+    const bool value = unit & 1;
+    unit >>= 1;
+    const int64_t number = unit / p.c.kv_heads;
+    const int h = (int)(unit - number * p.c.kv_heads);
+    const int32_t *cu = p.cu;
+    bool live = number < (p.tokens >> PL) + 2 * p.c.seqs;
+    const int b = last_at_most([cu](int i) { return (int64_t)(__ldg(cu + i) >> PL) + 2 * i; }, p.c.seqs, number, lane);
+    const int64_t first = __ldg(cu + b), count = __ldg(cu + b + 1) - first;
     const int64_t len = p.c.lens[b], before = len - count;
     const int64_t start = before > 0 ? before : 0;
-    const int64_t pg = (start >> PL) + (unit - ((first >> PL) + 2 * b));
-    if (count <= 0 || (pg << PL) >= len || pg >= p.c.width)
-        return;
-    const int page = __ldg(p.c.table + (int64_t)b * p.c.width + pg);
-    if ((unsigned)page >= (unsigned)p.c.blocks)
-        return;
-    const int64_t pos0 = pg << PL;
-    const int held = (int)(before > pos0 ? before - pos0 : 0);  // earlier tokens of the page
+    const int64_t pg = (start >> PL) + (number - ((first >> PL) + 2 * b)), pos0 = pg << PL;
+    live = live && count > 0 && pg >= (start >> PL) && pos0 < len && pg < p.c.width;
+    int page = live ? __ldg(p.c.table + (int64_t)b * p.c.width + pg) : -1;
+    live = (unsigned)page < (unsigned)p.c.blocks;
+    if (!live)
+        page = 0;
+    // the new slots lo .. hi - 1 of the page; the ones below lo hold earlier tokens
+    const int lo = (int)(start > pos0 ? start - pos0 : 0);
+    const int hi = live ? (int)(len - pos0 < PAGE ? len - pos0 : PAGE) : 0;
     const int64_t ph = (int64_t)page * p.c.kv_heads + h;
     float *scale = (value ? p.c.v_scale : p.c.k_scale) + ph;
-    const float old = held > 0 ? *scale : 0.f;
 
     Row row = p.krow;
     if (value) {
-        row.norm = false;
+        row.weight = nullptr;
         row.cos_sin = nullptr;
     }
-    auto is_new = [&](int slot, int64_t &token) {
-        const int64_t pos = pos0 + slot;
-        token = first + pos - before;
-        return slot < PAGE && pos >= start && pos < len && token >= 0 && token < p.tokens;
-    };
-    uint4 raw[R] = {};
-    float top = 0.f;
+    const Where at = elements_of<D>(p.krow, sub);
+    // row i of this group of lanes is slot lo + part + WARPS (i GROUPS + group): the first new slots go to all warps
+    auto slot_of = [&](int i) { return lo + part + WARPS * (i * GROUPS + lane / LANES); };
+    auto any = [&](int i) { return lo + part + WARPS * i * GROUPS < hi; };  // of the warp's
+    Raw raw[R] = {};
+#pragma unroll
+    for (int i = 0; i < R; ++i) {
+        const int64_t token = first + pos0 + slot_of(i) - before;
+        if (slot_of(i) < hi && token >= 0 && token < p.tokens)
+            raw[i] = load_raw((value ? p.v + token * p.v_stride : p.k + token * p.k_stride) + (int64_t)h * D, at);
+    }
+    float old = 0.f;
+    if (lane == 0 && lo > 0 && hi > 0)
+        old = *scale;
+    old = __shfl_sync(~0u, old, 0);
+    const Weights weights = load_weights(row, at);
     auto values = [&](int i, float (&y)[8]) {
-        Angles a;
-        load_angles<D>(row, pos0 + i * AT_ONCE + tid / LANES, sub, a);
         unpack8(raw[i], y);
-        turn<D>(row, a, sub, y);
+        turn<D>(row, weights, load_angles(row, pos0 + slot_of(i), sub), sub, y);
     };
+    // the scale needs every row, the codes need the scale: rows are computed twice, or kept where there is one
+    float top = 0.f, y[8] = {};
 #pragma unroll
-    for (int i = 0; i < R; ++i) {
-        int64_t token;
-        raw[i] = make_uint4(0, 0, 0, 0);
-        if (is_new(i * AT_ONCE + tid / LANES, token))
-            raw[i] = __ldcs(reinterpret_cast<const uint4 *>((value ? p.v + token * p.v_stride : p.k + token * p.k_stride) +
-                                                            (int64_t)h * D) + sub);
+    for (int i = 0; i < R; ++i)
+        if (any(i)) {
+            values(i, y);
+            top = fmaxf(top, max_abs<32>(y));
+        }
+    if constexpr (WARPS > 1) {
+        if (lane == 0)
+            s_max[warp] = top;
+        __syncthreads();
+#pragma unroll
+        for (int w = 0; w < WARPS; ++w)
+            top = fmaxf(top, s_max[warp - part + w]);
     }
-#pragma unroll
-    for (int i = 0; i < R; ++i) {
-        float y[8];
-        values(i, y);
-        top = fmaxf(top, max_abs<32>(y));
-    }
-    if (lane == 0)
-        s_max[warp] = top;
-    __syncthreads();
-#pragma unroll
-    for (int w = 0; w < PAGE_THREADS / 32; ++w)
-        top = fmaxf(top, s_max[w]);
+    if (hi == 0)
+        return;
     const float s = fmaxf(__fdiv_rn(top, FP8 ? 448.f : 127.f), old);
-    uint2 *codes = reinterpret_cast<uint2 *>((value ? p.c.v : p.c.k) + ((ph << PL) * D)) + sub;
+    uint8_t *codes = (value ? p.c.v : p.c.k) + ((ph << PL) * D);
 #pragma unroll
-    for (int i = 0; i < R; ++i) {
-        const int slot = i * AT_ONCE + tid / LANES;
-        int64_t token;
-        float y[8];
-        values(i, y);
-        if (is_new(slot, token))
-            codes[slot * LANES] = encode8<FP8>(y, s);
-        else if (slot < held && s > old)
-            codes[slot * LANES] = recode8<FP8>(codes[slot * LANES], __fdiv_rn(old, s));
-    }
-    if (tid == 0)
+    for (int i = 0; i < R; ++i)
+        if (any(i)) {
+            if (R > 1 && any(1))
+                values(i, y);
+            const int64_t token = first + pos0 + slot_of(i) - before;
+            if (slot_of(i) < hi && token >= 0 && token < p.tokens)
+                store_codes(codes + (int64_t)slot_of(i) * D, at, encode8<FP8>(y, s));
+        }
+    if (part == 0 && lane == 0)
         *scale = s;
+    if (lo > 0 && s > old && part == 0)
+        recode<FP8>(reinterpret_cast<uint4 *>(codes), lo * (D / 16), lane, __fdiv_rn(old, s));
 }
 
 // The values that the cache stands for: the last cu[b + 1] - cu[b] positions
-// of each sequence, one after the other.
+// of each sequence, one after the other; 8 codes a lane.
 template <int D, bool FP8>
 __global__ void __launch_bounds__(32 * HEAD_WARPS) kv8_read_kernel(const Kv8 c, const int32_t *cu, int64_t tokens,
                                                                    __nv_bfloat16 *k_out, __nv_bfloat16 *v_out,
                                                                    int chunks)
 {
     constexpr int LANES = D / 8, GROUPS = 32 / LANES;
-    pdl_wait();
-    pdl_launch_dependents();
     const int lane = threadIdx.x & 31, sub = lane % LANES;
     const int64_t task = (int64_t)blockIdx.x * HEAD_WARPS + (threadIdx.x >> 5);
-    const int64_t token = task / chunks;
+    const unsigned token = (unsigned)task / (unsigned)chunks;
+    pdl_wait();
+    pdl_launch_dependents();
     if (token >= tokens)
         return;
     const int b = cu ? owner_of(cu, c.seqs, token, lane) : (int)token;
-    const int64_t pos = (int64_t)c.lens[b] - (cu ? cu[b + 1] - token : 1);
-    const int h = (int)(task % chunks) * GROUPS + lane / LANES;
+    const int64_t len = c.lens[b], pos = len - (cu ? __ldg(cu + b + 1) - (int64_t)token : 1);
+    const int h = (int)(task - (int64_t)token * chunks) * GROUPS + lane / LANES;
     if (h >= c.kv_heads)
         return;
-    int64_t page = -1;
-    if (pos >= 0 && pos < c.lens[b] && (pos >> c.page_log2) < c.width)
+    int page = -1;
+    if (pos >= 0 && pos < len && (pos >> c.page_log2) < c.width)
         page = __ldg(c.table + (int64_t)b * c.width + (pos >> c.page_log2));
     float k[8] = {}, v[8] = {};
-    if (page >= 0 && page < c.blocks) {
-        const int64_t ph = page * c.kv_heads + h;
+    if ((unsigned)page < (unsigned)c.blocks) {
+        const int64_t ph = (int64_t)page * c.kv_heads + h;
         const int64_t at = ((ph << c.page_log2) + (pos & ((1 << c.page_log2) - 1))) * LANES + sub;
-        decode8<FP8>(__ldg(reinterpret_cast<const uint2 *>(c.k) + at), k);
-        decode8<FP8>(__ldg(reinterpret_cast<const uint2 *>(c.v) + at), v);
+        const uint2 kc = __ldg(reinterpret_cast<const uint2 *>(c.k) + at), vc = __ldg(reinterpret_cast<const uint2 *>(c.v) + at);
         const float sk = c.k_scale[ph], sv = c.v_scale[ph];
+        decode8<FP8>(kc, k);
+        decode8<FP8>(vc, v);
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
             k[i] *= sk;
             v[i] *= sv;
         }
     }
-    const int64_t to = (token * c.kv_heads + h) * LANES + sub;
-    reinterpret_cast<uint4 *>(k_out)[to] = pack8(k);
-    reinterpret_cast<uint4 *>(v_out)[to] = pack8(v);
+    const Where w = {8 * sub, 8 * sub + 4};
+    const int64_t to = ((int64_t)token * c.kv_heads + h) * D;
+    store_row(k_out + to, w, k);
+    store_row(v_out + to, w, v);
 }
 
 Row row_of(const HeadPrep &prep, const void *weight)
 {
-    return Row{static_cast<const __nv_bfloat16 *>(weight), weight != nullptr, prep.cos_sin, prep.positions, prep.rot,
+    return Row{static_cast<const __nv_bfloat16 *>(weight), prep.cos_sin, prep.positions, prep.rot,
                prep.interleaved, prep.eps};
 }
 
@@ -549,37 +592,43 @@ cudaError_t norm_rope(const HeadsIn &in, const int32_t *pos, cudaStream_t stream
     // for all of them; with few tokens one row each spreads the call over more SMs.
     const int heads = in.q_heads + in.k_heads;
     const bool few = in.tokens * heads * (D / 8) < 152LL * 2048;
-    const int chunks = chunks_of(heads, D, few ? 1 : 4);
-    const int64_t blocks = (in.tokens * chunks + HEAD_WARPS - 1) / HEAD_WARPS;
-    if (few)
-        return launch_pdl(qk_norm_rope_kernel<D, 1>, dim3((unsigned)blocks), dim3(32 * HEAD_WARPS), 0, stream, in,
-                          pos, chunks);
-    return launch_pdl(qk_norm_rope_kernel<D, 4>, dim3((unsigned)blocks), dim3(32 * HEAD_WARPS), 0, stream, in, pos,
-                      chunks);
+    const int R = few ? 1 : 4, q_chunks = chunks_of(in.q_heads, D, R), chunks = q_chunks + chunks_of(in.k_heads, D, R);
+    const dim3 grid((unsigned)((in.tokens * chunks + HEAD_WARPS - 1) / HEAD_WARPS)), block(32 * HEAD_WARPS);
+    return launch_pdl(few ? qk_norm_rope_kernel<D, 1> : qk_norm_rope_kernel<D, 4>, grid, block, 0, stream, in, pos,
+                      q_chunks, chunks);
+}
+
+template <int D, int PL, bool FP8>
+cudaError_t append_pages(AppendParams &p, cudaStream_t stream)
+{
+    constexpr int WARPS = PageUnit<D, PL>::WARPS, CTA_WARPS = PageUnit<D, PL>::CTA_WARPS;
+    if (p.heads.q_heads > 0) {
+        p.head_chunks = chunks_of(p.heads.q_heads, D, 4);
+        p.head_blocks = (int)((p.tokens * p.head_chunks + CTA_WARPS - 1) / CTA_WARPS);
+    }
+    const int64_t units = ((p.tokens >> PL) + 2LL * p.c.seqs) * p.c.kv_heads * 2, per = CTA_WARPS / WARPS;
+    return launch_pdl(kv8_append_kernel<D, PL, FP8>, dim3((unsigned)(p.head_blocks + (units + per - 1) / per)),
+                      dim3(32 * CTA_WARPS), 0, stream, p);
 }
 
 template <int D, bool FP8>
 cudaError_t append(AppendParams &p, cudaStream_t stream)
 {
-    const bool one = p.cu == nullptr;
-    const int warps = one ? HEAD_WARPS : PAGE_THREADS / 32;
-    if (p.heads.q_heads > 0) {
-        p.head_chunks = chunks_of(p.heads.q_heads, D, one ? 1 : 2);
-        p.head_blocks = (int)((p.tokens * p.head_chunks + warps - 1) / warps);
-    }
-    if (one) {
+    if (p.cu == nullptr) {
+        if (p.heads.q_heads > 0) {
+            p.head_chunks = chunks_of(p.heads.q_heads, D, 1);
+            p.head_blocks = (int)((p.tokens * p.head_chunks + HEAD_WARPS - 1) / HEAD_WARPS);
+        }
         const int64_t units = 2LL * p.c.seqs * p.c.kv_heads;
         return launch_pdl(kv8_append_one_kernel<D, FP8>,
                           dim3((unsigned)(p.head_blocks + (units + HEAD_WARPS - 1) / HEAD_WARPS)),
                           dim3(32 * HEAD_WARPS), 0, stream, p);
     }
-    const int64_t units = ((p.tokens >> p.c.page_log2) + 2LL * p.c.seqs) * p.c.kv_heads * 2;
-    const dim3 grid((unsigned)(p.head_blocks + units)), block(PAGE_THREADS);
     switch (p.c.page_log2) {
-    case 4: return launch_pdl(kv8_append_kernel<D, 4, FP8>, grid, block, 0, stream, p);
-    case 5: return launch_pdl(kv8_append_kernel<D, 5, FP8>, grid, block, 0, stream, p);
-    case 6: return launch_pdl(kv8_append_kernel<D, 6, FP8>, grid, block, 0, stream, p);
-    default: return launch_pdl(kv8_append_kernel<D, 7, FP8>, grid, block, 0, stream, p);
+    case 4: return append_pages<D, 4, FP8>(p, stream);
+    case 5: return append_pages<D, 5, FP8>(p, stream);
+    case 6: return append_pages<D, 6, FP8>(p, stream);
+    default: return append_pages<D, 7, FP8>(p, stream);
     }
 }
 
