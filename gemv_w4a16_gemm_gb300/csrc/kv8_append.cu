@@ -245,48 +245,87 @@ __global__ void __launch_bounds__(32 * HEAD_WARPS) qk_norm_rope_kernel(const Hea
 
 // --- codes
 
-// max |y| / top and the codes of 8 elements, for either format
+__device__ __forceinline__ uint32_t e4m3_pair(float lo, float hi)
+{
+    uint16_t h;
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(h) : "f"(hi), "f"(lo));
+    return h;
+}
+
+// The codes of y / 1, |y| <= 127 (int8).
+template <bool FP8>
+__device__ __forceinline__ uint2 encode8(const float (&y)[8])
+{
+    uint32_t w[2] = {0, 0};
+    if constexpr (FP8) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            w[i >> 1] |= e4m3_pair(y[2 * i], y[2 * i + 1]) << (16 * (i & 1));
+    } else {
+        // 1.5 2^23 + y rounds y to an integer (half to even) whose low byte is the code; |y| <= 127
+        uint32_t q[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            q[i] = __float_as_uint(__fadd_rn(y[i], 12582912.f));
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+            w[i] = prmt(prmt(q[4 * i], q[4 * i + 1], 0x0040u), prmt(q[4 * i + 2], q[4 * i + 3], 0x0040u), 0x5410u);
+    }
+    return make_uint2(w[0], w[1]);
+}
+
+// The codes of the correctly rounded quotients y / s, for |y| / top <= s.  A
+// quotient costs a dozen instructions; y times the rounded reciprocal lies
+// within 2^-22 of it and gives the same code except next to a rounding's edge,
+// where the quotient decides (int8: act_code8; e4m3: both ends of the interval
+// 2^-21 wide are converted and have to agree).
 template <bool FP8>
 __device__ __forceinline__ uint2 encode8(const float (&y)[8], float s)
 {
-    uint32_t w[2] = {0, 0};
-    if (s > 0.f) {
-        if constexpr (FP8) {
+    if (!(s > 0.f))
+        return make_uint2(0u, 0u);
+    float q[8];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                uint16_t h;
-                asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;"
-                    : "=h"(h)
-                    : "f"(__fdiv_rn(y[2 * i + 1], s)), "f"(__fdiv_rn(y[2 * i], s)));
-                w[i >> 1] |= (uint32_t)h << (16 * (i & 1));
-            }
-        } else {
+    for (int i = 0; i < 8; ++i)
+        q[i] = y[i];
+    if constexpr (FP8) {
+        const float r = __frcp_rn(s), lo = r * (1.f - 0x1p-21f), hi = r * (1.f + 0x1p-21f);
+        uint32_t a[2] = {0, 0}, b[2] = {0, 0};
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const float q = fminf(fmaxf(rintf(__fdiv_rn(y[i], s)), -127.f), 127.f);
-                w[i >> 2] |= ((uint32_t)(int)q & 0xFFu) << (8 * (i & 3));
-            }
+        for (int i = 0; i < 4; ++i) {
+            a[i >> 1] |= e4m3_pair(q[2 * i] * lo, q[2 * i + 1] * lo) << (16 * (i & 1));
+            b[i >> 1] |= e4m3_pair(q[2 * i] * hi, q[2 * i + 1] * hi) << (16 * (i & 1));
         }
+        if (a[0] != b[0] || a[1] != b[1] || !(s >= 0x1p-125f)) {  // below that the reciprocal overflows
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                q[i] = __fdiv_rn(q[i], s);
+            return encode8<true>(q);
+        }
+        return make_uint2(a[0], a[1]);
+    } else {
+        act_code8(q, s);
+        return encode8<false>(q);
     }
-    return make_uint2(w[0], w[1]);
 }
 
 template <bool FP8>
 __device__ __forceinline__ void decode8(uint2 c, float (&y)[8])
 {
+    if constexpr (FP8) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const uint32_t h = ((i & 2) ? c.y : c.x) >> (16 * (i & 1));
-        if constexpr (FP8) {
+        for (int i = 0; i < 4; ++i) {
             uint32_t f;
-            asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(f) : "h"((uint16_t)h));
+            asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(f) : "h"((uint16_t)(((i & 2) ? c.y : c.x) >> (16 * (i & 1)))));
             const float2 v = __half22float2(*reinterpret_cast<const __half2 *>(&f));
             y[2 * i] = v.x;
             y[2 * i + 1] = v.y;
-        } else {
-            y[2 * i] = (float)(int8_t)(h & 0xFF);
-            y[2 * i + 1] = (float)(int8_t)((h >> 8) & 0xFF);
         }
+    } else {
+        // the byte with its sign flipped under 0x4B0000 is 2^23 + 128 + code
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            y[i] = __uint_as_float(prmt((i < 4 ? c.x : c.y) ^ 0x80808080u, 0x4B000000u, 0x7440u + (i & 3))) - 8388736.f;
     }
 }
 
@@ -298,8 +337,8 @@ __device__ __forceinline__ uint2 recode8(uint2 c, float r)
     decode8<FP8>(c, y);
 #pragma unroll
     for (int i = 0; i < 8; ++i)
-        y[i] *= r;
-    return encode8<FP8>(y, 1.f);
+        y[i] = __fmul_rn(y[i], r);  // rounded by itself: not fused with the rounding to a code
+    return encode8<FP8>(y);
 }
 
 template <int LANES>
@@ -333,24 +372,25 @@ __device__ __forceinline__ void store_codes(uint8_t *row, Where w, uint2 c)
     *reinterpret_cast<uint32_t *>(row + w.second) = c.y;
 }
 
-// Rewrites n 16-byte groups of codes under the page's new scale, 4 KB at a
-// time, so that their loads wait for memory together.
+// Rewrites n 16-byte groups of codes under the page's new scale, by `all`
+// threads of which this is `me`, eight groups a thread at a time, so that their
+// loads wait for memory together.
 template <bool FP8>
-__device__ __forceinline__ void recode(uint4 *held, int n, int lane, float r)
+__device__ __forceinline__ void recode(uint4 *held, int n, int me, int all, float r)
 {
     constexpr int BATCH = 8;
-    for (int i0 = lane; i0 < n; i0 += 32 * BATCH) {
+    for (int i0 = me; i0 < n; i0 += all * BATCH) {
         uint4 c[BATCH];
 #pragma unroll
         for (int i = 0; i < BATCH; ++i)
-            if (i0 + 32 * i < n)
-                c[i] = held[i0 + 32 * i];
+            if (i0 + all * i < n)
+                c[i] = held[i0 + all * i];
 #pragma unroll
         for (int i = 0; i < BATCH; ++i)
-            if (i0 + 32 * i < n) {
+            if (i0 + all * i < n) {
                 const uint2 lo = recode8<FP8>(make_uint2(c[i].x, c[i].y), r);
                 const uint2 hi = recode8<FP8>(make_uint2(c[i].z, c[i].w), r);
-                held[i0 + 32 * i] = make_uint4(lo.x, lo.y, hi.x, hi.y);
+                held[i0 + all * i] = make_uint4(lo.x, lo.y, hi.x, hi.y);
             }
     }
 }
@@ -409,65 +449,61 @@ __global__ void __launch_bounds__(32 * HEAD_WARPS) kv8_append_one_kernel(const A
     if (lane == 0)
         *scale = s;
     if (slot > 0 && s > old)
-        recode<FP8>(reinterpret_cast<uint4 *>(codes), slot * (D / 16), lane, __fdiv_rn(old, s));
+        recode<FP8>(reinterpret_cast<uint4 *>(codes), slot * (D / 16), lane, 32, __fdiv_rn(old, s));
 }
 
-// Any number of new tokens per sequence: WARPS warps write the part of one
-// page (of one kv head, K or V) that they fill, each up to 2048 elements of
-// it in registers.  Page j of the new tokens of sequence b is number
-// cu[b] / page + 2 b + j: at least as many numbers lie between one sequence's
-// first and the next one's as it can touch pages, so tokens / page + 2 seqs
-// numbers cover every case and the ones without a page are left.
-template <int D, int PL>
-struct PageUnit {
-    static constexpr int WARPS = (D << PL) > 2048 ? (D << PL) / 2048 : 1;
-    static constexpr int CTA_WARPS = WARPS > 8 ? WARPS : 8;
-};
+// Any number of new tokens per sequence: `share` warps (a power of two) write
+// the part of one page (of one kv head, K or V) that they fill.  Page j of the
+// new tokens of sequence b is number cu[b] / page + 2 b + j: at least as many
+// numbers lie between one sequence's first and the next one's as it can touch
+// pages, so tokens / page + 2 seqs numbers cover every case and the ones
+// without a page are left.  The scale needs every row and the codes need the
+// scale: up to 2 rows of a group of lanes stay in registers in between, more
+// are computed again.  (64 registers a thread, so that the query heads' blocks
+// of the same launch keep 32 warps an SM busy with loads.)
+constexpr int PAGE_WARPS = 8;
 
-template <int D, int PL, bool FP8>
-__global__ void __launch_bounds__(32 * PageUnit<D, PL>::CTA_WARPS) kv8_append_kernel(const AppendParams p)
+template <int D, bool FP8>
+__global__ void __launch_bounds__(32 * PAGE_WARPS, 4) kv8_append_kernel(const AppendParams p, int share)
 {
-    constexpr int PAGE = 1 << PL, LANES = D / 8, GROUPS = 32 / LANES;
-    constexpr int WARPS = PageUnit<D, PL>::WARPS, CTA_WARPS = PageUnit<D, PL>::CTA_WARPS;
-    constexpr int R = (PAGE + WARPS * GROUPS - 1) / (WARPS * GROUPS);  // rows of a group of lanes
-    __shared__ float s_max[CTA_WARPS];
+    constexpr int LANES = D / 8, GROUPS = 32 / LANES, R = 2;
+    __shared__ float s_max[PAGE_WARPS];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, sub = lane % LANES;
     pdl_wait();
     pdl_launch_dependents();
-    if ((int)blockIdx.x < p.head_blocks) {
-        const int64_t task = (int64_t)blockIdx.x * CTA_WARPS + warp;
+    // the pages' blocks come first: they take longest
+    const int page_blocks = gridDim.x - p.head_blocks;
+    if ((int)blockIdx.x >= page_blocks) {
+        const int64_t task = (int64_t)(blockIdx.x - page_blocks) * PAGE_WARPS + warp;
         const unsigned token = (unsigned)task / (unsigned)p.head_chunks;
         if (token < p.tokens) {
             HeadsTask<D, 4> t;
             t.load(p.heads, token, (int)(task - (int64_t)token * p.head_chunks), p.head_chunks, lane);
             const int b = owner_of(p.cu, p.c.seqs, token, lane);
-            t.store(p.heads, (int64_t)p.c.lens[b] - p.cu[b + 1] + token, lane);
+            t.store(p.heads, (int64_t)p.c.lens[b] - __ldg(p.cu + b + 1) + token, lane);
         }
         return;
     }
     // the unit of this warp and its place among the unit's warps; K and V of a page, then its heads
-    int64_t unit = (int64_t)(blockIdx.x - p.head_blocks) * (CTA_WARPS / WARPS) + warp / WARPS;
-    const int part = warp % WARPS;
+    const unsigned unit = (blockIdx.x * PAGE_WARPS + warp) / (unsigned)share;
+    const int part = warp & (share - 1), page_log2 = p.c.page_log2, page = 1 << page_log2;
     const bool value = unit & 1;
-    unit >>= 1;
-    const int64_t number = unit / p.c.kv_heads;
-    const int h = (int)(unit - number * p.c.kv_heads);
+    const int number = (int)((unit >> 1) / (unsigned)p.c.kv_heads), h = (int)((unit >> 1) - number * (unsigned)p.c.kv_heads);
     const int32_t *cu = p.cu;
-    bool live = number < (p.tokens >> PL) + 2 * p.c.seqs;
-    const int b = last_at_most([cu](int i) { return (int64_t)(__ldg(cu + i) >> PL) + 2 * i; }, p.c.seqs, number, lane);
+    bool live = number < (p.tokens >> page_log2) + 2 * p.c.seqs;
+    const int b = last_at_most([cu, page_log2](int i) { return (int64_t)(__ldg(cu + i) >> page_log2) + 2 * i; }, p.c.seqs,
+                               number, lane);
     const int64_t first = __ldg(cu + b), count = __ldg(cu + b + 1) - first;
     const int64_t len = p.c.lens[b], before = len - count;
     const int64_t start = before > 0 ? before : 0;
-    const int64_t pg = (start >> PL) + (number - ((first >> PL) + 2 * b)), pos0 = pg << PL;
-    live = live && count > 0 && pg >= (start >> PL) && pos0 < len && pg < p.c.width;
-    int page = live ? __ldg(p.c.table + (int64_t)b * p.c.width + pg) : -1;
-    live = (unsigned)page < (unsigned)p.c.blocks;
-    if (!live)
-        page = 0;
+    const int64_t pg = (start >> page_log2) + (number - ((first >> page_log2) + 2 * b)), pos0 = pg << page_log2;
+    live = live && count > 0 && pg >= (start >> page_log2) && pos0 < len && pg < p.c.width;
+    const int block = live ? __ldg(p.c.table + (int64_t)b * p.c.width + pg) : -1;
+    live = (unsigned)block < (unsigned)p.c.blocks;
     // the new slots lo .. hi - 1 of the page; the ones below lo hold earlier tokens
     const int lo = (int)(start > pos0 ? start - pos0 : 0);
-    const int hi = live ? (int)(len - pos0 < PAGE ? len - pos0 : PAGE) : 0;
-    const int64_t ph = (int64_t)page * p.c.kv_heads + h;
+    const int hi = live ? (int)(len - pos0 < page ? len - pos0 : page) : 0;
+    const int64_t ph = (live ? (int64_t)block : 0) * p.c.kv_heads + h;
     float *scale = (value ? p.c.v_scale : p.c.k_scale) + ph;
 
     Row row = p.krow;
@@ -476,58 +512,62 @@ __global__ void __launch_bounds__(32 * PageUnit<D, PL>::CTA_WARPS) kv8_append_ke
         row.cos_sin = nullptr;
     }
     const Where at = elements_of<D>(p.krow, sub);
-    // row i of this group of lanes is slot lo + part + WARPS (i GROUPS + group): the first new slots go to all warps
-    auto slot_of = [&](int i) { return lo + part + WARPS * (i * GROUPS + lane / LANES); };
-    auto any = [&](int i) { return lo + part + WARPS * i * GROUPS < hi; };  // of the warp's
-    Raw raw[R] = {};
+    const __nv_bfloat16 *src = (value ? p.v : p.k) + (int64_t)h * D;
+    const int64_t stride = value ? p.v_stride : p.k_stride, token0 = first + pos0 - before;
+    // Row i of batch n of this group of lanes is a slot of its own; the first new slots go to all warps.
+    auto slot_of = [&](int n, int i) { return lo + part + share * ((n * R + i) * GROUPS + lane / LANES); };
+    auto any = [&](int n, int i) { return lo + part + share * (n * R + i) * GROUPS < hi; };  // of the warp's
+    auto is_token = [&](int slot) { return slot < hi && token0 + slot >= 0 && token0 + slot < p.tokens; };
+    const Weights weights = load_weights(row, at);
+    float y[R][8];
+    auto batch = [&](int n) {
+        Raw raw[R] = {};
 #pragma unroll
-    for (int i = 0; i < R; ++i) {
-        const int64_t token = first + pos0 + slot_of(i) - before;
-        if (slot_of(i) < hi && token >= 0 && token < p.tokens)
-            raw[i] = load_raw((value ? p.v + token * p.v_stride : p.k + token * p.k_stride) + (int64_t)h * D, at);
-    }
+        for (int i = 0; i < R; ++i)
+            if (is_token(slot_of(n, i)))
+                raw[i] = load_raw(src + (token0 + slot_of(n, i)) * stride, at);
+#pragma unroll
+        for (int i = 0; i < R; ++i) {
+            unpack8(raw[i], y[i]);
+            if (any(n, i))
+                turn<D>(row, weights, load_angles(row, pos0 + slot_of(n, i), sub), sub, y[i]);
+        }
+    };
     float old = 0.f;
     if (lane == 0 && lo > 0 && hi > 0)
         old = *scale;
-    old = __shfl_sync(~0u, old, 0);
-    const Weights weights = load_weights(row, at);
-    auto values = [&](int i, float (&y)[8]) {
-        unpack8(raw[i], y);
-        turn<D>(row, weights, load_angles(row, pos0 + slot_of(i), sub), sub, y);
-    };
-    // the scale needs every row, the codes need the scale: rows are computed twice, or kept where there is one
-    float top = 0.f, y[8] = {};
+    float top = 0.f;
+    for (int n = 0; n == 0 || any(n, 0); ++n) {
+        batch(n);
 #pragma unroll
-    for (int i = 0; i < R; ++i)
-        if (any(i)) {
-            values(i, y);
-            top = fmaxf(top, max_abs<32>(y));
-        }
-    if constexpr (WARPS > 1) {
+        for (int i = 0; i < R; ++i)
+            top = fmaxf(top, max_abs<32>(y[i]));
+    }
+    old = __shfl_sync(~0u, old, 0);
+    if (share > 1) {
         if (lane == 0)
             s_max[warp] = top;
         __syncthreads();
-#pragma unroll
-        for (int w = 0; w < WARPS; ++w)
+        for (int w = 0; w < share; ++w)
             top = fmaxf(top, s_max[warp - part + w]);
     }
     if (hi == 0)
         return;
     const float s = fmaxf(__fdiv_rn(top, FP8 ? 448.f : 127.f), old);
-    uint8_t *codes = (value ? p.c.v : p.c.k) + ((ph << PL) * D);
+    uint8_t *codes = (value ? p.c.v : p.c.k) + ((ph << page_log2) * D);
+    const bool kept = !any(1, 0);
+    for (int n = 0; n == 0 || any(n, 0); ++n) {
+        if (!kept)
+            batch(n);
 #pragma unroll
-    for (int i = 0; i < R; ++i)
-        if (any(i)) {
-            if (R > 1 && any(1))
-                values(i, y);
-            const int64_t token = first + pos0 + slot_of(i) - before;
-            if (slot_of(i) < hi && token >= 0 && token < p.tokens)
-                store_codes(codes + (int64_t)slot_of(i) * D, at, encode8<FP8>(y, s));
-        }
+        for (int i = 0; i < R; ++i)
+            if (is_token(slot_of(n, i)))
+                store_codes(codes + (int64_t)slot_of(n, i) * D, at, encode8<FP8>(y[i], s));
+    }
     if (part == 0 && lane == 0)
         *scale = s;
-    if (lo > 0 && s > old && part == 0)
-        recode<FP8>(reinterpret_cast<uint4 *>(codes), lo * (D / 16), lane, __fdiv_rn(old, s));
+    if (lo > 0 && s > old)
+        recode<FP8>(reinterpret_cast<uint4 *>(codes), lo * (D / 16), part * 32 + lane, 32 * share, __fdiv_rn(old, s));
 }
 
 // The values that the cache stands for: the last cu[b + 1] - cu[b] positions
@@ -598,19 +638,6 @@ cudaError_t norm_rope(const HeadsIn &in, const int32_t *pos, cudaStream_t stream
                       q_chunks, chunks);
 }
 
-template <int D, int PL, bool FP8>
-cudaError_t append_pages(AppendParams &p, cudaStream_t stream)
-{
-    constexpr int WARPS = PageUnit<D, PL>::WARPS, CTA_WARPS = PageUnit<D, PL>::CTA_WARPS;
-    if (p.heads.q_heads > 0) {
-        p.head_chunks = chunks_of(p.heads.q_heads, D, 4);
-        p.head_blocks = (int)((p.tokens * p.head_chunks + CTA_WARPS - 1) / CTA_WARPS);
-    }
-    const int64_t units = ((p.tokens >> PL) + 2LL * p.c.seqs) * p.c.kv_heads * 2, per = CTA_WARPS / WARPS;
-    return launch_pdl(kv8_append_kernel<D, PL, FP8>, dim3((unsigned)(p.head_blocks + (units + per - 1) / per)),
-                      dim3(32 * CTA_WARPS), 0, stream, p);
-}
-
 template <int D, bool FP8>
 cudaError_t append(AppendParams &p, cudaStream_t stream)
 {
@@ -624,12 +651,19 @@ cudaError_t append(AppendParams &p, cudaStream_t stream)
                           dim3((unsigned)(p.head_blocks + (units + HEAD_WARPS - 1) / HEAD_WARPS)),
                           dim3(32 * HEAD_WARPS), 0, stream, p);
     }
-    switch (p.c.page_log2) {
-    case 4: return append_pages<D, 4, FP8>(p, stream);
-    case 5: return append_pages<D, 5, FP8>(p, stream);
-    case 6: return append_pages<D, 6, FP8>(p, stream);
-    default: return append_pages<D, 7, FP8>(p, stream);
+    if (p.heads.q_heads > 0) {
+        p.head_chunks = chunks_of(p.heads.q_heads, D, 4);
+        p.head_blocks = (int)((p.tokens * p.head_chunks + PAGE_WARPS - 1) / PAGE_WARPS);
     }
+    // Warps per page: as many as hold a full page in registers, one where a sequence brings few
+    // tokens (64 sequences with one token: 14 us with 8, 6.4 us with one).
+    int share = 1;
+    if (p.tokens >= 8LL * p.c.seqs)
+        while (share < PAGE_WARPS && (D << p.c.page_log2) > 512 * share)
+            share *= 2;
+    const int64_t units = ((p.tokens >> p.c.page_log2) + 2LL * p.c.seqs) * p.c.kv_heads * 2, per = PAGE_WARPS / share;
+    return launch_pdl(kv8_append_kernel<D, FP8>, dim3((unsigned)(p.head_blocks + (units + per - 1) / per)),
+                      dim3(32 * PAGE_WARPS), 0, stream, p, share);
 }
 
 template <int D>
