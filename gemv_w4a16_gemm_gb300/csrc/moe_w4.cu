@@ -18,13 +18,18 @@
 //   down     y = W2 h, fp32
 //   combine  out = sum of weight * y, in the order of choice
 //
-// The two products.  A unit is RT 16-row tiles of one expert (a gate and an up
-// half each for gate/up) times that expert's tokens; KW warps share its K, each
-// streaming its 256-column super-blocks through a ring of its own in shared
-// memory (cp.async, contiguous RT * 2432 bytes), so the warps meet only to add
-// their sums.  The units of the active experts go round the resident CTAs.
-// A super-block's x fragments come through L1 (the fragment order makes them
-// two 16-byte loads per 64 columns), once for all RT tiles.
+// The two products.  A unit is one 16-row tile of an expert's result (for
+// gate/up the gate and the up tile of those rows) times that expert's tokens;
+// the units of the active experts go round the resident CTAs.  KW warps share
+// a unit's K: each takes every KW-th 256-column super-block, and they meet only
+// to add their sums.  A tile goes from global memory to registers: a lane's
+// 16-byte chunk of codes is four MMAs' A fragments, its rows' scales and zero
+// points are three more loads, and each register is loaded again for the next
+// tile (of the next unit, too) as soon as it is used up.  The tokens' rows, in
+// the order of the B fragments (two 16-byte loads a lane per 64 columns), come
+// through L1, which is free to hold them: no shared memory is used for tiles.
+// (Tiles through a cp.async ring in shared memory: 8 warps an SM and L1 misses
+// for the rows, 295 us for 64 tokens x 2 of 16 experts (6656, 4096).)
 //
 // Arithmetic.  A word of packed codes, masked, is a pair of bf16 subnormals
 // q 2^-133 (low nibbles) or q 2^-129 (high nibbles); one bf16x2 fma with 2^127
@@ -33,8 +38,6 @@
 // rounded to bf16, as an activation between two of the library's linear layers
 // is.
 #include <cooperative_groups.h>
-
-#include <atomic>
 
 #include "common.cuh"
 #include "decode.h"
@@ -47,7 +50,7 @@ namespace w4q {
 namespace {
 
 constexpr int TILE_BYTES = 2432;
-constexpr int MAX_EXPERTS = 512, MAX_TOPK = 16, MAX_TOKENS = 64;
+constexpr int MAX_EXPERTS = 512, MAX_TOKENS = 64;
 
 // ------------------------------------------------------------------- route
 
@@ -254,35 +257,75 @@ struct GemmParams {
     int KW;        // warps that share a unit's K
 };
 
-__device__ __forceinline__ void cp16(uint32_t dst, const void *src, uint64_t policy)
+__device__ __forceinline__ uint4 ldg_weight(const uint8_t *p)
 {
-    asm volatile("cp.async.cg.shared.global.L2::cache_hint [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "l"(policy)
-                 : "memory");
+    uint4 v;
+    asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "l"(p));
+    return v;
 }
 
-template <bool GATED, int RT, int NT, int S>
-struct GemmSmem {
-    static constexpr int STEP = RT * TILE_BYTES;
-    static constexpr int RING = GW * S * STEP;
-    static constexpr int SUMS = GW * RT * NT * 128 * 4;
-    static size_t bytes(int entries, int experts) { return RING + SUMS + entries * 4 + experts * 4 + 64 * 4; }
+// A lane's part of a tile: the four sub-blocks' codes, the bf16 scale pairs of
+// rows g, g + 8 for the 8 groups, and their zero points.
+struct Tile {
+    uint4 q[4], s[2], z;
 };
 
-// RT tiles a step: gate/up RT / 2 gate tiles, then the up tiles of the same
-// rows; down RT consecutive tiles.  NT groups of 8 tokens at a time.
-template <bool GATED, int RT, int NT, int S, int CPS>
-__global__ void __launch_bounds__(32 * GW, CPS) moe_gemm_kernel(const GemmParams p)
+template <int V>
+struct Count {
+    static constexpr int value = V;
+};
+
+// One sub-block (64 columns, two groups of 32) of a tile times NT groups of 8
+// tokens: acc += s * sum (q - z) x 2^-6.
+template <int NT>
+__device__ __forceinline__ void tile_step(const uint4 &q, uint32_t s0, uint32_t s1, uint32_t zz, const uint4 (&x)[NT][2],
+                                          float (&acc)[NT][4])
 {
-    using SM = GemmSmem<GATED, RT, NT, S>;
-    extern __shared__ __align__(16) uint8_t smem[];
-    float *s_sum = reinterpret_cast<float *>(smem + SM::RING);                     // [warp][RT][NT][128]
-    int *s_ids = reinterpret_cast<int *>(smem + SM::RING + SM::SUMS);              // [entries]
-    int *s_active = s_ids + p.entries;                                             // [active experts]
+#pragma unroll
+    for (int gr = 0; gr < 2; ++gr) {
+        // -z 2^-6 of rows g, g + 8
+        const uint32_t z0 = bf16x2_mul(prmt(zz, 0u, gr ? 0x4242u : 0x4040u), NEG_2P127);
+        const uint32_t z1 = bf16x2_mul(prmt(zz, 0u, gr ? 0x4343u : 0x4141u), NEG_2P127);
+        float d[NT][4];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+            d[nt][0] = d[nt][1] = d[nt][2] = d[nt][3] = 0.f;
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            const uint32_t w = (&q.x)[2 * gr + k], wh = w >> 8;
+            const uint32_t a[4] = {bf16x2_fma(w & 0x000F000Fu, BF_2P127, z0), bf16x2_fma(wh & 0x000F000Fu, BF_2P127, z1),
+                                   bf16x2_fma(w & 0x00F000F0u, BF_2P123, z0), bf16x2_fma(wh & 0x00F000F0u, BF_2P123, z1)};
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+                mma_bf16(d[nt], a, k ? x[nt][gr].z : x[nt][gr].x, k ? x[nt][gr].w : x[nt][gr].y, d[nt]);
+        }
+        const uint32_t sc = gr ? s1 : s0;
+        const float sa = bf16lo_to_f32(sc), sb = bf16hi_to_f32(sc);
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+            acc[nt][0] = fmaf(sa, d[nt][0], acc[nt][0]);
+            acc[nt][1] = fmaf(sa, d[nt][1], acc[nt][1]);
+            acc[nt][2] = fmaf(sb, d[nt][2], acc[nt][2]);
+            acc[nt][3] = fmaf(sb, d[nt][3], acc[nt][3]);
+        }
+    }
+}
+
+// Tiles of a unit: gate/up two (the gate tile and the up tile of the same 16
+// rows), down one.  NT groups of 8 tokens at a time, at most.
+template <bool GATED, int NT>
+__global__ void __launch_bounds__(32 * GW, 4) moe_gemm_kernel(const GemmParams p)
+{
+    constexpr int TU = GATED ? 2 : 1;
+    extern __shared__ __align__(16) int s_ids[];     // [entries], then the active experts
+    int *s_active = s_ids + p.entries;
+    __shared__ __align__(16) float s_sum[GW][TU * NT][128];
     __shared__ uint32_t s_mask[MAX_EXPERTS / 32];
     __shared__ int s_count;
     __shared__ int s_list[GW][MAX_TOKENS];  // a warp's tokens: entries of its expert
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
-    const uint64_t policy = policy_evict_first();
 
     if (tid < MAX_EXPERTS / 32)
         s_mask[tid] = 0;
@@ -312,49 +355,39 @@ __global__ void __launch_bounds__(32 * GW, CPS) moe_gemm_kernel(const GemmParams
     }
     __syncthreads();
 
-    constexpr int ROWS = GATED ? RT / 2 : RT;  // tiles of the result a unit covers
-    const int KB = p.K / 256, blocks = p.rows_out / (16 * ROWS);
+    const int KB = p.K / 256, blocks = p.rows_out / 16;
     const int units = s_count * blocks;
-    const int KW = p.KW, kw = warp % KW, group = warp / KW, groups = GW / KW;
+    const int KW = p.KW, kw = warp & (KW - 1), group = warp / KW, groups = GW / KW;
     const int first = blockIdx.x * groups + group, stride = gridDim.x * groups;
-    const int steps = kw < KB ? (KB - kw + KW - 1) / KW : 0;  // of this warp in a unit
+    if (first >= units)
+        return;  // the whole group, which has a barrier of its own
+    const uint8_t *codes = p.packed + 16 * lane, *scales = p.packed + 2048 + 16 * g;
 
-    const uint32_t ring = smem_addr(smem) + warp * (S * SM::STEP);
-    // the copies run S - 1 steps ahead, across units
-    int fu = first, fs = 0, fstage = 0;
-    auto fetch = [&]() {
-        if (fu < units && steps > 0) {
-            const int e = s_active[fu / blocks], blk = fu % blocks, b = kw + fs * KW;
-            const int tile = GATED ? e * (2 * p.rows_out / 16) + blk * ROWS : e * (p.rows_out / 16) + blk * ROWS;
-            const uint32_t dst = ring + fstage * SM::STEP;
-            auto part = [&](int tl, uint32_t to, int bytes) {
-                const uint8_t *src = p.packed + (((int64_t)(tl >> 3) * KB + b) * 8 + (tl & 7)) * TILE_BYTES;
-                for (int i = lane * 16; i < bytes; i += 512)
-                    cp16(to + i, src + i, policy);
-            };
-            if constexpr (GATED) {
-                part(tile, dst, ROWS * TILE_BYTES);
-                part(tile + p.rows_out / 16, dst + ROWS * TILE_BYTES, ROWS * TILE_BYTES);
-            } else {
-                part(tile, dst, RT * TILE_BYTES);
-            }
-            if (++fs == steps) {
-                fs = 0;
-                fu += stride;
-            }
-        }
-        asm volatile("cp.async.commit_group;" ::: "memory");
-        fstage = fstage + 1 == S ? 0 : fstage + 1;
+    // the tile of (unit u, super-block b, r) and the one after it, in the order
+    // in which this warp takes them
+    auto tile_at = [&](int u, int b, int r) -> int64_t {
+        const int e = s_active[(unsigned)u / (unsigned)blocks], blk = (unsigned)u % (unsigned)blocks;
+        const int tl = (e * TU + r) * blocks + blk;
+        return (((int64_t)(tl >> 3) * KB + b) * 8 + (tl & 7)) * TILE_BYTES;
     };
-
-    int stage = 0, last_e = -1, n = 0;
-    // An expert with more than 8 NT tokens takes several passes; the ring's order is that of one
-    // pass, so the further passes read their tiles again, without running ahead.
+    Tile w;
+    auto load_codes = [&](int64_t at, int sb) { w.q[sb] = ldg_weight(codes + at + 512 * sb); };
+    auto load_scales = [&](int64_t at) {
+        w.s[0] = ldg_weight(scales + at);
+        w.s[1] = ldg_weight(scales + at + 128);
+        w.z = ldg_weight(scales + at + 256);
+    };
+    {
+        const int64_t at = tile_at(first, kw, 0);
 #pragma unroll
-    for (int i = 0; i < S - 1; ++i)
-        fetch();
+        for (int sb = 0; sb < 4; ++sb)
+            load_codes(at, sb);
+        load_scales(at);
+    }
+
+    int last_e = -1, n = 0;
     for (int u = first; u < units; u += stride) {
-        const int e = s_active[u / blocks], blk = u % blocks;
+        const int e = s_active[(unsigned)u / (unsigned)blocks], blk = (unsigned)u % (unsigned)blocks;
         if (e != last_e) {
             n = 0;
             for (int i0 = 0; i0 < p.entries; i0 += 32) {
@@ -367,164 +400,111 @@ __global__ void __launch_bounds__(32 * GW, CPS) moe_gemm_kernel(const GemmParams
             __syncwarp();
             last_e = e;
         }
-        for (int n0 = 0; n0 < n; n0 += 8 * NT) {
-            const uint16_t *row[NT];
-            bool have[NT];
+        // an expert with more than 8 NT tokens takes several passes over its tiles
+        auto pass = [&](auto groups_of_8, int n0) {
+            constexpr int N = decltype(groups_of_8)::value;
+            const bool again = n0 + 8 * N < n;
+            const uint16_t *row[N];  // tokens past the last are its copies, and are not stored
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-                have[nt] = n0 + nt * 8 + g < n;
-                const int entry = have[nt] ? s_list[warp][n0 + nt * 8 + g] : 0;
+            for (int nt = 0; nt < N; ++nt) {
+                const int entry = s_list[warp][min(n0 + nt * 8 + g, n - 1)];
                 row[nt] = p.xf + (int64_t)(GATED ? entry / p.topk : entry) * p.K + 16 * t;
             }
-            const bool second = NT > 1 && n0 + 8 < n;
-            float acc[RT][NT][4];
+            float acc[TU][N][4];
 #pragma unroll
-            for (int r = 0; r < RT; ++r)
+            for (int r = 0; r < TU; ++r)
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
+                for (int nt = 0; nt < N; ++nt)
                     acc[r][nt][0] = acc[r][nt][1] = acc[r][nt][2] = acc[r][nt][3] = 0.f;
-            for (int s = 0; s < steps; ++s) {
-                const int b = kw + s * KW;
-                uint32_t src = ring + stage * SM::STEP;
-                if (n0 == 0) {
-                    asm volatile("cp.async.wait_group %0;" ::"n"(S - 2) : "memory");
-                    __syncwarp();  // every lane's copies are here, and the previous step's stage is read
-                    fetch();
-                } else {
-                    // a further pass: this step's tiles once more, into the ring's free stage
-                    src = ring + fstage * SM::STEP;
-                    const int tile = GATED ? e * (2 * p.rows_out / 16) + blk * ROWS : e * (p.rows_out / 16) + blk * ROWS;
-                    __syncwarp();
+            for (int b = kw; b < KB; b += KW) {
 #pragma unroll
-                    for (int r = 0; r < RT; ++r) {
-                        const int tl = GATED && r >= ROWS ? tile + p.rows_out / 16 + r - ROWS : tile + r;
-                        const uint8_t *from = p.packed + (((int64_t)(tl >> 3) * KB + b) * 8 + (tl & 7)) * TILE_BYTES;
-                        for (int i = lane * 16; i < TILE_BYTES; i += 512)
-                            cp16(src + r * TILE_BYTES + i, from + i, policy);
-                    }
-                    asm volatile("cp.async.commit_group;\n\tcp.async.wait_group 0;" ::: "memory");
-                    __syncwarp();
-                }
+                for (int r = 0; r < TU; ++r) {
+                    int64_t next = -1;
+                    if (r + 1 < TU)
+                        next = tile_at(u, b, r + 1);
+                    else if (b + KW < KB)
+                        next = tile_at(u, b + KW, 0);
+                    else if (again)
+                        next = tile_at(u, kw, 0);
+                    else if (u + stride < units)
+                        next = tile_at(u + stride, kw, 0);
+                    const uint4 s0 = w.s[0], s1 = w.s[1], z = w.z;
+                    if (next >= 0)
+                        load_scales(next);
 #pragma unroll
-                for (int sb = 0; sb < 4; ++sb) {
-                    uint4 x[NT][2];
+                    for (int sb = 0; sb < 4; ++sb) {
+                        uint4 x[N][2];
 #pragma unroll
-                    for (int nt = 0; nt < NT; ++nt) {
-                        x[nt][0] = x[nt][1] = make_uint4(0, 0, 0, 0);
-                        if (have[nt]) {
+                        for (int nt = 0; nt < N; ++nt) {
                             const uint4 *q = reinterpret_cast<const uint4 *>(row[nt] + b * 256 + sb * 64);
                             x[nt][0] = __ldg(q);
                             x[nt][1] = __ldg(q + 1);
                         }
-                    }
-#pragma unroll
-                    for (int r = 0; r < RT; ++r) {
-                        const uint32_t base = src + r * TILE_BYTES;
-                        const uint4 q = lds128(base + 512 * sb + 16 * lane);
-                        uint32_t sc[2], zz;
-                        asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];"
-                                     : "=r"(sc[0]), "=r"(sc[1])
-                                     : "r"(base + 2048 + 128 * (sb >> 1) + 16 * g + 8 * (sb & 1)));
-                        asm volatile("ld.shared.u32 %0, [%1];" : "=r"(zz) : "r"(base + 2304 + 16 * g + 4 * sb));
-#pragma unroll
-                        for (int gr = 0; gr < 2; ++gr) {
-                            // -z 2^-6 of rows g, g + 8
-                            const uint32_t z0 = bf16x2_mul(prmt(zz, 0u, gr ? 0x4242u : 0x4040u), NEG_2P127);
-                            const uint32_t z1 = bf16x2_mul(prmt(zz, 0u, gr ? 0x4343u : 0x4141u), NEG_2P127);
-                            float d[NT][4];
-#pragma unroll
-                            for (int nt = 0; nt < NT; ++nt)
-                                d[nt][0] = d[nt][1] = d[nt][2] = d[nt][3] = 0.f;
-#pragma unroll
-                            for (int k = 0; k < 2; ++k) {
-                                const uint32_t w = (&q.x)[2 * gr + k], wh = w >> 8;
-                                const uint32_t a[4] = {bf16x2_fma(w & 0x000F000Fu, BF_2P127, z0), bf16x2_fma(wh & 0x000F000Fu, BF_2P127, z1),
-                                                       bf16x2_fma(w & 0x00F000F0u, BF_2P123, z0), bf16x2_fma(wh & 0x00F000F0u, BF_2P123, z1)};
-#pragma unroll
-                                for (int nt = 0; nt < NT; ++nt)
-                                    if (nt == 0 || second)
-                                        mma_bf16(d[nt], a, k ? x[nt][gr].z : x[nt][gr].x, k ? x[nt][gr].w : x[nt][gr].y, d[nt]);
-                            }
-                            const float s0 = bf16lo_to_f32(sc[gr]), s1 = bf16hi_to_f32(sc[gr]);
-#pragma unroll
-                            for (int nt = 0; nt < NT; ++nt) {
-                                acc[r][nt][0] = fmaf(s0, d[nt][0], acc[r][nt][0]);
-                                acc[r][nt][1] = fmaf(s0, d[nt][1], acc[r][nt][1]);
-                                acc[r][nt][2] = fmaf(s1, d[nt][2], acc[r][nt][2]);
-                                acc[r][nt][3] = fmaf(s1, d[nt][3], acc[r][nt][3]);
-                            }
-                        }
+                        const uint4 &sc = sb < 2 ? s0 : s1;
+                        tile_step<N>(w.q[sb], sb & 1 ? sc.z : sc.x, sb & 1 ? sc.w : sc.y, (&z.x)[sb], x, acc[r]);
+                        if (next >= 0)
+                            load_codes(next, sb);
                     }
                 }
-                if (n0 == 0)
-                    stage = stage + 1 == S ? 0 : stage + 1;
             }
             // --- the sums of the warps that share the unit, and the result
-            float *mine = s_sum + warp * (RT * NT * 128);
             if (KW > 1) {
 #pragma unroll
-                for (int r = 0; r < RT; ++r)
+                for (int r = 0; r < TU; ++r)
 #pragma unroll
-                    for (int nt = 0; nt < NT; ++nt)
-                        *reinterpret_cast<float4 *>(mine + (r * NT + nt) * 128 + lane * 4) =
+                    for (int nt = 0; nt < N; ++nt)
+                        *reinterpret_cast<float4 *>(&s_sum[warp][r * N + nt][lane * 4]) =
                             make_float4(acc[r][nt][0], acc[r][nt][1], acc[r][nt][2], acc[r][nt][3]);
                 asm volatile("bar.sync %0, %1;" ::"r"(1 + group), "r"(32 * KW) : "memory");
             }
-            // fragment f of the result goes to warp f % KW
-            for (int f = kw; f < ROWS * NT; f += KW) {
-                float v[2][4];
 #pragma unroll
-                for (int half = 0; half < (GATED ? 2 : 1); ++half) {
-                    const int fr = f + half * ROWS * NT;
-                    if (KW > 1) {
-                        v[half][0] = v[half][1] = v[half][2] = v[half][3] = 0.f;
-                        for (int w = 0; w < KW; ++w) {
-                            const float4 x = *reinterpret_cast<const float4 *>(
-                                s_sum + (group * KW + w) * (RT * NT * 128) + fr * 128 + lane * 4);
-                            v[half][0] += x.x;
-                            v[half][1] += x.y;
-                            v[half][2] += x.z;
-                            v[half][3] += x.w;
+            for (int nt = 0; nt < N; ++nt) {
+                if ((nt & (KW - 1)) != kw)
+                    continue;
+                if (KW > 1)
+#pragma unroll
+                    for (int r = 0; r < TU; ++r) {
+                        acc[r][nt][0] = acc[r][nt][1] = acc[r][nt][2] = acc[r][nt][3] = 0.f;
+                        for (int v = 0; v < KW; ++v) {
+                            const float4 x = *reinterpret_cast<const float4 *>(&s_sum[group * KW + v][r * N + nt][lane * 4]);
+                            acc[r][nt][0] += x.x;
+                            acc[r][nt][1] += x.y;
+                            acc[r][nt][2] += x.z;
+                            acc[r][nt][3] += x.w;
                         }
-                    } else {
-#pragma unroll
-                        for (int r = 0; r < RT; ++r)
-#pragma unroll
-                            for (int nt = 0; nt < NT; ++nt)
-                                if (r * NT + nt == fr)
-#pragma unroll
-                                    for (int i = 0; i < 4; ++i)
-                                        v[half][i] = acc[r][nt][i];
                     }
-                }
-                const int tile = blk * ROWS + f / NT, col = n0 + (f % NT) * 8 + 2 * t;
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
-                    if (col + i >= n)
+                    const int col = n0 + nt * 8 + 2 * t + i;
+                    if (col >= n)
                         continue;
-                    const int entry = s_list[warp][col + i];
+                    const int entry = s_list[warp][col];
                     if constexpr (GATED) {
-                        // rows g (even half of the fragment order) and g + 8 of the 16
-                        uint16_t *dst = p.h + (int64_t)entry * p.rows_out + (tile >> 2) * 64 + (g >> 1) * 16 + (tile & 3) * 4 + (g & 1);
+                        // rows g and g + 8 of the 16, in fragment order
+                        uint16_t *dst = p.h + (int64_t)entry * p.rows_out + (blk >> 2) * 64 + (g >> 1) * 16 + (blk & 3) * 4 + (g & 1);
 #pragma unroll
                         for (int e8 = 0; e8 < 2; ++e8) {
-                            const float gate = v[0][2 * e8 + i] * 64.f, up = v[1][2 * e8 + i] * 64.f;
-                            const float hv = gate / (1.f + __expf(-gate)) * up;
-                            const __nv_bfloat16 hb = __float2bfloat16_rn(hv);
+                            const float gate = acc[0][nt][2 * e8 + i] * 64.f, up = acc[TU - 1][nt][2 * e8 + i] * 64.f;
+                            const __nv_bfloat16 hb = __float2bfloat16_rn(gate / (1.f + __expf(-gate)) * up);
                             dst[2 * e8] = *reinterpret_cast<const uint16_t *>(&hb);
                         }
                     } else {
-                        float *dst = p.y + (int64_t)entry * p.rows_out + tile * 16 + g;
-                        dst[0] = v[0][i] * 64.f;
-                        dst[8] = v[0][2 + i] * 64.f;
+                        float *dst = p.y + (int64_t)entry * p.rows_out + blk * 16 + g;
+                        dst[0] = acc[0][nt][i] * 64.f;
+                        dst[8] = acc[0][nt][2 + i] * 64.f;
                     }
                 }
             }
             if (KW > 1)  // the sums are read
                 asm volatile("bar.sync %0, %1;" ::"r"(1 + group), "r"(32 * KW) : "memory");
-        }
+        };
+        int n0 = 0;
+        if constexpr (NT > 1)
+            for (; n - n0 > 8; n0 += 16)
+                pass(Count<2>(), n0);
+        for (; n0 < n; n0 += 8)
+            pass(Count<1>(), n0);
     }
-    asm volatile("cp.async.wait_all;" ::: "memory");
 }
 
 // out[m] = sum over the choices of weight * y, four elements a thread
@@ -551,21 +531,17 @@ __global__ void __launch_bounds__(128) moe_combine_kernel(const float *y, const 
     reinterpret_cast<uint2 *>(out + (int64_t)m * hidden)[d] = *reinterpret_cast<const uint2 *>(o);
 }
 
-template <bool GATED, int RT, int NT, int S, int CPS>
+template <bool GATED>
 cudaError_t launch_gemm(GemmParams p, int sm_count, cudaStream_t stream)
 {
-    using SM = GemmSmem<GATED, RT, NT, S>;
-    static std::atomic<unsigned long long> done{0};
-    auto fn = moe_gemm_kernel<GATED, RT, NT, S, CPS>;
-    cudaError_t e = smem_opt_in_once(done, fn, (int)SM::bytes(MAX_TOKENS * MAX_TOPK, MAX_EXPERTS));
-    if (e != cudaSuccess)
-        return e;
     const int KB = p.K / 256;
-    p.KW = KB >= 4 ? 4 : (KB >= 2 ? 2 : 1);
+    p.KW = KB >= 8 ? 4 : (KB >= 2 ? 2 : 1);
     const int most = p.entries < p.experts ? p.entries : p.experts;
-    const long long ctas = ((long long)most * (p.rows_out / (16 * (GATED ? RT / 2 : RT))) * p.KW + GW - 1) / GW;
-    const long long grid = ctas < (long long)sm_count * CPS ? ctas : (long long)sm_count * CPS;
-    return launch_pdl(fn, dim3((unsigned)grid), dim3(32 * GW), SM::bytes(p.entries, p.experts), stream, p);
+    const long long ctas = ((long long)most * (p.rows_out / 16) * p.KW + GW - 1) / GW;
+    const long long grid = ctas < 4LL * sm_count ? ctas : 4LL * sm_count;
+    const size_t smem = (size_t)(p.entries + p.experts) * 4;
+    return launch_pdl(p.entries > 8 * p.topk ? moe_gemm_kernel<GATED, 2> : moe_gemm_kernel<GATED, 1>, dim3((unsigned)grid),
+                      dim3(32 * GW), smem, stream, p);
 }
 
 struct Workspace {
@@ -627,15 +603,9 @@ cudaError_t launch_moe(const Moe &a, int sm_count, void *workspace, cudaStream_t
                      a.hidden, a.inter, 1};
     GemmParams down = {static_cast<const uint8_t *>(a.w2), h, ids, nullptr, y, a.tokens * a.topk, a.topk, a.experts,
                        a.inter, a.hidden, 1};
-    if (a.tokens <= 8) {
-        e = launch_gemm<true, 2, 1, 2, 4>(up, sm_count, stream);
-        if (e == cudaSuccess)
-            e = launch_gemm<false, 2, 1, 2, 4>(down, sm_count, stream);
-    } else {
-        e = launch_gemm<true, 4, 2, 2, 2>(up, sm_count, stream);
-        if (e == cudaSuccess)
-            e = launch_gemm<false, 4, 2, 2, 2>(down, sm_count, stream);
-    }
+    e = launch_gemm<true>(up, sm_count, stream);
+    if (e == cudaSuccess)
+        e = launch_gemm<false>(down, sm_count, stream);
     if (e != cudaSuccess)
         return e;
     const long long threads = (long long)a.tokens * (a.hidden / 4);
