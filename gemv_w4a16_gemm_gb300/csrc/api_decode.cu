@@ -80,7 +80,7 @@ int check_moe(int64_t tokens, int64_t hidden, int64_t inter, int64_t experts, in
     if (tokens <= 0 || hidden <= 0 || inter <= 0 || experts <= 0 || topk <= 0 || topk > experts)
         return W4Q_ERR_INVALID_ARG;
     if (tokens > 64 || hidden % 256 != 0 || inter % 256 != 0 || hidden > 32768 || inter > 32768 || experts > 512 ||
-        topk > 16)
+        topk > 16 || experts * 2 * inter * hidden > (1LL << 36))  // a packed weight's offsets
         return W4Q_ERR_UNSUPPORTED;
     return W4Q_OK;
 }

@@ -18,18 +18,22 @@
 //   down     y = W2 h, fp32
 //   combine  out = sum of weight * y, in the order of choice
 //
-// The two products.  A unit is one 16-row tile of an expert's result (for
-// gate/up the gate and the up tile of those rows) times that expert's tokens;
-// the units of the active experts go round the resident CTAs.  KW warps share
-// a unit's K: each takes every KW-th 256-column super-block, and they meet only
-// to add their sums.  A tile goes from global memory to registers: a lane's
-// 16-byte chunk of codes is four MMAs' A fragments, its rows' scales and zero
-// points are three more loads, and each register is loaded again for the next
-// tile (of the next unit, too) as soon as it is used up.  The tokens' rows, in
-// the order of the B fragments (two 16-byte loads a lane per 64 columns), come
-// through L1, which is free to hold them: no shared memory is used for tiles.
-// (Tiles through a cp.async ring in shared memory: 8 warps an SM and L1 misses
-// for the rows, 295 us for 64 tokens x 2 of 16 experts (6656, 4096).)
+// The two products.  A unit is a pair of 16-row tiles of an expert (for gate/up
+// the gate and the up tile of the same rows, for down two neighbours) times that
+// expert's tokens.  The line of all units of the active experts, weighted by
+// what their numbers of tokens cost, is cut into equal ranges, one per resident
+// CTA, those of an SM's CTAs side by side, so that an SM's L1 holds the rows of
+// one or two experts' tokens.  KW warps share a unit's K: each takes every KW-th
+// 256-column super-block, and they meet only to add their sums.  A tile goes
+// from global memory to registers: a lane's 16-byte chunk of codes is four MMAs'
+// A fragments, its rows' scales and zero points are three more loads, and each
+// register is loaded again for the next super-block (of the next unit, too) as
+// soon as it is used up.  The tokens' rows, in the order of the B fragments (two
+// 16-byte loads a lane per 64 columns, for both tiles), come through L1, one
+// sub-block ahead: no shared memory is used for either.
+// (64 tokens x 2 of 16 experts (6656, 4096): tiles through a cp.async ring in
+// shared memory 295 us; single tiles in registers, rows loaded where they are
+// used 255 us; this xxx us.)
 //
 // Arithmetic.  A word of packed codes, masked, is a pair of bf16 subnormals
 // q 2^-133 (low nibbles) or q 2^-129 (high nibbles); one bf16x2 fma with 2^127
@@ -255,6 +259,7 @@ struct GemmParams {
     int K;         // columns
     int rows_out;  // rows per expert of the result
     int KW;        // warps that share a unit's K
+    int sms;
 };
 
 __device__ __forceinline__ uint4 ldg_weight(const uint8_t *p)
@@ -266,10 +271,10 @@ __device__ __forceinline__ uint4 ldg_weight(const uint8_t *p)
     return v;
 }
 
-// A lane's part of a tile: the four sub-blocks' codes, the bf16 scale pairs of
-// rows g, g + 8 for the 8 groups, and their zero points.
-struct Tile {
-    uint4 q[4], s[2], z;
+// A lane's part of a pair of tiles: the four sub-blocks' codes, the bf16 scale
+// pairs of rows g, g + 8 for the 8 groups, and their zero points.
+struct Pair {
+    uint4 q[2][4], s[2][2], z[2];
 };
 
 template <int V>
@@ -313,80 +318,126 @@ __device__ __forceinline__ void tile_step(const uint4 &q, uint32_t s0, uint32_t 
     }
 }
 
-// Tiles of a unit: gate/up two (the gate tile and the up tile of the same 16
-// rows), down one.  NT groups of 8 tokens at a time, at most.
-template <bool GATED, int NT>
-__global__ void __launch_bounds__(32 * GW, 4) moe_gemm_kernel(const GemmParams p)
+// What a unit of an expert with n tokens costs, in quarters of one with up to 8:
+// one pass over its tiles for every 16 tokens, or 8.
+__device__ __forceinline__ int unit_cost(int n, int nt)
 {
-    constexpr int TU = GATED ? 2 : 1;
-    extern __shared__ __align__(16) int s_ids[];     // [entries], then the active experts
-    int *s_active = s_ids + p.entries;
-    __shared__ __align__(16) float s_sum[GW][TU * NT][128];
-    __shared__ uint32_t s_mask[MAX_EXPERTS / 32];
+    const int full = nt > 1 ? (n + 7) / 16 : 0, left = n - 16 * full;
+    return 5 * full + (left > 0 ? (left + 7) / 8 * 4 : 0);
+}
+
+// NT groups of 8 tokens at a time, at most.
+template <bool GATED, int NT>
+__global__ void __launch_bounds__(32 * GW, NT > 1 ? 3 : 4) moe_gemm_kernel(const GemmParams p)
+{
+    extern __shared__ __align__(16) int s_ids[];  // [entries], then [experts]: active experts, costs before them
+    int *s_active = s_ids + p.entries, *s_before = s_active + p.experts;
+    __shared__ __align__(16) float s_sum[GW][2 * NT][128];
+    __shared__ int s_tokens[MAX_EXPERTS];
     __shared__ int s_count;
     __shared__ int s_list[GW][MAX_TOKENS];  // a warp's tokens: entries of its expert
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
 
-    if (tid < MAX_EXPERTS / 32)
-        s_mask[tid] = 0;
+    for (int i = tid; i < p.experts; i += 32 * GW)
+        s_tokens[i] = 0;
     pdl_wait();
     pdl_launch_dependents();
     __syncthreads();
     for (int i = tid; i < p.entries; i += 32 * GW) {
         const int e = __ldg(p.ids + i);
         s_ids[i] = e;
-        atomicOr(&s_mask[e >> 5], 1u << (e & 31));
+        atomicAdd(&s_tokens[e], 1);
     }
     __syncthreads();
-    if (warp == 0) {  // the active experts in order
-        const uint32_t m = lane < MAX_EXPERTS / 32 ? s_mask[lane] : 0u;
-        int n = __popc(m), at = n;
+    const int KB = p.K / 256, blocks = p.rows_out / (GATED ? 16 : 32);
+    if (warp == 0) {  // the active experts in order, and the cost of the units before each
+        int count = 0, cost = 0;
+        for (int e0 = 0; e0 < p.experts; e0 += 32) {
+            const int n = e0 + lane < p.experts ? s_tokens[e0 + lane] : 0;
+            const uint32_t m = __ballot_sync(~0u, n > 0);
+            const int c = n > 0 ? unit_cost(n, NT) * blocks : 0;
+            int x = c;
 #pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int y = __shfl_up_sync(~0u, at, o);
-            if (lane >= o)
-                at += y;
+            for (int o = 1; o < 32; o <<= 1) {
+                const int y = __shfl_up_sync(~0u, x, o);
+                if (lane >= o)
+                    x += y;
+            }
+            if (n > 0) {
+                const int at = count + __popc(m & ((1u << lane) - 1));
+                s_active[at] = e0 + lane;
+                s_before[at] = cost + x - c;
+            }
+            count += __popc(m);
+            cost += __shfl_sync(~0u, x, 31);
         }
-        if (lane == 31)
-            s_count = at;
-        at -= n;
-        for (uint32_t r = m; r != 0; r &= r - 1)
-            s_active[at++] = 32 * lane + __ffs(r) - 1;
+        if (lane == 0) {
+            s_count = count;
+            s_before[count] = cost;  // [experts] + 1
+        }
     }
     __syncthreads();
 
-    const int KB = p.K / 256, blocks = p.rows_out / 16;
-    const int units = s_count * blocks;
     const int KW = p.KW, kw = warp & (KW - 1), group = warp / KW, groups = GW / KW;
-    const int first = blockIdx.x * groups + group, stride = gridDim.x * groups;
-    if (first >= units)
+    // CTAs c, c + sms, c + 2 sms .. share an SM, as far as the hardware deals them out in turn
+    const int per_sm = (gridDim.x + p.sms - 1) / p.sms;
+    const int place = gridDim.x % p.sms == 0 ? (blockIdx.x % p.sms) * per_sm + blockIdx.x / p.sms : blockIdx.x;
+    const int ranges = gridDim.x * groups, mine = place * groups + group;
+    auto unit_after = [&](int cut) -> int {  // the first unit at or past the cost cut / ranges of the whole
+        const int count = s_count;
+        const long long at = (long long)s_before[count] * cut / ranges;
+        int lo = 0, hi = count;
+        while (hi - lo > 1) {
+            const int mid = (lo + hi) >> 1;
+            if (s_before[mid] <= at)
+                lo = mid;
+            else
+                hi = mid;
+        }
+        const int each = (s_before[lo + 1] - s_before[lo]) / blocks;
+        return lo * blocks + min(blocks, (int)((at - s_before[lo] + each - 1) / each));
+    };
+    const int first = unit_after(mine), last = unit_after(mine + 1);
+    if (first >= last)
         return;  // the whole group, which has a barrier of its own
     const uint8_t *codes = p.packed + 16 * lane, *scales = p.packed + 2048 + 16 * g;
 
-    // the tile of (unit u, super-block b, r) and the one after it, in the order
-    // in which this warp takes them
-    auto tile_at = [&](int u, int b, int r) -> int64_t {
+    // Where unit u's first tile of this warp's first super-block lies, in 16 bytes (32 bits reach 64
+    // GB); rows_out / 16 is a multiple of 16, so the pair's second tile lies `second`, and the next
+    // super-block 8 tiles, from it.
+    constexpr uint32_t TILE16 = TILE_BYTES / 16, NEXT_SB = 8 * TILE16, NONE = ~0u;
+    const uint32_t second = GATED ? (uint32_t)(blocks >> 3) * KB * NEXT_SB : TILE16;
+    auto unit_at = [&](int u) -> uint32_t {
         const int e = s_active[(unsigned)u / (unsigned)blocks], blk = (unsigned)u % (unsigned)blocks;
-        const int tl = (e * TU + r) * blocks + blk;
-        return (((int64_t)(tl >> 3) * KB + b) * 8 + (tl & 7)) * TILE_BYTES;
+        const int tl = e * 2 * blocks + (GATED ? blk : 2 * blk);
+        return (uint32_t)(tl >> 3) * KB * NEXT_SB + (tl & 7) * TILE16 + kw * NEXT_SB;
     };
-    Tile w;
-    auto load_codes = [&](int64_t at, int sb) { w.q[sb] = ldg_weight(codes + at + 512 * sb); };
-    auto load_scales = [&](int64_t at) {
-        w.s[0] = ldg_weight(scales + at);
-        w.s[1] = ldg_weight(scales + at + 128);
-        w.z = ldg_weight(scales + at + 256);
+    Pair w;
+    auto load_codes = [&](uint32_t at, int r, int sb) {
+        w.q[r][sb] = ldg_weight(codes + (uint64_t)(at + r * second) * 16 + 512 * sb);
     };
-    {
-        const int64_t at = tile_at(first, kw, 0);
+    auto load_scales = [&](uint32_t at, int r, int half) {
+        w.s[r][half] = ldg_weight(scales + (uint64_t)(at + r * second) * 16 + 128 * half);
+    };
+    auto load_zeros = [&](uint32_t at, int r) { w.z[r] = ldg_weight(scales + (uint64_t)(at + r * second) * 16 + 256); };
+    uint32_t here = unit_at(first), there;
 #pragma unroll
-        for (int sb = 0; sb < 4; ++sb)
-            load_codes(at, sb);
-        load_scales(at);
+    for (int r = 0; r < 2; ++r) {
+        load_zeros(here, r);
+        load_scales(here, r, 0);
     }
+#pragma unroll
+    for (int sb = 0; sb < 4; ++sb)
+#pragma unroll
+        for (int r = 0; r < 2; ++r)
+            load_codes(here, r, sb);
+#pragma unroll
+    for (int r = 0; r < 2; ++r)
+        load_scales(here, r, 1);
 
     int last_e = -1, n = 0;
-    for (int u = first; u < units; u += stride) {
+    for (int u = first; u < last; ++u, here = there) {
+        there = u + 1 < last ? unit_at(u + 1) : NONE;
         const int e = s_active[(unsigned)u / (unsigned)blocks], blk = (unsigned)u % (unsigned)blocks;
         if (e != last_e) {
             n = 0;
@@ -404,53 +455,71 @@ __global__ void __launch_bounds__(32 * GW, 4) moe_gemm_kernel(const GemmParams p
         auto pass = [&](auto groups_of_8, int n0) {
             constexpr int N = decltype(groups_of_8)::value;
             const bool again = n0 + 8 * N < n;
-            const uint16_t *row[N];  // tokens past the last are its copies, and are not stored
+            const uint4 *row[N];  // tokens past the last are its copies, and are not stored
 #pragma unroll
             for (int nt = 0; nt < N; ++nt) {
                 const int entry = s_list[warp][min(n0 + nt * 8 + g, n - 1)];
-                row[nt] = p.xf + (int64_t)(GATED ? entry / p.topk : entry) * p.K + 16 * t;
+                row[nt] = reinterpret_cast<const uint4 *>(
+                    p.xf + (int64_t)(GATED ? (unsigned)entry / (unsigned)p.topk : entry) * p.K + kw * 256 + 16 * t);
             }
-            float acc[TU][N][4];
+            float acc[2][N][4];
 #pragma unroll
-            for (int r = 0; r < TU; ++r)
+            for (int r = 0; r < 2; ++r)
 #pragma unroll
                 for (int nt = 0; nt < N; ++nt)
                     acc[r][nt][0] = acc[r][nt][1] = acc[r][nt][2] = acc[r][nt][3] = 0.f;
-            for (int b = kw; b < KB; b += KW) {
+            uint4 x[N][2];
 #pragma unroll
-                for (int r = 0; r < TU; ++r) {
-                    int64_t next = -1;
-                    if (r + 1 < TU)
-                        next = tile_at(u, b, r + 1);
-                    else if (b + KW < KB)
-                        next = tile_at(u, b + KW, 0);
-                    else if (again)
-                        next = tile_at(u, kw, 0);
-                    else if (u + stride < units)
-                        next = tile_at(u + stride, kw, 0);
-                    const uint4 s0 = w.s[0], s1 = w.s[1], z = w.z;
-                    if (next >= 0)
-                        load_scales(next);
+            for (int nt = 0; nt < N; ++nt) {
+                x[nt][0] = __ldg(row[nt]);
+                x[nt][1] = __ldg(row[nt] + 1);
+            }
+            uint32_t at = here;
+            for (int b = kw; b < KB; b += KW, at += KW * NEXT_SB) {
+                const bool more = b + KW < KB;
+                const uint32_t next = more ? at + KW * NEXT_SB : again ? here : there;
+                const uint4 z[2] = {w.z[0], w.z[1]};
+                if (next != NONE) {
+                    load_zeros(next, 0);
+                    load_zeros(next, 1);
+                }
 #pragma unroll
-                    for (int sb = 0; sb < 4; ++sb) {
-                        uint4 x[N][2];
+                for (int sb = 0; sb < 4; ++sb) {
+                    uint4 ahead[N][2];
 #pragma unroll
-                        for (int nt = 0; nt < N; ++nt) {
-                            const uint4 *q = reinterpret_cast<const uint4 *>(row[nt] + b * 256 + sb * 64);
-                            x[nt][0] = __ldg(q);
-                            x[nt][1] = __ldg(q + 1);
+                    for (int nt = 0; nt < N; ++nt) {
+                        ahead[nt][0] = x[nt][0];
+                        ahead[nt][1] = x[nt][1];
+                        if (sb < 3 || more) {
+                            const uint4 *src = row[nt] + (sb < 3 ? 8 * (sb + 1) : KW * 32);
+                            ahead[nt][0] = __ldg(src);
+                            ahead[nt][1] = __ldg(src + 1);
                         }
-                        const uint4 &sc = sb < 2 ? s0 : s1;
-                        tile_step<N>(w.q[sb], sb & 1 ? sc.z : sc.x, sb & 1 ? sc.w : sc.y, (&z.x)[sb], x, acc[r]);
-                        if (next >= 0)
-                            load_codes(next, sb);
+                    }
+#pragma unroll
+                    for (int r = 0; r < 2; ++r) {
+                        const uint4 &sc = w.s[r][sb >> 1];
+                        tile_step<N>(w.q[r][sb], sb & 1 ? sc.z : sc.x, sb & 1 ? sc.w : sc.y, (&z[r].x)[sb], x, acc[r]);
+                        if (next != NONE) {
+                            load_codes(next, r, sb);
+                            if (sb & 1)
+                                load_scales(next, r, sb >> 1);
+                        }
+                    }
+#pragma unroll
+                    for (int nt = 0; nt < N; ++nt) {
+                        x[nt][0] = ahead[nt][0];
+                        x[nt][1] = ahead[nt][1];
                     }
                 }
+#pragma unroll
+                for (int nt = 0; nt < N; ++nt)
+                    row[nt] += KW * 32;
             }
             // --- the sums of the warps that share the unit, and the result
             if (KW > 1) {
 #pragma unroll
-                for (int r = 0; r < TU; ++r)
+                for (int r = 0; r < 2; ++r)
 #pragma unroll
                     for (int nt = 0; nt < N; ++nt)
                         *reinterpret_cast<float4 *>(&s_sum[warp][r * N + nt][lane * 4]) =
@@ -463,14 +532,14 @@ __global__ void __launch_bounds__(32 * GW, 4) moe_gemm_kernel(const GemmParams p
                     continue;
                 if (KW > 1)
 #pragma unroll
-                    for (int r = 0; r < TU; ++r) {
+                    for (int r = 0; r < 2; ++r) {
                         acc[r][nt][0] = acc[r][nt][1] = acc[r][nt][2] = acc[r][nt][3] = 0.f;
                         for (int v = 0; v < KW; ++v) {
-                            const float4 x = *reinterpret_cast<const float4 *>(&s_sum[group * KW + v][r * N + nt][lane * 4]);
-                            acc[r][nt][0] += x.x;
-                            acc[r][nt][1] += x.y;
-                            acc[r][nt][2] += x.z;
-                            acc[r][nt][3] += x.w;
+                            const float4 y = *reinterpret_cast<const float4 *>(&s_sum[group * KW + v][r * N + nt][lane * 4]);
+                            acc[r][nt][0] += y.x;
+                            acc[r][nt][1] += y.y;
+                            acc[r][nt][2] += y.z;
+                            acc[r][nt][3] += y.w;
                         }
                     }
 #pragma unroll
@@ -484,14 +553,17 @@ __global__ void __launch_bounds__(32 * GW, 4) moe_gemm_kernel(const GemmParams p
                         uint16_t *dst = p.h + (int64_t)entry * p.rows_out + (blk >> 2) * 64 + (g >> 1) * 16 + (blk & 3) * 4 + (g & 1);
 #pragma unroll
                         for (int e8 = 0; e8 < 2; ++e8) {
-                            const float gate = acc[0][nt][2 * e8 + i] * 64.f, up = acc[TU - 1][nt][2 * e8 + i] * 64.f;
+                            const float gate = acc[0][nt][2 * e8 + i] * 64.f, up = acc[1][nt][2 * e8 + i] * 64.f;
                             const __nv_bfloat16 hb = __float2bfloat16_rn(gate / (1.f + __expf(-gate)) * up);
                             dst[2 * e8] = *reinterpret_cast<const uint16_t *>(&hb);
                         }
                     } else {
-                        float *dst = p.y + (int64_t)entry * p.rows_out + blk * 16 + g;
-                        dst[0] = acc[0][nt][i] * 64.f;
-                        dst[8] = acc[0][nt][2 + i] * 64.f;
+                        float *dst = p.y + (int64_t)entry * p.rows_out + blk * 32 + g;
+#pragma unroll
+                        for (int r = 0; r < 2; ++r) {
+                            dst[16 * r] = acc[r][nt][i] * 64.f;
+                            dst[16 * r + 8] = acc[r][nt][2 + i] * 64.f;
+                        }
                     }
                 }
             }
@@ -536,12 +608,14 @@ cudaError_t launch_gemm(GemmParams p, int sm_count, cudaStream_t stream)
 {
     const int KB = p.K / 256;
     p.KW = KB >= 8 ? 4 : (KB >= 2 ? 2 : 1);
+    p.sms = sm_count;
+    const bool few = p.entries <= 8 * p.topk;
     const int most = p.entries < p.experts ? p.entries : p.experts;
-    const long long ctas = ((long long)most * (p.rows_out / 16) * p.KW + GW - 1) / GW;
-    const long long grid = ctas < 4LL * sm_count ? ctas : 4LL * sm_count;
-    const size_t smem = (size_t)(p.entries + p.experts) * 4;
-    return launch_pdl(p.entries > 8 * p.topk ? moe_gemm_kernel<GATED, 2> : moe_gemm_kernel<GATED, 1>, dim3((unsigned)grid),
-                      dim3(32 * GW), smem, stream, p);
+    const long long ctas = ((long long)most * (p.rows_out / (GATED ? 16 : 32)) * p.KW + GW - 1) / GW;
+    const long long resident = (few ? 4LL : 3LL) * sm_count;
+    const size_t smem = (size_t)(p.entries + 2 * p.experts + 1) * 4;
+    return launch_pdl(few ? moe_gemm_kernel<GATED, 1> : moe_gemm_kernel<GATED, 2>,
+                      dim3((unsigned)(ctas < resident ? ctas : resident)), dim3(32 * GW), smem, stream, p);
 }
 
 struct Workspace {
@@ -600,9 +674,9 @@ cudaError_t launch_moe(const Moe &a, int sm_count, void *workspace, cudaStream_t
         return e;
 
     GemmParams up = {static_cast<const uint8_t *>(a.w13), xf, ids, h, nullptr, a.tokens * a.topk, a.topk, a.experts,
-                     a.hidden, a.inter, 1};
+                     a.hidden, a.inter, 1, 1};
     GemmParams down = {static_cast<const uint8_t *>(a.w2), h, ids, nullptr, y, a.tokens * a.topk, a.topk, a.experts,
-                       a.inter, a.hidden, 1};
+                       a.inter, a.hidden, 1, 1};
     e = launch_gemm<true>(up, sm_count, stream);
     if (e == cudaSuccess)
         e = launch_gemm<false>(down, sm_count, stream);
