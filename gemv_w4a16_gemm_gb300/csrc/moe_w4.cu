@@ -21,10 +21,13 @@
 // The two products.  A unit is a pair of 16-row tiles of an expert (for gate/up
 // the gate and the up tile of the same rows, for down two neighbours) times that
 // expert's tokens.  The line of all units of the active experts, weighted by
-// what their numbers of tokens cost, is cut into equal ranges, one per resident
-// CTA, those of an SM's CTAs side by side, so that an SM's L1 holds the rows of
-// one or two experts' tokens.  KW warps share a unit's K: each takes every KW-th
-// 256-column super-block, and they meet only to add their sums.  A tile goes
+// what their numbers of tokens cost, is cut into equal ranges, those of an SM's
+// warps side by side, so that an SM's L1 holds the rows of one or two experts'
+// tokens.  With much to do (STREAM) the line is cut at any 256-column super-block
+// into one range per warp; a unit that warps share is joined by the last of them
+// to finish, from the workspace and in the line's order.  With little to do the
+// cuts fall between units, and the KW warps of a group share a unit's K and join
+// in shared memory, which is sooner done.  A tile goes
 // from global memory to registers: a lane's 16-byte chunk of codes is four MMAs'
 // A fragments, its rows' scales and zero points are three more loads, and each
 // register is loaded again for the next super-block (of the next unit, too) as
@@ -71,6 +74,8 @@ struct RouteParams {
     int tokens, hidden, experts, topk;
     bool sigmoid, renormalize;
     float scale;
+    unsigned *counters;  // set to zero for the products
+    int counter_count;
 };
 
 __device__ __forceinline__ uint32_t order_key(float v)  // larger for larger v, at least 1; NaN is the least
@@ -131,6 +136,8 @@ __global__ void __launch_bounds__(32 * ROUTE_WARPS) moe_route_kernel(const Route
         dst[(g + 8) * 8 + 2 * t] = acc[2];
         dst[(g + 8) * 8 + 2 * t + 1] = acc[3];
     }
+    for (int i = blockIdx.x * 32 * ROUTE_WARPS + tid; i < p.counter_count; i += gridDim.x * 32 * ROUTE_WARPS)
+        p.counters[i] = 0;
     // x in fragment order: of 64 columns, lane t's pairs 16j + 2t and 16j + 8 + 2t, j = 0..3
     for (int i = rank * 32 * ROUTE_WARPS + tid; i < ROUTE_TOKENS * p.hidden / 16; i += ROUTE_CTAS * 32 * ROUTE_WARPS) {
         const int m = m0 + i / (p.hidden / 16), at = i % (p.hidden / 16);
@@ -238,6 +245,9 @@ __global__ void __launch_bounds__(32 * ROUTE_WARPS) moe_route_kernel(const Route
 // ------------------------------------------------------------ the products
 
 constexpr int GW = 4;  // warps of a CTA
+#ifndef W4Q_MOE_AHEAD
+#define W4Q_MOE_AHEAD 1
+#endif
 
 // bf16 pairs
 constexpr uint32_t BF_2P127 = 0x7F007F00u, BF_2P123 = 0x7D007D00u, NEG_2P127 = 0xFF00FF00u;
@@ -260,6 +270,8 @@ struct GemmParams {
     int rows_out;  // rows per expert of the result
     int KW;        // warps that share a unit's K
     int sms;
+    float *part;       // STREAM: [2 * warps][token groups][2][128], a warp's parts of the unit that it continues and of the one that it begins
+    unsigned *arrived; // STREAM: [warps], by the warp that begins the unit; zeroed by the route kernel
 };
 
 __device__ __forceinline__ uint4 ldg_weight(const uint8_t *p)
@@ -271,11 +283,26 @@ __device__ __forceinline__ uint4 ldg_weight(const uint8_t *p)
     return v;
 }
 
+// volatile: the compiler is not to move it down to its use
+__device__ __forceinline__ uint4 ldg_row(const uint4 *p)
+{
+    uint4 v;
+    asm volatile("ld.global.nc.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "l"(p));
+    return v;
+}
+
 // A lane's part of a pair of tiles: the four sub-blocks' codes, the bf16 scale
 // pairs of rows g, g + 8 for the 8 groups, and their zero points.
 struct Pair {
     uint4 q[2][4], s[2][2], z[2];
 };
+
+__device__ __forceinline__ void prefetch_tile(const uint8_t *p)
+{
+    asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(p), "n"(TILE_BYTES) : "memory");
+}
 
 template <int V>
 struct Count {
@@ -327,12 +354,12 @@ __device__ __forceinline__ int unit_cost(int n, int nt)
 }
 
 // NT groups of 8 tokens at a time, at most.
-template <bool GATED, int NT>
+template <bool GATED, int NT, bool STREAM>
 __global__ void __launch_bounds__(32 * GW, NT > 1 ? 3 : 4) moe_gemm_kernel(const GemmParams p)
 {
-    extern __shared__ __align__(16) int s_ids[];  // [entries], then [experts]: active experts, costs before them
-    int *s_active = s_ids + p.entries, *s_before = s_active + p.experts;
-    __shared__ __align__(16) float s_sum[GW][2 * NT][128];
+    extern __shared__ __align__(16) long long s_before[];  // [experts + 1]: what the steps before an active expert cost
+    int *s_active = reinterpret_cast<int *>(s_before + p.experts + 1), *s_ids = s_active + p.experts;  // [experts], [entries]
+    __shared__ __align__(16) float s_sum[STREAM ? 1 : GW][2 * NT][128];
     __shared__ int s_tokens[MAX_EXPERTS];
     __shared__ int s_count;
     __shared__ int s_list[GW][MAX_TOKENS];  // a warp's tokens: entries of its expert
@@ -351,15 +378,16 @@ __global__ void __launch_bounds__(32 * GW, NT > 1 ? 3 : 4) moe_gemm_kernel(const
     __syncthreads();
     const int KB = p.K / 256, blocks = p.rows_out / (GATED ? 16 : 32);
     if (warp == 0) {  // the active experts in order, and the cost of the units before each
-        int count = 0, cost = 0;
+        int count = 0;
+        long long cost = 0;
         for (int e0 = 0; e0 < p.experts; e0 += 32) {
             const int n = e0 + lane < p.experts ? s_tokens[e0 + lane] : 0;
             const uint32_t m = __ballot_sync(~0u, n > 0);
-            const int c = n > 0 ? unit_cost(n, NT) * blocks : 0;
-            int x = c;
+            const long long c = n > 0 ? (long long)unit_cost(n, NT) * blocks * KB : 0;
+            long long x = c;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
-                const int y = __shfl_up_sync(~0u, x, o);
+                const long long y = __shfl_up_sync(~0u, x, o);
                 if (lane >= o)
                     x += y;
             }
@@ -373,33 +401,46 @@ __global__ void __launch_bounds__(32 * GW, NT > 1 ? 3 : 4) moe_gemm_kernel(const
         }
         if (lane == 0) {
             s_count = count;
-            s_before[count] = cost;  // [experts] + 1
+            s_before[count] = cost;
         }
     }
     __syncthreads();
 
-    const int KW = p.KW, kw = warp & (KW - 1), group = warp / KW, groups = GW / KW;
+    const int KW = STREAM ? 1 : p.KW, kw = warp & (KW - 1), group = warp / KW, groups = GW / KW;
     // CTAs c, c + sms, c + 2 sms .. share an SM, as far as the hardware deals them out in turn
     const int per_sm = (gridDim.x + p.sms - 1) / p.sms;
     const int place = gridDim.x % p.sms == 0 ? (blockIdx.x % p.sms) * per_sm + blockIdx.x / p.sms : blockIdx.x;
-    const int ranges = gridDim.x * groups, mine = place * groups + group;
-    auto unit_after = [&](int cut) -> int {  // the first unit at or past the cost cut / ranges of the whole
-        const int count = s_count;
-        const long long at = (long long)s_before[count] * cut / ranges;
+    const int count = s_count, mine = place * groups + group;
+    const long long total = s_before[count];
+    int ranges = gridDim.x * groups;
+    if constexpr (STREAM)  // no range is shorter than a step, which costs at most unit_cost(MAX_TOKENS)
+        ranges = (int)min((long long)ranges, max(1ll, total / (5 * MAX_TOKENS / 16 + 1)));
+    if (mine >= ranges)
+        return;
+    auto expert_at = [&](long long cost) -> int {  // the last one with before <= cost
         int lo = 0, hi = count;
         while (hi - lo > 1) {
             const int mid = (lo + hi) >> 1;
-            if (s_before[mid] <= at)
+            if (s_before[mid] <= cost)
                 lo = mid;
             else
                 hi = mid;
         }
-        const int each = (s_before[lo + 1] - s_before[lo]) / blocks;
-        return lo * blocks + min(blocks, (int)((at - s_before[lo] + each - 1) / each));
+        return lo;
     };
-    const int first = unit_after(mine), last = unit_after(mine + 1);
-    if (first >= last)
+    // the first step (STREAM) or unit that begins at or past that share of the whole cost
+    auto cut_at = [&](int cut) -> int {
+        const int items = STREAM ? blocks * KB : blocks;
+        const long long at = total * cut / ranges;
+        const int a = expert_at(at);
+        const int each = (int)((s_before[a + 1] - s_before[a]) / items);
+        return a * items + min(items, (int)((at - s_before[a] + each - 1) / each));
+    };
+    const int from = cut_at(mine), to = cut_at(mine + 1);
+    if (from >= to)
         return;  // the whole group, which has a barrier of its own
+    const int first = STREAM ? (unsigned)from / (unsigned)KB : from, last = STREAM ? (unsigned)(to + KB - 1) / (unsigned)KB : to;
+    const int begin = STREAM ? from - first * KB : kw;  // the first unit's first super-block
     const uint8_t *codes = p.packed + 16 * lane, *scales = p.packed + 2048 + 16 * g;
 
     // Where unit u's first tile of this warp's first super-block lies, in 16 bytes (32 bits reach 64
@@ -420,7 +461,7 @@ __global__ void __launch_bounds__(32 * GW, NT > 1 ? 3 : 4) moe_gemm_kernel(const
         w.s[r][half] = ldg_weight(scales + (uint64_t)(at + r * second) * 16 + 128 * half);
     };
     auto load_zeros = [&](uint32_t at, int r) { w.z[r] = ldg_weight(scales + (uint64_t)(at + r * second) * 16 + 256); };
-    uint32_t here = unit_at(first), there;
+    uint32_t here = unit_at(first) + (STREAM ? begin * NEXT_SB : 0), there;
 #pragma unroll
     for (int r = 0; r < 2; ++r) {
         load_zeros(here, r);
@@ -435,9 +476,66 @@ __global__ void __launch_bounds__(32 * GW, NT > 1 ? 3 : 4) moe_gemm_kernel(const
     for (int r = 0; r < 2; ++r)
         load_scales(here, r, 1);
 
+    // The warp's steps go to L2 AHEAD steps before they are loaded: a register's load has one step's
+    // time to arrive, which memory under load exceeds and L2 does not.
+    constexpr int AHEAD = W4Q_MOE_AHEAD;
+    int pu = first, pb = begin;
+    uint32_t pat = here;
+    auto prefetch = [&](bool issue) {
+        if (pu >= last)
+            return;
+        if (issue && lane < 2)
+            prefetch_tile(p.packed + (uint64_t)(pat + lane * second) * 16);
+        pb += KW;
+        pat += KW * NEXT_SB;
+        if (pb >= (STREAM ? min(KB, to - pu * KB) : KB)) {
+            pb = kw;
+            if (++pu < last)
+                pat = unit_at(pu);
+        }
+    };
+    prefetch(false);
+#pragma unroll 1
+    for (int i = 0; i < AHEAD; ++i)
+        prefetch(true);
+
+    auto part_of = [&](int range, bool begins) -> float * {
+        return p.part + (int64_t)(2 * range + (begins ? 1 : 0)) * ((p.entries / p.topk + 7) / 8) * 256;
+    };
+    // the result of a pair of tiles for the 8 tokens col0 .. of the warp's list of n
+    auto store = [&](const float (&v)[2][4], int col0, int n, int blk) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const int col = col0 + 2 * t + i;
+            if (col >= n)
+                continue;
+            const int entry = s_list[warp][col];
+            if constexpr (GATED) {
+                // rows g and g + 8 of the 16, in fragment order
+                uint16_t *dst = p.h + (int64_t)entry * p.rows_out + (blk >> 2) * 64 + (g >> 1) * 16 + (blk & 3) * 4 + (g & 1);
+#pragma unroll
+                for (int e8 = 0; e8 < 2; ++e8) {
+                    const float gate = v[0][2 * e8 + i] * 64.f, up = v[1][2 * e8 + i] * 64.f;
+                    const __nv_bfloat16 hb = __float2bfloat16_rn(gate / (1.f + __expf(-gate)) * up);
+                    dst[2 * e8] = *reinterpret_cast<const uint16_t *>(&hb);
+                }
+            } else {
+                float *dst = p.y + (int64_t)entry * p.rows_out + blk * 32 + g;
+#pragma unroll
+                for (int r = 0; r < 2; ++r) {
+                    dst[16 * r] = v[r][i] * 64.f;
+                    dst[16 * r + 8] = v[r][2 + i] * 64.f;
+                }
+            }
+        }
+    };
+
     int last_e = -1, n = 0;
     for (int u = first; u < last; ++u, here = there) {
         there = u + 1 < last ? unit_at(u + 1) : NONE;
+        const int b0 = STREAM ? (u == first ? begin : 0) : kw;
+        const int b1 = STREAM ? min(KB, to - u * KB) : KB;
+        const bool whole = !STREAM || (b0 == 0 && b1 == KB);
         const int e = s_active[(unsigned)u / (unsigned)blocks], blk = (unsigned)u % (unsigned)blocks;
         if (e != last_e) {
             n = 0;
@@ -460,7 +558,7 @@ __global__ void __launch_bounds__(32 * GW, NT > 1 ? 3 : 4) moe_gemm_kernel(const
             for (int nt = 0; nt < N; ++nt) {
                 const int entry = s_list[warp][min(n0 + nt * 8 + g, n - 1)];
                 row[nt] = reinterpret_cast<const uint4 *>(
-                    p.xf + (int64_t)(GATED ? (unsigned)entry / (unsigned)p.topk : entry) * p.K + kw * 256 + 16 * t);
+                    p.xf + (int64_t)(GATED ? (unsigned)entry / (unsigned)p.topk : entry) * p.K + b0 * 256 + 16 * t);
             }
             float acc[2][N][4];
 #pragma unroll
@@ -471,14 +569,16 @@ __global__ void __launch_bounds__(32 * GW, NT > 1 ? 3 : 4) moe_gemm_kernel(const
             uint4 x[N][2];
 #pragma unroll
             for (int nt = 0; nt < N; ++nt) {
-                x[nt][0] = __ldg(row[nt]);
-                x[nt][1] = __ldg(row[nt] + 1);
+                x[nt][0] = ldg_row(row[nt]);
+                x[nt][1] = ldg_row(row[nt] + 1);
             }
             uint32_t at = here;
-            for (int b = kw; b < KB; b += KW, at += KW * NEXT_SB) {
-                const bool more = b + KW < KB;
+            for (int b = b0; b < b1; b += KW, at += KW * NEXT_SB) {
+                const bool more = b + KW < b1;
                 const uint32_t next = more ? at + KW * NEXT_SB : again ? here : there;
                 const uint4 z[2] = {w.z[0], w.z[1]};
+                if (n0 == 0)
+                    prefetch(true);
                 if (next != NONE) {
                     load_zeros(next, 0);
                     load_zeros(next, 1);
@@ -492,8 +592,8 @@ __global__ void __launch_bounds__(32 * GW, NT > 1 ? 3 : 4) moe_gemm_kernel(const
                         ahead[nt][1] = x[nt][1];
                         if (sb < 3 || more) {
                             const uint4 *src = row[nt] + (sb < 3 ? 8 * (sb + 1) : KW * 32);
-                            ahead[nt][0] = __ldg(src);
-                            ahead[nt][1] = __ldg(src + 1);
+                            ahead[nt][0] = ldg_row(src);
+                            ahead[nt][1] = ldg_row(src + 1);
                         }
                     }
 #pragma unroll
@@ -517,12 +617,22 @@ __global__ void __launch_bounds__(32 * GW, NT > 1 ? 3 : 4) moe_gemm_kernel(const
                     row[nt] += KW * 32;
             }
             // --- the sums of the warps that share the unit, and the result
+            if (STREAM && !whole) {
+                float *part = part_of(mine, b0 == 0) + (n0 / 8) * 256 + lane * 4;
+#pragma unroll
+                for (int nt = 0; nt < N; ++nt)
+#pragma unroll
+                    for (int r = 0; r < 2; ++r)
+                        __stcg(reinterpret_cast<float4 *>(part + (nt * 2 + r) * 128),
+                               make_float4(acc[r][nt][0], acc[r][nt][1], acc[r][nt][2], acc[r][nt][3]));
+                return;
+            }
             if (KW > 1) {
 #pragma unroll
                 for (int r = 0; r < 2; ++r)
 #pragma unroll
                     for (int nt = 0; nt < N; ++nt)
-                        *reinterpret_cast<float4 *>(&s_sum[warp][r * N + nt][lane * 4]) =
+                        *reinterpret_cast<float4 *>(&s_sum[STREAM ? 0 : warp][r * N + nt][lane * 4]) =
                             make_float4(acc[r][nt][0], acc[r][nt][1], acc[r][nt][2], acc[r][nt][3]);
                 asm volatile("bar.sync %0, %1;" ::"r"(1 + group), "r"(32 * KW) : "memory");
             }
@@ -530,42 +640,22 @@ __global__ void __launch_bounds__(32 * GW, NT > 1 ? 3 : 4) moe_gemm_kernel(const
             for (int nt = 0; nt < N; ++nt) {
                 if ((nt & (KW - 1)) != kw)
                     continue;
-                if (KW > 1)
+                float v[2][4];
 #pragma unroll
-                    for (int r = 0; r < 2; ++r) {
-                        acc[r][nt][0] = acc[r][nt][1] = acc[r][nt][2] = acc[r][nt][3] = 0.f;
-                        for (int v = 0; v < KW; ++v) {
-                            const float4 y = *reinterpret_cast<const float4 *>(&s_sum[group * KW + v][r * N + nt][lane * 4]);
-                            acc[r][nt][0] += y.x;
-                            acc[r][nt][1] += y.y;
-                            acc[r][nt][2] += y.z;
-                            acc[r][nt][3] += y.w;
-                        }
-                    }
-#pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    const int col = n0 + nt * 8 + 2 * t + i;
-                    if (col >= n)
-                        continue;
-                    const int entry = s_list[warp][col];
-                    if constexpr (GATED) {
-                        // rows g and g + 8 of the 16, in fragment order
-                        uint16_t *dst = p.h + (int64_t)entry * p.rows_out + (blk >> 2) * 64 + (g >> 1) * 16 + (blk & 3) * 4 + (g & 1);
-#pragma unroll
-                        for (int e8 = 0; e8 < 2; ++e8) {
-                            const float gate = acc[0][nt][2 * e8 + i] * 64.f, up = acc[1][nt][2 * e8 + i] * 64.f;
-                            const __nv_bfloat16 hb = __float2bfloat16_rn(gate / (1.f + __expf(-gate)) * up);
-                            dst[2 * e8] = *reinterpret_cast<const uint16_t *>(&hb);
-                        }
-                    } else {
-                        float *dst = p.y + (int64_t)entry * p.rows_out + blk * 32 + g;
-#pragma unroll
-                        for (int r = 0; r < 2; ++r) {
-                            dst[16 * r] = acc[r][nt][i] * 64.f;
-                            dst[16 * r + 8] = acc[r][nt][2 + i] * 64.f;
+                for (int r = 0; r < 2; ++r) {
+                    v[r][0] = acc[r][nt][0], v[r][1] = acc[r][nt][1], v[r][2] = acc[r][nt][2], v[r][3] = acc[r][nt][3];
+                    if (KW > 1) {
+                        v[r][0] = v[r][1] = v[r][2] = v[r][3] = 0.f;
+                        for (int q = 0; q < KW; ++q) {
+                            const float4 y = *reinterpret_cast<const float4 *>(&s_sum[STREAM ? 0 : group * KW + q][r * N + nt][lane * 4]);
+                            v[r][0] += y.x;
+                            v[r][1] += y.y;
+                            v[r][2] += y.z;
+                            v[r][3] += y.w;
                         }
                     }
                 }
+                store(v, n0 + nt * 8, n, blk);
             }
             if (KW > 1)  // the sums are read
                 asm volatile("bar.sync %0, %1;" ::"r"(1 + group), "r"(32 * KW) : "memory");
@@ -576,6 +666,41 @@ __global__ void __launch_bounds__(32 * GW, NT > 1 ? 3 : 4) moe_gemm_kernel(const
                 pass(Count<2>(), n0);
         for (; n0 < n; n0 += 8)
             pass(Count<1>(), n0);
+
+        if (STREAM && !whole) {
+            // the warps that hold the unit's first and last step: step x is in the last range whose
+            // share of the cost, rounded down, is at most what the steps before x cost
+            const int a = (unsigned)u / (unsigned)blocks;
+            const long long each = (s_before[a + 1] - s_before[a]) / ((long long)blocks * KB);
+            const long long cost0 = s_before[a] + (long long)blk * KB * each, cost1 = cost0 + (KB - 1) * each;
+            const int w0 = (int)(((cost0 + 1) * ranges - 1) / total), w1 = (int)(((cost1 + 1) * ranges - 1) / total);
+            __syncwarp();
+            unsigned before = 0;
+            if (lane == 0) {
+                __threadfence();
+                before = atomic_add_acq_rel(p.arrived + w0, 1u);
+                __threadfence();
+            }
+            before = __shfl_sync(~0u, before, 0);
+            __syncwarp();
+            if (before == (unsigned)(w1 - w0)) {
+                for (int c = 0; c < n; c += 8) {
+                    float v[2][4] = {};
+                    for (int q = w0; q <= w1; ++q) {
+                        const float *part = part_of(q, q == w0) + (c / 8) * 256 + lane * 4;
+#pragma unroll
+                        for (int r = 0; r < 2; ++r) {
+                            const float4 y = __ldcg(reinterpret_cast<const float4 *>(part + r * 128));
+                            v[r][0] += y.x;
+                            v[r][1] += y.y;
+                            v[r][2] += y.z;
+                            v[r][3] += y.w;
+                        }
+                    }
+                    store(v, c, n, blk);
+                }
+            }
+        }
     }
 }
 
@@ -606,22 +731,24 @@ __global__ void __launch_bounds__(128) moe_combine_kernel(const float *y, const 
 template <bool GATED>
 cudaError_t launch_gemm(GemmParams p, int sm_count, cudaStream_t stream)
 {
-    const int KB = p.K / 256;
-    p.KW = KB >= 8 ? 4 : (KB >= 2 ? 2 : 1);
-    p.sms = sm_count;
     const bool few = p.entries <= 8 * p.topk;
-    const int most = p.entries < p.experts ? p.entries : p.experts;
-    const long long ctas = ((long long)most * (p.rows_out / (GATED ? 16 : 32)) * p.KW + GW - 1) / GW;
-    const long long resident = (few ? 4LL : 3LL) * sm_count;
-    const size_t smem = (size_t)(p.entries + 2 * p.experts + 1) * 4;
-    return launch_pdl(few ? moe_gemm_kernel<GATED, 1> : moe_gemm_kernel<GATED, 2>,
-                      dim3((unsigned)(ctas < resident ? ctas : resident)), dim3(32 * GW), smem, stream, p);
+    const int KB = p.K / 256, most = p.entries < p.experts ? p.entries : p.experts;
+    const long long units = (long long)most * (p.rows_out / (GATED ? 16 : 32)), resident = (few ? 4LL : 3LL) * sm_count;
+    const bool stream_k = units * KB >= 8 * GW * resident;  // steps a warp, if every expert that can be active is
+    p.KW = stream_k ? 1 : KB >= 8 ? 4 : (KB >= 2 ? 2 : 1);
+    p.sms = sm_count;
+    const long long ctas = stream_k ? resident : (units * p.KW + GW - 1) / GW;
+    const size_t smem = (size_t)(p.experts + 1) * 8 + (size_t)(p.entries + p.experts) * 4;
+    auto fn = few ? (stream_k ? moe_gemm_kernel<GATED, 1, true> : moe_gemm_kernel<GATED, 1, false>)
+                  : (stream_k ? moe_gemm_kernel<GATED, 2, true> : moe_gemm_kernel<GATED, 2, false>);
+    return launch_pdl(fn, dim3((unsigned)(ctas < resident ? ctas : resident)), dim3(32 * GW), smem, stream, p);
 }
 
 struct Workspace {
-    size_t xf, h, y, ids, weights, bytes;
+    size_t xf, h, y, ids, weights, part, arrived, bytes;
+    int warps;
 };
-Workspace layout(int tokens, int hidden, int inter, int topk)
+Workspace layout(int tokens, int hidden, int inter, int topk, int sm_count)
 {
     Workspace w;
     size_t at = 0;
@@ -635,28 +762,33 @@ Workspace layout(int tokens, int hidden, int inter, int topk)
     w.y = take((size_t)tokens * topk * hidden * 4);
     w.ids = take((size_t)tokens * topk * 4);
     w.weights = take((size_t)tokens * topk * 4);
+    w.warps = 4 * GW * sm_count;
+    w.part = take((size_t)2 * w.warps * ((tokens + 7) / 8) * 256 * 4);
+    w.arrived = take((size_t)2 * w.warps * 4);  // of either product
     w.bytes = at;
     return w;
 }
 
 }  // namespace
 
-size_t moe_workspace(int tokens, int hidden, int inter, int topk)
+size_t moe_workspace(int tokens, int hidden, int inter, int topk, int sm_count)
 {
-    return layout(tokens, hidden, inter, topk).bytes;
+    return layout(tokens, hidden, inter, topk, sm_count).bytes;
 }
 
 cudaError_t launch_moe(const Moe &a, int sm_count, void *workspace, cudaStream_t stream)
 {
-    const Workspace w = layout(a.tokens, a.hidden, a.inter, a.topk);
+    const Workspace w = layout(a.tokens, a.hidden, a.inter, a.topk, sm_count);
     char *base = static_cast<char *>(workspace);
     uint16_t *xf = reinterpret_cast<uint16_t *>(base + w.xf), *h = reinterpret_cast<uint16_t *>(base + w.h);
     float *y = reinterpret_cast<float *>(base + w.y), *weights = reinterpret_cast<float *>(base + w.weights);
     int32_t *ids = reinterpret_cast<int32_t *>(base + w.ids);
+    float *part = reinterpret_cast<float *>(base + w.part);
+    unsigned *arrived = reinterpret_cast<unsigned *>(base + w.arrived);
 
     RouteParams r = {static_cast<const __nv_bfloat16 *>(a.x), static_cast<const __nv_bfloat16 *>(a.router), a.bias, xf,
                      ids, weights, a.ids_out, a.weights_out, a.tokens, a.hidden, a.experts, a.topk, a.sigmoid,
-                     a.renormalize, a.scale};
+                     a.renormalize, a.scale, arrived, 2 * w.warps};
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)((a.tokens + ROUTE_TOKENS - 1) / ROUTE_TOKENS * ROUTE_CTAS));
     cfg.blockDim = dim3(32 * ROUTE_WARPS);
@@ -674,9 +806,9 @@ cudaError_t launch_moe(const Moe &a, int sm_count, void *workspace, cudaStream_t
         return e;
 
     GemmParams up = {static_cast<const uint8_t *>(a.w13), xf, ids, h, nullptr, a.tokens * a.topk, a.topk, a.experts,
-                     a.hidden, a.inter, 1, 1};
+                     a.hidden, a.inter, 1, 1, part, arrived};
     GemmParams down = {static_cast<const uint8_t *>(a.w2), h, ids, nullptr, y, a.tokens * a.topk, a.topk, a.experts,
-                       a.inter, a.hidden, 1, 1};
+                       a.inter, a.hidden, 1, 1, part, arrived + w.warps};
     e = launch_gemm<true>(up, sm_count, stream);
     if (e == cudaSuccess)
         e = launch_gemm<false>(down, sm_count, stream);
