@@ -10,10 +10,12 @@
 // depth of dependent loads count as much.
 //
 // Four launches, each started while its predecessor finishes:
-//   route    one cluster of 8 CTAs per 8 tokens: the logits as m16n8k16 MMAs
-//            (bf16 products, fp32 sums) split over the cluster's 64 warps by
-//            experts and K, joined in the first CTA's shared memory, and the
-//            choice there; x is written in the order of the MMA fragments.
+//   route    one cluster of 8 CTAs: the logits as m16n8k16 MMAs (bf16 products,
+//            fp32 sums) split over the cluster's 64 warps by experts and K;
+//            CTA r joins those of tokens 8r .. 8r + 7 in its shared memory and
+//            chooses, a warp a token; the first CTA sorts the choices by expert
+//            for the products.  Other clusters meanwhile write x in the order
+//            of the MMA fragments.
 //   gate/up  h = silu(gate) * up for every (token, chosen expert)
 //   down     y = W2 h, fp32
 //   combine  out = sum of weight * y, in the order of choice
@@ -62,12 +64,23 @@ constexpr int MAX_EXPERTS = 512, MAX_TOKENS = 64;
 // ------------------------------------------------------------------- route
 
 constexpr int ROUTE_CTAS = 8, ROUTE_WARPS = 8, ROUTE_TOKENS = 8;
+constexpr int MAX_ENTRIES = MAX_TOKENS * 16;
+
+// What the products need of the choice: the active experts in order, each with
+// its entries (token * topk + place, in order) and what the units before it cost.
+struct Plan {
+    int count, pad[3];
+    int expert[MAX_EXPERTS];
+    int before[MAX_EXPERTS + 4];  // [count + 1]
+    int offset[MAX_EXPERTS + 4];  // [count + 1], into entries
+    int entries[MAX_ENTRIES];
+};
 
 struct RouteParams {
     const __nv_bfloat16 *x, *router;
     const float *bias;
     uint16_t *xf;      // [tokens][hidden] in fragment order
-    int32_t *ids;      // [tokens][topk]
+    Plan *plan;
     float *weights;    // [tokens][topk]
     int32_t *ids_out;  // the caller's, or null
     float *weights_out;
@@ -78,6 +91,15 @@ struct RouteParams {
     int counter_count;
 };
 
+// What a super-block of a unit of an expert with n tokens costs, in quarters of
+// one with up to 8: one pass over its tiles for every 16 tokens (with more than
+// 8 tokens in all), or 8.
+__device__ __forceinline__ int step_cost(int n, bool sixteens)
+{
+    const int full = sixteens ? (n + 7) / 16 : 0, left = n - 16 * full;
+    return 5 * full + (left > 0 ? (left + 7) / 8 * 4 : 0);
+}
+
 __device__ __forceinline__ uint32_t order_key(float v)  // larger for larger v, at least 1; NaN is the least
 {
     const uint32_t b = __float_as_uint(v);
@@ -85,160 +107,224 @@ __device__ __forceinline__ uint32_t order_key(float v)  // larger for larger v, 
     return v != v ? 1u : max(k, 1u);
 }
 
+// TT groups of 8 tokens, up to 32 PER experts.
+template <int TT, int PER>
 __global__ void __launch_bounds__(32 * ROUTE_WARPS) moe_route_kernel(const RouteParams p)
 {
-    // partial logits of the cluster's warps, in the first CTA: [slice][expert][token]
-    __shared__ float s_part[ROUTE_CTAS * ROUTE_WARPS * 16 * ROUTE_TOKENS];
-    __shared__ float s_logit[ROUTE_TOKENS][MAX_EXPERTS];
-    cg::cluster_group cluster = cg::this_cluster();
-    const int rank = (int)cluster.block_rank();
+    // the cluster's warps' parts of this CTA's tokens' logits: [slice][16 experts' tile][token][expert]
+    __shared__ float s_part[ROUTE_CTAS * ROUTE_WARPS][ROUTE_TOKENS * 16];
+    __shared__ uint16_t s_ids[MAX_ENTRIES];            // the first CTA's: all choices
+    __shared__ uint32_t s_mask[32 * PER][2];           // the tokens of an expert
+    __shared__ uint16_t s_offset[32 * PER];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
-    const int m0 = (blockIdx.x / ROUTE_CTAS) * ROUTE_TOKENS;
-    cluster.sync();  // the first CTA runs before anything is written to its shared memory
+
+    if (blockIdx.x >= ROUTE_CTAS) {
+        pdl_wait();
+        pdl_launch_dependents();
+        const int me = (blockIdx.x - ROUTE_CTAS) * 32 * ROUTE_WARPS + tid, all = (gridDim.x - ROUTE_CTAS) * 32 * ROUTE_WARPS;
+        for (int i = me; i < p.counter_count; i += all)
+            p.counters[i] = 0;
+        // x in fragment order: of 64 columns, lane t's pairs 16j + 2t and 16j + 8 + 2t, j = 0..3
+        const int per = p.hidden / 16;
+        for (int i = me; i < p.tokens * per; i += all) {
+            const int m = i / per, at = i - m * per;
+            const uint32_t *src = reinterpret_cast<const uint32_t *>(p.x + (int64_t)m * p.hidden) + (at / 4) * 32 + at % 4;
+            uint32_t w[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                w[j] = __ldg(src + 4 * j);
+            uint4 *dst = reinterpret_cast<uint4 *>(p.xf + (int64_t)m * p.hidden) + 2 * at;
+            dst[0] = make_uint4(w[0], w[1], w[2], w[3]);
+            dst[1] = make_uint4(w[4], w[5], w[6], w[7]);
+        }
+        return;
+    }
+
+    cg::cluster_group cluster = cg::this_cluster();
+    const int rank = blockIdx.x;
+    for (int i = tid; i < 64 * PER; i += 32 * ROUTE_WARPS)
+        s_mask[i / 2][i % 2] = 0;
+    cluster.sync();  // every CTA runs before anything is written to its shared memory
     pdl_wait();
     pdl_launch_dependents();
 
     const int mt = (p.experts + 15) / 16;
     const int slices = ROUTE_CTAS * ROUTE_WARPS / mt;
     const int gw = rank * ROUTE_WARPS + warp;
-    const int tile = gw % mt, slice = gw / mt;
+    const int slice = gw / mt, tile = gw - slice * mt;
     if (slice < slices) {
         const int chunks = p.hidden / 32;
         const int c0 = chunks * slice / slices, c1 = chunks * (slice + 1) / slices;
-        const int e0 = tile * 16 + g, e1 = e0 + 8, m = m0 + g;
-        const uint4 zero = make_uint4(0, 0, 0, 0);
+        // rows past the last are its copies: their logits are not read
+        const int e0 = min(tile * 16 + g, p.experts - 1), e1 = min(tile * 16 + 8 + g, p.experts - 1);
         const uint4 *ra = reinterpret_cast<const uint4 *>(p.router + (int64_t)e0 * p.hidden) + t;
         const uint4 *rb = reinterpret_cast<const uint4 *>(p.router + (int64_t)e1 * p.hidden) + t;
-        const uint4 *rx = reinterpret_cast<const uint4 *>(p.x + (int64_t)m * p.hidden) + t;
-        const bool ha = e0 < p.experts, hb = e1 < p.experts, hx = m < p.tokens;
-        float acc[4] = {0.f, 0.f, 0.f, 0.f};
-        constexpr int U = 4;
+        const uint4 *rx[TT];
+        float acc[TT][4];
+#pragma unroll
+        for (int n = 0; n < TT; ++n) {
+            rx[n] = reinterpret_cast<const uint4 *>(p.x + (int64_t)min(n * 8 + g, p.tokens - 1) * p.hidden) + t;
+            acc[n][0] = acc[n][1] = acc[n][2] = acc[n][3] = 0.f;
+        }
+        constexpr int U = TT == 1 ? 8 : (TT == 8 ? 2 : 4);  // chunks whose loads go out together
         for (int c = c0; c < c1; c += U) {
-            uint4 a[U], b[U], x[U];
+            uint4 a[U], b[U], x[U][TT];
 #pragma unroll
             for (int i = 0; i < U; ++i) {
-                const bool in = c + i < c1;
-                a[i] = in && ha ? __ldg(ra + 4 * (c + i)) : zero;
-                b[i] = in && hb ? __ldg(rb + 4 * (c + i)) : zero;
-                x[i] = in && hx ? __ldg(rx + 4 * (c + i)) : zero;
+                const int at = 4 * min(c + i, c1 - 1);
+                a[i] = __ldg(ra + at);
+                b[i] = __ldg(rb + at);
+#pragma unroll
+                for (int n = 0; n < TT; ++n)
+                    x[i][n] = __ldg(rx[n] + at);
             }
 #pragma unroll
-            for (int i = 0; i < U; ++i) {
-                const uint32_t f0[4] = {a[i].x, b[i].x, a[i].y, b[i].y};
-                const uint32_t f1[4] = {a[i].z, b[i].z, a[i].w, b[i].w};
-                mma_bf16(acc, f0, x[i].x, x[i].y, acc);
-                mma_bf16(acc, f1, x[i].z, x[i].w, acc);
+            for (int i = 0; i < U; ++i)
+                if (c + i < c1) {
+                    const uint32_t f0[4] = {a[i].x, b[i].x, a[i].y, b[i].y};
+                    const uint32_t f1[4] = {a[i].z, b[i].z, a[i].w, b[i].w};
+#pragma unroll
+                    for (int n = 0; n < TT; ++n) {
+                        mma_bf16(acc[n], f0, x[i][n].x, x[i][n].y, acc[n]);
+                        mma_bf16(acc[n], f1, x[i][n].z, x[i][n].w, acc[n]);
+                    }
+                }
+        }
+#pragma unroll
+        for (int n = 0; n < TT; ++n) {
+            float *dst = cluster.map_shared_rank(&s_part[gw][0], n);
+            dst[(2 * t) * 16 + g] = acc[n][0];
+            dst[(2 * t + 1) * 16 + g] = acc[n][1];
+            dst[(2 * t) * 16 + 8 + g] = acc[n][2];
+            dst[(2 * t + 1) * 16 + 8 + g] = acc[n][3];
+        }
+    }
+    cluster.sync();
+    const int m = rank * ROUTE_TOKENS + warp;  // one warp per token
+    if (m < p.tokens) {
+        float score[PER];
+        uint32_t key[PER];
+        float top = -INFINITY, sum = 0.f;
+#pragma unroll
+        for (int i = 0; i < PER; ++i) {
+            const int e = 32 * i + lane;
+            score[i] = -INFINITY;
+            key[i] = 0u;
+            if (e < p.experts) {
+                float v = 0.f;
+#pragma unroll 8
+                for (int s = 0; s < slices; ++s)
+                    v += s_part[s * mt + e / 16][warp * 16 + e % 16];
+                score[i] = v;
+                key[i] = order_key(v);
+                top = fmaxf(top, v);
             }
         }
-        float *dst = cluster.map_shared_rank(s_part, 0) + gw * 128;
-        dst[g * 8 + 2 * t] = acc[0];
-        dst[g * 8 + 2 * t + 1] = acc[1];
-        dst[(g + 8) * 8 + 2 * t] = acc[2];
-        dst[(g + 8) * 8 + 2 * t + 1] = acc[3];
-    }
-    for (int i = blockIdx.x * 32 * ROUTE_WARPS + tid; i < p.counter_count; i += gridDim.x * 32 * ROUTE_WARPS)
-        p.counters[i] = 0;
-    // x in fragment order: of 64 columns, lane t's pairs 16j + 2t and 16j + 8 + 2t, j = 0..3
-    for (int i = rank * 32 * ROUTE_WARPS + tid; i < ROUTE_TOKENS * p.hidden / 16; i += ROUTE_CTAS * 32 * ROUTE_WARPS) {
-        const int m = m0 + i / (p.hidden / 16), at = i % (p.hidden / 16);
-        if (m < p.tokens) {
-            const uint32_t *src = reinterpret_cast<const uint32_t *>(p.x + (int64_t)m * p.hidden) + (at / 4) * 32 + at % 4;
-            uint32_t w[8];
+        if (p.sigmoid) {
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                w[2 * j] = __ldg(src + 8 * j);
-                w[2 * j + 1] = __ldg(src + 8 * j + 4);
+            for (int i = 0; i < PER; ++i) {
+                const int e = 32 * i + lane;
+                if (e < p.experts) {
+                    score[i] = 1.f / (1.f + expf(-score[i]));
+                    key[i] = order_key(score[i] + (p.bias ? __ldg(p.bias + e) : 0.f));
+                }
             }
-            uint4 *dst = reinterpret_cast<uint4 *>(p.xf + (int64_t)m * p.hidden) + 2 * at;
-            dst[0] = make_uint4(w[0], w[1], w[2], w[3]);
-            dst[1] = make_uint4(w[4], w[5], w[6], w[7]);
+        } else {
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1)
+                top = fmaxf(top, __shfl_xor_sync(~0u, top, o));
+#pragma unroll
+            for (int i = 0; i < PER; ++i) {
+                score[i] = 32 * i + lane < p.experts ? expf(score[i] - top) : 0.f;
+                sum += score[i];
+            }
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1)
+                sum += __shfl_xor_sync(~0u, sum, o);
+        }
+        float mine = 0.f, chosen = 0.f;  // lane k: the k-th chosen score
+        int id = 0;
+        for (int k = 0; k < p.topk; ++k) {
+            uint32_t best = 0;
+#pragma unroll
+            for (int i = 0; i < PER; ++i)
+                best = max(best, key[i]);
+            best = __reduce_max_sync(~0u, best);
+            uint32_t at = ~0u;
+#pragma unroll
+            for (int i = PER - 1; i >= 0; --i)
+                if (key[i] == best)
+                    at = 32 * i + lane;
+            at = __reduce_min_sync(~0u, at);
+            float v = 0.f;
+#pragma unroll
+            for (int i = 0; i < PER; ++i)
+                if (32 * i + lane == (int)at) {
+                    v = score[i];
+                    key[i] = 0;
+                }
+            v = __shfl_sync(~0u, v, at & 31);
+            chosen += v;
+            if (lane == k) {
+                mine = v;
+                id = (int)at;
+            }
+        }
+        if (lane < p.topk) {
+            const float all = p.renormalize ? chosen : (p.sigmoid ? 1.f : sum);
+            const float w = all > 0.f ? mine / all * p.scale : 0.f;
+            p.weights[m * p.topk + lane] = w;
+            cluster.map_shared_rank(s_ids, 0)[m * p.topk + lane] = (uint16_t)id;
+            atomicOr(cluster.map_shared_rank(&s_mask[0][0], 0) + 2 * id + (m >> 5), 1u << (m & 31));
+            if (p.ids_out)
+                p.ids_out[m * p.topk + lane] = id;
+            if (p.weights_out)
+                p.weights_out[m * p.topk + lane] = w;
         }
     }
     cluster.sync();
     if (rank != 0)
         return;
-    for (int i = tid; i < ROUTE_TOKENS * p.experts; i += 32 * ROUTE_WARPS) {
-        const int m = i % ROUTE_TOKENS, e = i / ROUTE_TOKENS;
-        float v = 0.f;
-        for (int s = 0; s < slices; ++s)
-            v += s_part[(s * mt + e / 16) * 128 + (e % 16) * 8 + m];
-        s_logit[m][e] = v;
+    // the choices by expert: an expert's tokens are bits of its mask
+    if (warp == 0) {
+        int count = 0, cost = 0, entries = 0;
+#pragma unroll
+        for (int i = 0; i < PER; ++i) {
+            const int e = 32 * i + lane, n = __popc(s_mask[e][0]) + __popc(s_mask[e][1]);
+            const uint32_t active = __ballot_sync(~0u, n > 0);
+            const int c = step_cost(n, p.tokens > 8);
+            int xc = c, xn = n;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int yc = __shfl_up_sync(~0u, xc, o), yn = __shfl_up_sync(~0u, xn, o);
+                if (lane >= o) {
+                    xc += yc;
+                    xn += yn;
+                }
+            }
+            s_offset[e] = (uint16_t)(entries + xn - n);
+            if (n > 0) {
+                const int at = count + __popc(active & ((1u << lane) - 1));
+                p.plan->expert[at] = e;
+                p.plan->before[at] = cost + xc - c;
+                p.plan->offset[at] = entries + xn - n;
+            }
+            count += __popc(active);
+            cost += __shfl_sync(~0u, xc, 31);
+            entries += __shfl_sync(~0u, xn, 31);
+        }
+        if (lane == 0) {
+            p.plan->count = count;
+            p.plan->before[count] = cost;
+            p.plan->offset[count] = entries;
+        }
     }
     __syncthreads();
-    // one warp per token
-    const int m = m0 + warp;
-    if (m >= p.tokens)
-        return;
-    constexpr int PER = MAX_EXPERTS / 32;
-    float score[PER];
-    uint32_t key[PER];
-    float top = -INFINITY, sum = 0.f;
-#pragma unroll
-    for (int i = 0; i < PER; ++i) {
-        const int e = 32 * i + lane;
-        score[i] = e < p.experts ? s_logit[warp][e] : -INFINITY;
-        key[i] = e < p.experts ? order_key(score[i]) : 0u;
-        top = fmaxf(top, score[i]);
-    }
-    if (p.sigmoid) {
-#pragma unroll
-        for (int i = 0; i < PER; ++i) {
-            const int e = 32 * i + lane;
-            if (e < p.experts) {
-                score[i] = 1.f / (1.f + expf(-score[i]));
-                key[i] = order_key(score[i] + (p.bias ? __ldg(p.bias + e) : 0.f));
-            }
-        }
-    } else {
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1)
-            top = fmaxf(top, __shfl_xor_sync(~0u, top, o));
-#pragma unroll
-        for (int i = 0; i < PER; ++i) {
-            score[i] = 32 * i + lane < p.experts ? expf(score[i] - top) : 0.f;
-            sum += score[i];
-        }
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1)
-            sum += __shfl_xor_sync(~0u, sum, o);
-    }
-    float mine = 0.f, chosen = 0.f;  // lane k: the k-th chosen score
-    int id = 0;
-    for (int k = 0; k < p.topk; ++k) {
-        uint32_t best = 0;
-#pragma unroll
-        for (int i = 0; i < PER; ++i)
-            best = max(best, key[i]);
-        best = __reduce_max_sync(~0u, best);
-        uint32_t at = ~0u;
-#pragma unroll
-        for (int i = PER - 1; i >= 0; --i)
-            if (key[i] == best)
-                at = 32 * i + lane;
-        at = __reduce_min_sync(~0u, at);
-        float v = 0.f;
-#pragma unroll
-        for (int i = 0; i < PER; ++i)
-            if (32 * i + lane == (int)at) {
-                v = score[i];
-                key[i] = 0;
-            }
-        v = __shfl_sync(~0u, v, at & 31);
-        chosen += v;
-        if (lane == k) {
-            mine = v;
-            id = (int)at;
-        }
-    }
-    if (lane < p.topk) {
-        const float all = p.renormalize ? chosen : (p.sigmoid ? 1.f : sum);
-        const float w = all > 0.f ? mine / all * p.scale : 0.f;
-        p.ids[m * p.topk + lane] = id;
-        p.weights[m * p.topk + lane] = w;
-        if (p.ids_out)
-            p.ids_out[m * p.topk + lane] = id;
-        if (p.weights_out)
-            p.weights_out[m * p.topk + lane] = w;
+    for (int i = tid; i < p.tokens * p.topk; i += 32 * ROUTE_WARPS) {
+        const int e = s_ids[i], mm = i / p.topk;
+        const uint32_t lo = s_mask[e][0], hi = s_mask[e][1], below = (1u << (mm & 31)) - 1;
+        const int before = mm < 32 ? __popc(lo & below) : __popc(lo) + __popc(hi & below);
+        p.plan->entries[s_offset[e] + before] = i;
     }
 }
 
@@ -262,7 +348,7 @@ __device__ __forceinline__ uint32_t bf16x2_fma(uint32_t a, uint32_t b, uint32_t 
 struct GemmParams {
     const uint8_t *packed;
     const uint16_t *xf;  // rows in fragment order
-    const int32_t *ids;  // [entries]
+    const Plan *plan;
     uint16_t *h;         // gate/up: [entries][rows_out] in fragment order
     float *y;            // down: [entries][rows_out]
     int entries, topk, experts;
@@ -345,96 +431,54 @@ __device__ __forceinline__ void tile_step(const uint4 &q, uint32_t s0, uint32_t 
     }
 }
 
-// What a unit of an expert with n tokens costs, in quarters of one with up to 8:
-// one pass over its tiles for every 16 tokens, or 8.
-__device__ __forceinline__ int unit_cost(int n, int nt)
-{
-    const int full = nt > 1 ? (n + 7) / 16 : 0, left = n - 16 * full;
-    return 5 * full + (left > 0 ? (left + 7) / 8 * 4 : 0);
-}
-
 // NT groups of 8 tokens at a time, at most.
 template <bool GATED, int NT, bool STREAM>
 __global__ void __launch_bounds__(32 * GW, NT > 1 ? 3 : 4) moe_gemm_kernel(const GemmParams p)
 {
-    extern __shared__ __align__(16) long long s_before[];  // [experts + 1]: what the steps before an active expert cost
-    int *s_active = reinterpret_cast<int *>(s_before + p.experts + 1), *s_ids = s_active + p.experts;  // [experts], [entries]
+    extern __shared__ int s_before[];  // [experts + 1] each: costs before, offsets, numbers of the active experts
+    int *s_offset = s_before + p.experts + 1, *s_expert = s_offset + p.experts + 1;
     __shared__ __align__(16) float s_sum[STREAM ? 1 : GW][2 * NT][128];
-    __shared__ int s_tokens[MAX_EXPERTS];
-    __shared__ int s_count;
-    __shared__ int s_list[GW][MAX_TOKENS];  // a warp's tokens: entries of its expert
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
 
-    for (int i = tid; i < p.experts; i += 32 * GW)
-        s_tokens[i] = 0;
     pdl_wait();
     pdl_launch_dependents();
-    __syncthreads();
-    for (int i = tid; i < p.entries; i += 32 * GW) {
-        const int e = __ldg(p.ids + i);
-        s_ids[i] = e;
-        atomicAdd(&s_tokens[e], 1);
-    }
-    __syncthreads();
-    const int KB = p.K / 256, blocks = p.rows_out / (GATED ? 16 : 32);
-    if (warp == 0) {  // the active experts in order, and the cost of the units before each
-        int count = 0;
-        long long cost = 0;
-        for (int e0 = 0; e0 < p.experts; e0 += 32) {
-            const int n = e0 + lane < p.experts ? s_tokens[e0 + lane] : 0;
-            const uint32_t m = __ballot_sync(~0u, n > 0);
-            const long long c = n > 0 ? (long long)unit_cost(n, NT) * blocks * KB : 0;
-            long long x = c;
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const long long y = __shfl_up_sync(~0u, x, o);
-                if (lane >= o)
-                    x += y;
-            }
-            if (n > 0) {
-                const int at = count + __popc(m & ((1u << lane) - 1));
-                s_active[at] = e0 + lane;
-                s_before[at] = cost + x - c;
-            }
-            count += __popc(m);
-            cost += __shfl_sync(~0u, x, 31);
-        }
-        if (lane == 0) {
-            s_count = count;
-            s_before[count] = cost;
-        }
+    const int count = p.plan->count;
+    for (int i = tid; i < p.experts + 1; i += 32 * GW) {
+        s_before[i] = p.plan->before[i];
+        s_offset[i] = p.plan->offset[i];
+        s_expert[i] = i < p.experts ? p.plan->expert[i] : 0;
     }
     __syncthreads();
 
+    const int KB = p.K / 256, blocks = p.rows_out / (GATED ? 16 : 32);
     const int KW = STREAM ? 1 : p.KW, kw = warp & (KW - 1), group = warp / KW, groups = GW / KW;
     // CTAs c, c + sms, c + 2 sms .. share an SM, as far as the hardware deals them out in turn
     const int per_sm = (gridDim.x + p.sms - 1) / p.sms;
     const int place = gridDim.x % p.sms == 0 ? (blockIdx.x % p.sms) * per_sm + blockIdx.x / p.sms : blockIdx.x;
-    const int count = s_count, mine = place * groups + group;
-    const long long total = s_before[count];
-    int ranges = gridDim.x * groups;
-    if constexpr (STREAM)  // no range is shorter than a step, which costs at most unit_cost(MAX_TOKENS)
-        ranges = (int)min((long long)ranges, max(1ll, total / (5 * MAX_TOKENS / 16 + 1)));
-    if (mine >= ranges)
+    const int mine = place * groups + group, SB = blocks * KB;
+    // Share r of the whole cost ends at share * r + min(r, extra).  (At most 512 experts, 64 x 16
+    // choices, 2048 blocks and 128 super-blocks: less than 2^30.)
+    const unsigned total = (unsigned)s_before[count] * SB;
+    unsigned ranges = gridDim.x * groups;
+    if constexpr (STREAM)  // no range is shorter than a step, which costs at most 5 * 64 / 16
+        ranges = min(ranges, max(1u, total / (5 * MAX_TOKENS / 16 + 1)));
+    if (mine >= (int)ranges)
         return;
-    auto expert_at = [&](long long cost) -> int {  // the last one with before <= cost
+    const unsigned share = total / ranges, extra = total - share * ranges;
+    // the first step (STREAM) or unit that begins at or past that end
+    auto cut_at = [&](unsigned r) -> int {
+        const unsigned at = share * r + min(r, extra);
+        const int whole = (int)(at / (unsigned)SB);
         int lo = 0, hi = count;
         while (hi - lo > 1) {
             const int mid = (lo + hi) >> 1;
-            if (s_before[mid] <= cost)
+            if (s_before[mid] <= whole)
                 lo = mid;
             else
                 hi = mid;
         }
-        return lo;
-    };
-    // the first step (STREAM) or unit that begins at or past that share of the whole cost
-    auto cut_at = [&](int cut) -> int {
-        const int items = STREAM ? blocks * KB : blocks;
-        const long long at = total * cut / ranges;
-        const int a = expert_at(at);
-        const int each = (int)((s_before[a + 1] - s_before[a]) / items);
-        return a * items + min(items, (int)((at - s_before[a] + each - 1) / each));
+        const unsigned each = (s_before[lo + 1] - s_before[lo]) * (STREAM ? 1 : KB), items = STREAM ? SB : blocks;
+        return lo * items + min(items, (at - (unsigned)s_before[lo] * SB + each - 1) / each);
     };
     const int from = cut_at(mine), to = cut_at(mine + 1);
     if (from >= to)
@@ -448,11 +492,22 @@ __global__ void __launch_bounds__(32 * GW, NT > 1 ? 3 : 4) moe_gemm_kernel(const
     // super-block 8 tiles, from it.
     constexpr uint32_t TILE16 = TILE_BYTES / 16, NEXT_SB = 8 * TILE16, NONE = ~0u;
     const uint32_t second = GATED ? (uint32_t)(blocks >> 3) * KB * NEXT_SB : TILE16;
-    auto unit_at = [&](int u) -> uint32_t {
-        const int e = s_active[(unsigned)u / (unsigned)blocks], blk = (unsigned)u % (unsigned)blocks;
-        const int tl = e * 2 * blocks + (GATED ? blk : 2 * blk);
+    struct Cursor {
+        int a, blk;  // the unit: an active expert's block of rows
+    };
+    auto next_unit = [&](Cursor &c) {
+        if (++c.blk == blocks) {
+            c.blk = 0;
+            ++c.a;
+        }
+    };
+    auto unit_at = [&](Cursor c) -> uint32_t {
+        const int tl = s_expert[c.a] * 2 * blocks + (GATED ? c.blk : 2 * c.blk);
         return (uint32_t)(tl >> 3) * KB * NEXT_SB + (tl & 7) * TILE16 + kw * NEXT_SB;
     };
+    Cursor cur;
+    cur.a = (unsigned)first / (unsigned)blocks;
+    cur.blk = first - cur.a * blocks;
     Pair w;
     auto load_codes = [&](uint32_t at, int r, int sb) {
         w.q[r][sb] = ldg_weight(codes + (uint64_t)(at + r * second) * 16 + 512 * sb);
@@ -461,7 +516,7 @@ __global__ void __launch_bounds__(32 * GW, NT > 1 ? 3 : 4) moe_gemm_kernel(const
         w.s[r][half] = ldg_weight(scales + (uint64_t)(at + r * second) * 16 + 128 * half);
     };
     auto load_zeros = [&](uint32_t at, int r) { w.z[r] = ldg_weight(scales + (uint64_t)(at + r * second) * 16 + 256); };
-    uint32_t here = unit_at(first) + (STREAM ? begin * NEXT_SB : 0), there;
+    uint32_t here = unit_at(cur) + (STREAM ? begin * NEXT_SB : 0), there;
 #pragma unroll
     for (int r = 0; r < 2; ++r) {
         load_zeros(here, r);
@@ -481,6 +536,7 @@ __global__ void __launch_bounds__(32 * GW, NT > 1 ? 3 : 4) moe_gemm_kernel(const
     constexpr int AHEAD = W4Q_MOE_AHEAD;
     int pu = first, pb = begin;
     uint32_t pat = here;
+    Cursor pcur = cur;
     auto prefetch = [&](bool issue) {
         if (pu >= last)
             return;
@@ -490,8 +546,9 @@ __global__ void __launch_bounds__(32 * GW, NT > 1 ? 3 : 4) moe_gemm_kernel(const
         pat += KW * NEXT_SB;
         if (pb >= (STREAM ? min(KB, to - pu * KB) : KB)) {
             pb = kw;
+            next_unit(pcur);
             if (++pu < last)
-                pat = unit_at(pu);
+                pat = unit_at(pcur);
         }
     };
     prefetch(false);
@@ -503,13 +560,13 @@ __global__ void __launch_bounds__(32 * GW, NT > 1 ? 3 : 4) moe_gemm_kernel(const
         return p.part + (int64_t)(2 * range + (begins ? 1 : 0)) * ((p.entries / p.topk + 7) / 8) * 256;
     };
     // the result of a pair of tiles for the 8 tokens col0 .. of the warp's list of n
-    auto store = [&](const float (&v)[2][4], int col0, int n, int blk) {
+    auto store = [&](const float (&v)[2][4], int col0, const int *list, int n, int blk) {
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
             const int col = col0 + 2 * t + i;
             if (col >= n)
                 continue;
-            const int entry = s_list[warp][col];
+            const int entry = __ldg(list + col);
             if constexpr (GATED) {
                 // rows g and g + 8 of the 16, in fragment order
                 uint16_t *dst = p.h + (int64_t)entry * p.rows_out + (blk >> 2) * 64 + (g >> 1) * 16 + (blk & 3) * 4 + (g & 1);
@@ -530,25 +587,15 @@ __global__ void __launch_bounds__(32 * GW, NT > 1 ? 3 : 4) moe_gemm_kernel(const
         }
     };
 
-    int last_e = -1, n = 0;
-    for (int u = first; u < last; ++u, here = there) {
-        there = u + 1 < last ? unit_at(u + 1) : NONE;
+    for (int u = first; u < last; ++u, here = there, next_unit(cur)) {
+        Cursor after = cur;
+        next_unit(after);
+        there = u + 1 < last ? unit_at(after) : NONE;
         const int b0 = STREAM ? (u == first ? begin : 0) : kw;
         const int b1 = STREAM ? min(KB, to - u * KB) : KB;
         const bool whole = !STREAM || (b0 == 0 && b1 == KB);
-        const int e = s_active[(unsigned)u / (unsigned)blocks], blk = (unsigned)u % (unsigned)blocks;
-        if (e != last_e) {
-            n = 0;
-            for (int i0 = 0; i0 < p.entries; i0 += 32) {
-                const bool is = i0 + lane < p.entries && s_ids[i0 + lane] == e;
-                const uint32_t m = __ballot_sync(~0u, is);
-                if (is)
-                    s_list[warp][n + __popc(m & ((1u << lane) - 1))] = i0 + lane;
-                n += __popc(m);
-            }
-            __syncwarp();
-            last_e = e;
-        }
+        const int *list = p.plan->entries + s_offset[cur.a];
+        const int n = s_offset[cur.a + 1] - s_offset[cur.a];
         // an expert with more than 8 NT tokens takes several passes over its tiles
         auto pass = [&](auto groups_of_8, int n0) {
             constexpr int N = decltype(groups_of_8)::value;
@@ -556,7 +603,7 @@ __global__ void __launch_bounds__(32 * GW, NT > 1 ? 3 : 4) moe_gemm_kernel(const
             const uint4 *row[N];  // tokens past the last are its copies, and are not stored
 #pragma unroll
             for (int nt = 0; nt < N; ++nt) {
-                const int entry = s_list[warp][min(n0 + nt * 8 + g, n - 1)];
+                const int entry = __ldg(list + min(n0 + nt * 8 + g, n - 1));
                 row[nt] = reinterpret_cast<const uint4 *>(
                     p.xf + (int64_t)(GATED ? (unsigned)entry / (unsigned)p.topk : entry) * p.K + b0 * 256 + 16 * t);
             }
@@ -655,7 +702,7 @@ __global__ void __launch_bounds__(32 * GW, NT > 1 ? 3 : 4) moe_gemm_kernel(const
                         }
                     }
                 }
-                store(v, n0 + nt * 8, n, blk);
+                store(v, n0 + nt * 8, list, n, cur.blk);
             }
             if (KW > 1)  // the sums are read
                 asm volatile("bar.sync %0, %1;" ::"r"(1 + group), "r"(32 * KW) : "memory");
@@ -668,12 +715,15 @@ __global__ void __launch_bounds__(32 * GW, NT > 1 ? 3 : 4) moe_gemm_kernel(const
             pass(Count<1>(), n0);
 
         if (STREAM && !whole) {
-            // the warps that hold the unit's first and last step: step x is in the last range whose
-            // share of the cost, rounded down, is at most what the steps before x cost
-            const int a = (unsigned)u / (unsigned)blocks;
-            const long long each = (s_before[a + 1] - s_before[a]) / ((long long)blocks * KB);
-            const long long cost0 = s_before[a] + (long long)blk * KB * each, cost1 = cost0 + (KB - 1) * each;
-            const int w0 = (int)(((cost0 + 1) * ranges - 1) / total), w1 = (int)(((cost1 + 1) * ranges - 1) / total);
+            // the warps that hold the unit's first and last step: a step is in the last range whose
+            // beginning is at most what the steps before it cost
+            const unsigned each = s_before[cur.a + 1] - s_before[cur.a];
+            const unsigned cost0 = (unsigned)s_before[cur.a] * SB + (unsigned)cur.blk * KB * each, cost1 = cost0 + (KB - 1) * each;
+            auto owner = [&](unsigned cost) -> int {
+                const unsigned longer = (share + 1) * extra;
+                return cost < longer ? cost / (share + 1) : extra + (cost - longer) / share;
+            };
+            const int w0 = owner(cost0), w1 = owner(cost1);
             __syncwarp();
             unsigned before = 0;
             if (lane == 0) {
@@ -697,7 +747,7 @@ __global__ void __launch_bounds__(32 * GW, NT > 1 ? 3 : 4) moe_gemm_kernel(const
                             v[r][3] += y.w;
                         }
                     }
-                    store(v, c, n, blk);
+                    store(v, c, list, n, cur.blk);
                 }
             }
         }
@@ -738,14 +788,14 @@ cudaError_t launch_gemm(GemmParams p, int sm_count, cudaStream_t stream)
     p.KW = stream_k ? 1 : KB >= 8 ? 4 : (KB >= 2 ? 2 : 1);
     p.sms = sm_count;
     const long long ctas = stream_k ? resident : (units * p.KW + GW - 1) / GW;
-    const size_t smem = (size_t)(p.experts + 1) * 8 + (size_t)(p.entries + p.experts) * 4;
+    const size_t smem = (size_t)3 * (p.experts + 1) * 4;
     auto fn = few ? (stream_k ? moe_gemm_kernel<GATED, 1, true> : moe_gemm_kernel<GATED, 1, false>)
                   : (stream_k ? moe_gemm_kernel<GATED, 2, true> : moe_gemm_kernel<GATED, 2, false>);
     return launch_pdl(fn, dim3((unsigned)(ctas < resident ? ctas : resident)), dim3(32 * GW), smem, stream, p);
 }
 
 struct Workspace {
-    size_t xf, h, y, ids, weights, part, arrived, bytes;
+    size_t xf, h, y, plan, weights, part, arrived, bytes;
     int warps;
 };
 Workspace layout(int tokens, int hidden, int inter, int topk, int sm_count)
@@ -760,7 +810,7 @@ Workspace layout(int tokens, int hidden, int inter, int topk, int sm_count)
     w.xf = take((size_t)tokens * hidden * 2);
     w.h = take((size_t)tokens * topk * inter * 2);
     w.y = take((size_t)tokens * topk * hidden * 4);
-    w.ids = take((size_t)tokens * topk * 4);
+    w.plan = take(sizeof(Plan));
     w.weights = take((size_t)tokens * topk * 4);
     w.warps = 4 * GW * sm_count;
     w.part = take((size_t)2 * w.warps * ((tokens + 7) / 8) * 256 * 4);
@@ -782,15 +832,17 @@ cudaError_t launch_moe(const Moe &a, int sm_count, void *workspace, cudaStream_t
     char *base = static_cast<char *>(workspace);
     uint16_t *xf = reinterpret_cast<uint16_t *>(base + w.xf), *h = reinterpret_cast<uint16_t *>(base + w.h);
     float *y = reinterpret_cast<float *>(base + w.y), *weights = reinterpret_cast<float *>(base + w.weights);
-    int32_t *ids = reinterpret_cast<int32_t *>(base + w.ids);
+    Plan *plan = reinterpret_cast<Plan *>(base + w.plan);
     float *part = reinterpret_cast<float *>(base + w.part);
     unsigned *arrived = reinterpret_cast<unsigned *>(base + w.arrived);
 
     RouteParams r = {static_cast<const __nv_bfloat16 *>(a.x), static_cast<const __nv_bfloat16 *>(a.router), a.bias, xf,
-                     ids, weights, a.ids_out, a.weights_out, a.tokens, a.hidden, a.experts, a.topk, a.sigmoid,
+                     plan, weights, a.ids_out, a.weights_out, a.tokens, a.hidden, a.experts, a.topk, a.sigmoid,
                      a.renormalize, a.scale, arrived, 2 * w.warps};
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)((a.tokens + ROUTE_TOKENS - 1) / ROUTE_TOKENS * ROUTE_CTAS));
+    const long long items = (long long)a.tokens * a.hidden / 16, per_cluster = ROUTE_CTAS * 32 * ROUTE_WARPS;
+    const int others = (int)(items <= per_cluster ? 1 : items >= 8 * per_cluster ? 8 : items / per_cluster);
+    cfg.gridDim = dim3(ROUTE_CTAS * (1 + others));
     cfg.blockDim = dim3(32 * ROUTE_WARPS);
     cfg.stream = stream;
     cudaLaunchAttribute attr[2];
@@ -801,13 +853,19 @@ cudaError_t launch_moe(const Moe &a, int sm_count, void *workspace, cudaStream_t
     attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
-    cudaError_t e = cudaLaunchKernelEx(&cfg, moe_route_kernel, r);
+    using Route = void (*)(const RouteParams);
+    static const Route routes[4][2] = {{moe_route_kernel<1, 4>, moe_route_kernel<1, 16>},
+                                       {moe_route_kernel<2, 4>, moe_route_kernel<2, 16>},
+                                       {moe_route_kernel<4, 4>, moe_route_kernel<4, 16>},
+                                       {moe_route_kernel<8, 4>, moe_route_kernel<8, 16>}};
+    const Route route = routes[a.tokens <= 8 ? 0 : a.tokens <= 16 ? 1 : a.tokens <= 32 ? 2 : 3][a.experts <= 128 ? 0 : 1];
+    cudaError_t e = cudaLaunchKernelEx(&cfg, route, (const RouteParams)r);
     if (e != cudaSuccess)
         return e;
 
-    GemmParams up = {static_cast<const uint8_t *>(a.w13), xf, ids, h, nullptr, a.tokens * a.topk, a.topk, a.experts,
+    GemmParams up = {static_cast<const uint8_t *>(a.w13), xf, plan, h, nullptr, a.tokens * a.topk, a.topk, a.experts,
                      a.hidden, a.inter, 1, 1, part, arrived};
-    GemmParams down = {static_cast<const uint8_t *>(a.w2), h, ids, nullptr, y, a.tokens * a.topk, a.topk, a.experts,
+    GemmParams down = {static_cast<const uint8_t *>(a.w2), h, plan, nullptr, y, a.tokens * a.topk, a.topk, a.experts,
                        a.inter, a.hidden, 1, 1, part, arrived + w.warps};
     e = launch_gemm<true>(up, sm_count, stream);
     if (e == cudaSuccess)
