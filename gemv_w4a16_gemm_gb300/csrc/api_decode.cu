@@ -212,8 +212,7 @@ size_t moe_workspace_bytes(int64_t tokens, int64_t hidden, int64_t inter, int64_
 {
     if (check_moe(tokens, hidden, inter, experts, topk) != W4Q_OK)
         return 0;
-    const int sms = device_sms();
-    return w4q::moe_workspace((int)tokens, (int)hidden, (int)inter, topk, sms < 1 ? 1 : sms);
+    return w4q::moe_workspace((int)tokens, (int)hidden, (int)inter, topk);
 }
 
 int moe_w4a16(const void *x, const void *router, const float *bias, const void *w13, const void *w2, void *out,
@@ -230,10 +229,9 @@ int moe_w4a16(const void *x, const void *router, const float *bias, const void *
     if (!aligned16(x) || !aligned16(router) || !aligned16(bias) || !aligned16(w13) || !aligned16(w2) ||
         !aligned16(out) || !aligned16(ids_out) || !aligned16(weights_out) || !aligned16(workspace))
         return W4Q_ERR_MISALIGNED;
-    const int sms = device_sms();
-    if (workspace == nullptr ||
-        workspace_bytes < w4q::moe_workspace((int)tokens, (int)hidden, (int)inter, topk, sms < 1 ? 1 : sms))
+    if (workspace == nullptr || workspace_bytes < w4q::moe_workspace((int)tokens, (int)hidden, (int)inter, topk))
         return W4Q_ERR_WORKSPACE;
+    const int sms = device_sms();
     if (sms < 1)
         return W4Q_ERR_CUDA;
     const w4q::Moe a = {x, router, bias, w13, w2, out, ids_out, weights_out, (int)tokens, (int)hidden, (int)inter,

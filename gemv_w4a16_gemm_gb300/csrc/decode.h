@@ -77,7 +77,7 @@ struct Moe {
     bool sigmoid, renormalize;
     float scale;
 };
-size_t moe_workspace(int tokens, int hidden, int inter, int topk, int sm_count);
+size_t moe_workspace(int tokens, int hidden, int inter, int topk);
 cudaError_t launch_moe(const Moe &a, int sm_count, void *workspace, cudaStream_t stream);
 
 }  // namespace w4q

@@ -23,22 +23,20 @@
 // The two products.  A unit is a pair of 16-row tiles of an expert (for gate/up
 // the gate and the up tile of the same rows, for down two neighbours) times that
 // expert's tokens.  The line of all units of the active experts, weighted by
-// what their numbers of tokens cost, is cut into equal ranges, those of an SM's
-// warps side by side, so that an SM's L1 holds the rows of one or two experts'
-// tokens.  With much to do (STREAM) the line is cut at any 256-column super-block
-// into one range per warp; a unit that warps share is joined by the last of them
-// to finish, from the workspace and in the line's order.  With little to do the
-// cuts fall between units, and the KW warps of a group share a unit's K and join
-// in shared memory, which is sooner done.  A tile goes
+// what their numbers of tokens cost, is cut into equal ranges, one per SM (one
+// CTA of 16 warps, or 12 with more registers).  A CTA takes its units in rounds:
+// a warp each while there are as many as warps, and a unit's K split over as
+// many warps as there are for the rest (their sums meet in shared memory), so
+// the warps end together.  All warps of a round walk along K side by side, so
+// that L1 serves their tokens' rows: an expert with 16 tokens of 6656 elements
+// has 213 KB of them, more than L1 holds (with warps at places of their own on
+// K, such experts took twice as long as those with 8).  A tile goes
 // from global memory to registers: a lane's 16-byte chunk of codes is four MMAs'
 // A fragments, its rows' scales and zero points are three more loads, and each
 // register is loaded again for the next super-block (of the next unit, too) as
 // soon as it is used up.  The tokens' rows, in the order of the B fragments (two
-// 16-byte loads a lane per 64 columns, for both tiles), come through L1, one
-// sub-block ahead: no shared memory is used for either.
-// (64 tokens x 2 of 16 experts (6656, 4096): tiles through a cp.async ring in
-// shared memory 295 us; single tiles in registers, rows loaded where they are
-// used 255 us; this xxx us.)
+// 16-byte loads a lane per 64 columns, for both tiles), are loaded one sub-block
+// ahead.
 //
 // Arithmetic.  A word of packed codes, masked, is a pair of bf16 subnormals
 // q 2^-133 (low nibbles) or q 2^-129 (high nibbles); one bf16x2 fma with 2^127
@@ -87,8 +85,6 @@ struct RouteParams {
     int tokens, hidden, experts, topk;
     bool sigmoid, renormalize;
     float scale;
-    unsigned *counters;  // set to zero for the products
-    int counter_count;
 };
 
 // What a super-block of a unit of an expert with n tokens costs, in quarters of
@@ -122,8 +118,6 @@ __global__ void __launch_bounds__(32 * ROUTE_WARPS) moe_route_kernel(const Route
         pdl_wait();
         pdl_launch_dependents();
         const int me = (blockIdx.x - ROUTE_CTAS) * 32 * ROUTE_WARPS + tid, all = (gridDim.x - ROUTE_CTAS) * 32 * ROUTE_WARPS;
-        for (int i = me; i < p.counter_count; i += all)
-            p.counters[i] = 0;
         // x in fragment order: of 64 columns, lane t's pairs 16j + 2t and 16j + 8 + 2t, j = 0..3
         const int per = p.hidden / 16;
         for (int i = me; i < p.tokens * per; i += all) {
@@ -330,10 +324,6 @@ __global__ void __launch_bounds__(32 * ROUTE_WARPS) moe_route_kernel(const Route
 
 // ------------------------------------------------------------ the products
 
-constexpr int GW = 4;  // warps of a CTA
-#ifndef W4Q_MOE_AHEAD
-#define W4Q_MOE_AHEAD 1
-#endif
 
 // bf16 pairs
 constexpr uint32_t BF_2P127 = 0x7F007F00u, BF_2P123 = 0x7D007D00u, NEG_2P127 = 0xFF00FF00u;
@@ -354,10 +344,6 @@ struct GemmParams {
     int entries, topk, experts;
     int K;         // columns
     int rows_out;  // rows per expert of the result
-    int KW;        // warps that share a unit's K
-    int sms;
-    float *part;       // STREAM: [2 * warps][token groups][2][128], a warp's parts of the unit that it continues and of the one that it begins
-    unsigned *arrived; // STREAM: [warps], by the warp that begins the unit; zeroed by the route kernel
 };
 
 __device__ __forceinline__ uint4 ldg_weight(const uint8_t *p)
@@ -367,6 +353,16 @@ __device__ __forceinline__ uint4 ldg_weight(const uint8_t *p)
                  : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
                  : "l"(p));
     return v;
+}
+
+// As mma_bf16, but free to be moved: the scheduler interleaves the four or eight
+// independent chains of a sub-block.
+__device__ __forceinline__ void mma_free(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1)
+{
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 "
+        "{%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
 // volatile: the compiler is not to move it down to its use
@@ -384,11 +380,6 @@ __device__ __forceinline__ uint4 ldg_row(const uint4 *p)
 struct Pair {
     uint4 q[2][4], s[2][2], z[2];
 };
-
-__device__ __forceinline__ void prefetch_tile(const uint8_t *p)
-{
-    asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(p), "n"(TILE_BYTES) : "memory");
-}
 
 template <int V>
 struct Count {
@@ -417,7 +408,7 @@ __device__ __forceinline__ void tile_step(const uint4 &q, uint32_t s0, uint32_t 
                                    bf16x2_fma(w & 0x00F000F0u, BF_2P123, z0), bf16x2_fma(wh & 0x00F000F0u, BF_2P123, z1)};
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
-                mma_bf16(d[nt], a, k ? x[nt][gr].z : x[nt][gr].x, k ? x[nt][gr].w : x[nt][gr].y, d[nt]);
+                mma_free(d[nt], a, k ? x[nt][gr].z : x[nt][gr].x, k ? x[nt][gr].w : x[nt][gr].y);
         }
         const uint32_t sc = gr ? s1 : s0;
         const float sa = bf16lo_to_f32(sc), sb = bf16hi_to_f32(sc);
@@ -431,44 +422,35 @@ __device__ __forceinline__ void tile_step(const uint4 &q, uint32_t s0, uint32_t 
     }
 }
 
-// NT groups of 8 tokens at a time, at most.
-template <bool GATED, int NT, bool STREAM>
-__global__ void __launch_bounds__(32 * GW, NT > 1 ? 3 : 4) moe_gemm_kernel(const GemmParams p)
+// NT groups of 8 tokens at a time, at most; W warps.
+template <bool GATED, int NT, int W>
+__global__ void __launch_bounds__(32 * W, 1) moe_gemm_kernel(const GemmParams p)
 {
     extern __shared__ int s_before[];  // [experts + 1] each: costs before, offsets, numbers of the active experts
     int *s_offset = s_before + p.experts + 1, *s_expert = s_offset + p.experts + 1;
-    __shared__ __align__(16) float s_sum[STREAM ? 1 : GW][2 * NT][128];
+    __shared__ __align__(16) float s_sum[W][2 * NT][128];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
 
     pdl_wait();
     pdl_launch_dependents();
     const int count = p.plan->count;
-    for (int i = tid; i < p.experts + 1; i += 32 * GW) {
+    for (int i = tid; i < p.experts + 1; i += 32 * W) {
         s_before[i] = p.plan->before[i];
         s_offset[i] = p.plan->offset[i];
         s_expert[i] = i < p.experts ? p.plan->expert[i] : 0;
     }
     __syncthreads();
 
+    // A unit: an active expert's block of rows.  Share r of the whole cost ends at share * r +
+    // min(r, extra).  (At most 512 experts, 64 x 16 choices, 2048 blocks: less than 2^23.)
+    struct Unit {
+        int a, blk;
+    };
     const int KB = p.K / 256, blocks = p.rows_out / (GATED ? 16 : 32);
-    const int KW = STREAM ? 1 : p.KW, kw = warp & (KW - 1), group = warp / KW, groups = GW / KW;
-    // CTAs c, c + sms, c + 2 sms .. share an SM, as far as the hardware deals them out in turn
-    const int per_sm = (gridDim.x + p.sms - 1) / p.sms;
-    const int place = gridDim.x % p.sms == 0 ? (blockIdx.x % p.sms) * per_sm + blockIdx.x / p.sms : blockIdx.x;
-    const int mine = place * groups + group, SB = blocks * KB;
-    // Share r of the whole cost ends at share * r + min(r, extra).  (At most 512 experts, 64 x 16
-    // choices, 2048 blocks and 128 super-blocks: less than 2^30.)
-    const unsigned total = (unsigned)s_before[count] * SB;
-    unsigned ranges = gridDim.x * groups;
-    if constexpr (STREAM)  // no range is shorter than a step, which costs at most 5 * 64 / 16
-        ranges = min(ranges, max(1u, total / (5 * MAX_TOKENS / 16 + 1)));
-    if (mine >= (int)ranges)
-        return;
-    const unsigned share = total / ranges, extra = total - share * ranges;
-    // the first step (STREAM) or unit that begins at or past that end
-    auto cut_at = [&](unsigned r) -> int {
+    const unsigned total = (unsigned)s_before[count] * blocks, share = total / gridDim.x, extra = total - share * gridDim.x;
+    auto cut_at = [&](unsigned r) -> Unit {  // the first unit that begins at or past that end
         const unsigned at = share * r + min(r, extra);
-        const int whole = (int)(at / (unsigned)SB);
+        const int whole = (int)(at / (unsigned)blocks);
         int lo = 0, hi = count;
         while (hi - lo > 1) {
             const int mid = (lo + hi) >> 1;
@@ -477,37 +459,53 @@ __global__ void __launch_bounds__(32 * GW, NT > 1 ? 3 : 4) moe_gemm_kernel(const
             else
                 hi = mid;
         }
-        const unsigned each = (s_before[lo + 1] - s_before[lo]) * (STREAM ? 1 : KB), items = STREAM ? SB : blocks;
-        return lo * items + min(items, (at - (unsigned)s_before[lo] * SB + each - 1) / each);
+        const unsigned each = s_before[lo + 1] - s_before[lo], blk = (at - (unsigned)s_before[lo] * blocks + each - 1) / each;
+        return blk < (unsigned)blocks ? Unit{lo, (int)blk} : Unit{lo + 1, 0};
     };
-    const int from = cut_at(mine), to = cut_at(mine + 1);
-    if (from >= to)
-        return;  // the whole group, which has a barrier of its own
-    const int first = STREAM ? (unsigned)from / (unsigned)KB : from, last = STREAM ? (unsigned)(to + KB - 1) / (unsigned)KB : to;
-    const int begin = STREAM ? from - first * KB : kw;  // the first unit's first super-block
+    const Unit at = cut_at(blockIdx.x), end = cut_at(blockIdx.x + 1);
+
+    // Rounds: the units that the CTA takes at once, all of one expert, and the warps of each.  All
+    // warps go through all rounds (their barriers are the whole CTA's), a warp without a unit idle.
+    struct Round {
+        Unit first;
+        int units, KW;  // units = 0: no round left
+    };
+    auto round_at = [&](Unit at) -> Round {
+        if (at.a > end.a || (at.a == end.a && at.blk >= end.blk))
+            return {at, 0, 1};
+        const int left = (at.a == end.a ? end.blk : blocks) - at.blk;
+        int KW = 1;
+        while (W / KW > left && KW < KB)
+            ++KW;
+        return {at, min(left, W / KW), KW};
+    };
+    auto after = [&](const Round &r) -> Unit {
+        const int blk = r.first.blk + r.units;
+        return blk == blocks ? Unit{r.first.a + 1, 0} : Unit{r.first.a, blk};
+    };
+    // this warp's next round with a unit, from r on
+    auto next_active = [&](Round r) -> Round {
+        while (r.units > 0 && warp / r.KW >= r.units)
+            r = round_at(after(r));
+        return r;
+    };
+    Round round = round_at(at);
+    if (round.units == 0)
+        return;  // the whole CTA
     const uint8_t *codes = p.packed + 16 * lane, *scales = p.packed + 2048 + 16 * g;
 
-    // Where unit u's first tile of this warp's first super-block lies, in 16 bytes (32 bits reach 64
-    // GB); rows_out / 16 is a multiple of 16, so the pair's second tile lies `second`, and the next
+    // Where this warp's first pair of tiles of a round lies, in 16 bytes (32 bits reach 64 GB);
+    // rows_out / 16 is a multiple of 16, so the pair's second tile lies `second`, and the next
     // super-block 8 tiles, from it.
     constexpr uint32_t TILE16 = TILE_BYTES / 16, NEXT_SB = 8 * TILE16, NONE = ~0u;
     const uint32_t second = GATED ? (uint32_t)(blocks >> 3) * KB * NEXT_SB : TILE16;
-    struct Cursor {
-        int a, blk;  // the unit: an active expert's block of rows
+    auto place_of = [&](const Round &r) -> uint32_t {
+        if (r.units == 0)
+            return NONE;
+        const int group = warp / r.KW, blk = r.first.blk + group;
+        const int tl = s_expert[r.first.a] * 2 * blocks + (GATED ? blk : 2 * blk);
+        return (uint32_t)(tl >> 3) * KB * NEXT_SB + (tl & 7) * TILE16 + (warp - group * r.KW) * NEXT_SB;
     };
-    auto next_unit = [&](Cursor &c) {
-        if (++c.blk == blocks) {
-            c.blk = 0;
-            ++c.a;
-        }
-    };
-    auto unit_at = [&](Cursor c) -> uint32_t {
-        const int tl = s_expert[c.a] * 2 * blocks + (GATED ? c.blk : 2 * c.blk);
-        return (uint32_t)(tl >> 3) * KB * NEXT_SB + (tl & 7) * TILE16 + kw * NEXT_SB;
-    };
-    Cursor cur;
-    cur.a = (unsigned)first / (unsigned)blocks;
-    cur.blk = first - cur.a * blocks;
     Pair w;
     auto load_codes = [&](uint32_t at, int r, int sb) {
         w.q[r][sb] = ldg_weight(codes + (uint64_t)(at + r * second) * 16 + 512 * sb);
@@ -516,96 +514,46 @@ __global__ void __launch_bounds__(32 * GW, NT > 1 ? 3 : 4) moe_gemm_kernel(const
         w.s[r][half] = ldg_weight(scales + (uint64_t)(at + r * second) * 16 + 128 * half);
     };
     auto load_zeros = [&](uint32_t at, int r) { w.z[r] = ldg_weight(scales + (uint64_t)(at + r * second) * 16 + 256); };
-    uint32_t here = unit_at(cur) + (STREAM ? begin * NEXT_SB : 0), there;
+    uint32_t here = place_of(next_active(round));
+    if (here != NONE) {
 #pragma unroll
-    for (int r = 0; r < 2; ++r) {
-        load_zeros(here, r);
-        load_scales(here, r, 0);
-    }
+        for (int r = 0; r < 2; ++r) {
+            load_zeros(here, r);
+            load_scales(here, r, 0);
+        }
 #pragma unroll
-    for (int sb = 0; sb < 4; ++sb)
+        for (int sb = 0; sb < 4; ++sb)
+#pragma unroll
+            for (int r = 0; r < 2; ++r)
+                load_codes(here, r, sb);
 #pragma unroll
         for (int r = 0; r < 2; ++r)
-            load_codes(here, r, sb);
-#pragma unroll
-    for (int r = 0; r < 2; ++r)
-        load_scales(here, r, 1);
+            load_scales(here, r, 1);
+    }
 
-    // The warp's steps go to L2 AHEAD steps before they are loaded: a register's load has one step's
-    // time to arrive, which memory under load exceeds and L2 does not.
-    constexpr int AHEAD = W4Q_MOE_AHEAD;
-    int pu = first, pb = begin;
-    uint32_t pat = here;
-    Cursor pcur = cur;
-    auto prefetch = [&](bool issue) {
-        if (pu >= last)
-            return;
-        if (issue && lane < 2)
-            prefetch_tile(p.packed + (uint64_t)(pat + lane * second) * 16);
-        pb += KW;
-        pat += KW * NEXT_SB;
-        if (pb >= (STREAM ? min(KB, to - pu * KB) : KB)) {
-            pb = kw;
-            next_unit(pcur);
-            if (++pu < last)
-                pat = unit_at(pcur);
-        }
-    };
-    prefetch(false);
-#pragma unroll 1
-    for (int i = 0; i < AHEAD; ++i)
-        prefetch(true);
-
-    auto part_of = [&](int range, bool begins) -> float * {
-        return p.part + (int64_t)(2 * range + (begins ? 1 : 0)) * ((p.entries / p.topk + 7) / 8) * 256;
-    };
-    // the result of a pair of tiles for the 8 tokens col0 .. of the warp's list of n
-    auto store = [&](const float (&v)[2][4], int col0, const int *list, int n, int blk) {
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const int col = col0 + 2 * t + i;
-            if (col >= n)
-                continue;
-            const int entry = __ldg(list + col);
-            if constexpr (GATED) {
-                // rows g and g + 8 of the 16, in fragment order
-                uint16_t *dst = p.h + (int64_t)entry * p.rows_out + (blk >> 2) * 64 + (g >> 1) * 16 + (blk & 3) * 4 + (g & 1);
-#pragma unroll
-                for (int e8 = 0; e8 < 2; ++e8) {
-                    const float gate = v[0][2 * e8 + i] * 64.f, up = v[1][2 * e8 + i] * 64.f;
-                    const __nv_bfloat16 hb = __float2bfloat16_rn(gate / (1.f + __expf(-gate)) * up);
-                    dst[2 * e8] = *reinterpret_cast<const uint16_t *>(&hb);
-                }
-            } else {
-                float *dst = p.y + (int64_t)entry * p.rows_out + blk * 32 + g;
-#pragma unroll
-                for (int r = 0; r < 2; ++r) {
-                    dst[16 * r] = v[r][i] * 64.f;
-                    dst[16 * r + 8] = v[r][2 + i] * 64.f;
-                }
-            }
-        }
-    };
-
-    for (int u = first; u < last; ++u, here = there, next_unit(cur)) {
-        Cursor after = cur;
-        next_unit(after);
-        there = u + 1 < last ? unit_at(after) : NONE;
-        const int b0 = STREAM ? (u == first ? begin : 0) : kw;
-        const int b1 = STREAM ? min(KB, to - u * KB) : KB;
-        const bool whole = !STREAM || (b0 == 0 && b1 == KB);
-        const int *list = p.plan->entries + s_offset[cur.a];
-        const int n = s_offset[cur.a + 1] - s_offset[cur.a];
+    for (; round.units > 0; round = round_at(after(round))) {
+        const int KW = round.KW, group = warp / KW, kw = warp - group * KW, blk = round.first.blk + group;
+        const bool active = group < round.units;
+        const int *list = p.plan->entries + s_offset[round.first.a];
+        const int n = s_offset[round.first.a + 1] - s_offset[round.first.a];
+        const uint32_t there = active ? place_of(next_active(round_at(after(round)))) : here;
         // an expert with more than 8 NT tokens takes several passes over its tiles
         auto pass = [&](auto groups_of_8, int n0) {
             constexpr int N = decltype(groups_of_8)::value;
+            if (!active) {
+                if (KW > 1) {
+                    __syncthreads();
+                    __syncthreads();
+                }
+                return;
+            }
             const bool again = n0 + 8 * N < n;
             const uint4 *row[N];  // tokens past the last are its copies, and are not stored
 #pragma unroll
             for (int nt = 0; nt < N; ++nt) {
                 const int entry = __ldg(list + min(n0 + nt * 8 + g, n - 1));
                 row[nt] = reinterpret_cast<const uint4 *>(
-                    p.xf + (int64_t)(GATED ? (unsigned)entry / (unsigned)p.topk : entry) * p.K + b0 * 256 + 16 * t);
+                    p.xf + (int64_t)(GATED ? (unsigned)entry / (unsigned)p.topk : entry) * p.K + kw * 256 + 16 * t);
             }
             float acc[2][N][4];
 #pragma unroll
@@ -620,12 +568,10 @@ __global__ void __launch_bounds__(32 * GW, NT > 1 ? 3 : 4) moe_gemm_kernel(const
                 x[nt][1] = ldg_row(row[nt] + 1);
             }
             uint32_t at = here;
-            for (int b = b0; b < b1; b += KW, at += KW * NEXT_SB) {
-                const bool more = b + KW < b1;
+            for (int b = kw; b < KB; b += KW, at += KW * NEXT_SB) {
+                const bool more = b + KW < KB;
                 const uint32_t next = more ? at + KW * NEXT_SB : again ? here : there;
                 const uint4 z[2] = {w.z[0], w.z[1]};
-                if (n0 == 0)
-                    prefetch(true);
                 if (next != NONE) {
                     load_zeros(next, 0);
                     load_zeros(next, 1);
@@ -664,28 +610,18 @@ __global__ void __launch_bounds__(32 * GW, NT > 1 ? 3 : 4) moe_gemm_kernel(const
                     row[nt] += KW * 32;
             }
             // --- the sums of the warps that share the unit, and the result
-            if (STREAM && !whole) {
-                float *part = part_of(mine, b0 == 0) + (n0 / 8) * 256 + lane * 4;
-#pragma unroll
-                for (int nt = 0; nt < N; ++nt)
-#pragma unroll
-                    for (int r = 0; r < 2; ++r)
-                        __stcg(reinterpret_cast<float4 *>(part + (nt * 2 + r) * 128),
-                               make_float4(acc[r][nt][0], acc[r][nt][1], acc[r][nt][2], acc[r][nt][3]));
-                return;
-            }
             if (KW > 1) {
 #pragma unroll
                 for (int r = 0; r < 2; ++r)
 #pragma unroll
                     for (int nt = 0; nt < N; ++nt)
-                        *reinterpret_cast<float4 *>(&s_sum[STREAM ? 0 : warp][r * N + nt][lane * 4]) =
+                        *reinterpret_cast<float4 *>(&s_sum[warp][r * N + nt][lane * 4]) =
                             make_float4(acc[r][nt][0], acc[r][nt][1], acc[r][nt][2], acc[r][nt][3]);
-                asm volatile("bar.sync %0, %1;" ::"r"(1 + group), "r"(32 * KW) : "memory");
+                __syncthreads();
             }
 #pragma unroll
             for (int nt = 0; nt < N; ++nt) {
-                if ((nt & (KW - 1)) != kw)
+                if (nt % KW != kw)
                     continue;
                 float v[2][4];
 #pragma unroll
@@ -693,8 +629,9 @@ __global__ void __launch_bounds__(32 * GW, NT > 1 ? 3 : 4) moe_gemm_kernel(const
                     v[r][0] = acc[r][nt][0], v[r][1] = acc[r][nt][1], v[r][2] = acc[r][nt][2], v[r][3] = acc[r][nt][3];
                     if (KW > 1) {
                         v[r][0] = v[r][1] = v[r][2] = v[r][3] = 0.f;
+#pragma unroll 4
                         for (int q = 0; q < KW; ++q) {
-                            const float4 y = *reinterpret_cast<const float4 *>(&s_sum[STREAM ? 0 : group * KW + q][r * N + nt][lane * 4]);
+                            const float4 y = *reinterpret_cast<const float4 *>(&s_sum[warp - kw + q][r * N + nt][lane * 4]);
                             v[r][0] += y.x;
                             v[r][1] += y.y;
                             v[r][2] += y.z;
@@ -702,10 +639,33 @@ __global__ void __launch_bounds__(32 * GW, NT > 1 ? 3 : 4) moe_gemm_kernel(const
                         }
                     }
                 }
-                store(v, n0 + nt * 8, list, n, cur.blk);
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const int col = n0 + nt * 8 + 2 * t + i;
+                    if (col >= n)
+                        continue;
+                    const int entry = __ldg(list + col);
+                    if constexpr (GATED) {
+                        // rows g and g + 8 of the 16, in fragment order
+                        uint16_t *dst = p.h + (int64_t)entry * p.rows_out + (blk >> 2) * 64 + (g >> 1) * 16 + (blk & 3) * 4 + (g & 1);
+#pragma unroll
+                        for (int e8 = 0; e8 < 2; ++e8) {
+                            const float gate = v[0][2 * e8 + i] * 64.f, up = v[1][2 * e8 + i] * 64.f;
+                            const __nv_bfloat16 hb = __float2bfloat16_rn(gate / (1.f + __expf(-gate)) * up);
+                            dst[2 * e8] = *reinterpret_cast<const uint16_t *>(&hb);
+                        }
+                    } else {
+                        float *dst = p.y + (int64_t)entry * p.rows_out + blk * 32 + g;
+#pragma unroll
+                        for (int r = 0; r < 2; ++r) {
+                            dst[16 * r] = v[r][i] * 64.f;
+                            dst[16 * r + 8] = v[r][2 + i] * 64.f;
+                        }
+                    }
+                }
             }
             if (KW > 1)  // the sums are read
-                asm volatile("bar.sync %0, %1;" ::"r"(1 + group), "r"(32 * KW) : "memory");
+                __syncthreads();
         };
         int n0 = 0;
         if constexpr (NT > 1)
@@ -713,44 +673,7 @@ __global__ void __launch_bounds__(32 * GW, NT > 1 ? 3 : 4) moe_gemm_kernel(const
                 pass(Count<2>(), n0);
         for (; n0 < n; n0 += 8)
             pass(Count<1>(), n0);
-
-        if (STREAM && !whole) {
-            // the warps that hold the unit's first and last step: a step is in the last range whose
-            // beginning is at most what the steps before it cost
-            const unsigned each = s_before[cur.a + 1] - s_before[cur.a];
-            const unsigned cost0 = (unsigned)s_before[cur.a] * SB + (unsigned)cur.blk * KB * each, cost1 = cost0 + (KB - 1) * each;
-            auto owner = [&](unsigned cost) -> int {
-                const unsigned longer = (share + 1) * extra;
-                return cost < longer ? cost / (share + 1) : extra + (cost - longer) / share;
-            };
-            const int w0 = owner(cost0), w1 = owner(cost1);
-            __syncwarp();
-            unsigned before = 0;
-            if (lane == 0) {
-                __threadfence();
-                before = atomic_add_acq_rel(p.arrived + w0, 1u);
-                __threadfence();
-            }
-            before = __shfl_sync(~0u, before, 0);
-            __syncwarp();
-            if (before == (unsigned)(w1 - w0)) {
-                for (int c = 0; c < n; c += 8) {
-                    float v[2][4] = {};
-                    for (int q = w0; q <= w1; ++q) {
-                        const float *part = part_of(q, q == w0) + (c / 8) * 256 + lane * 4;
-#pragma unroll
-                        for (int r = 0; r < 2; ++r) {
-                            const float4 y = __ldcg(reinterpret_cast<const float4 *>(part + r * 128));
-                            v[r][0] += y.x;
-                            v[r][1] += y.y;
-                            v[r][2] += y.z;
-                            v[r][3] += y.w;
-                        }
-                    }
-                    store(v, c, list, n, cur.blk);
-                }
-            }
-        }
+        here = there;
     }
 }
 
@@ -779,26 +702,19 @@ __global__ void __launch_bounds__(128) moe_combine_kernel(const float *y, const 
 }
 
 template <bool GATED>
-cudaError_t launch_gemm(GemmParams p, int sm_count, cudaStream_t stream)
+cudaError_t launch_gemm(const GemmParams &p, int sm_count, cudaStream_t stream)
 {
+    // with up to 8 tokens no expert has more
     const bool few = p.entries <= 8 * p.topk;
-    const int KB = p.K / 256, most = p.entries < p.experts ? p.entries : p.experts;
-    const long long units = (long long)most * (p.rows_out / (GATED ? 16 : 32)), resident = (few ? 4LL : 3LL) * sm_count;
-    const bool stream_k = units * KB >= 8 * GW * resident;  // steps a warp, if every expert that can be active is
-    p.KW = stream_k ? 1 : KB >= 8 ? 4 : (KB >= 2 ? 2 : 1);
-    p.sms = sm_count;
-    const long long ctas = stream_k ? resident : (units * p.KW + GW - 1) / GW;
     const size_t smem = (size_t)3 * (p.experts + 1) * 4;
-    auto fn = few ? (stream_k ? moe_gemm_kernel<GATED, 1, true> : moe_gemm_kernel<GATED, 1, false>)
-                  : (stream_k ? moe_gemm_kernel<GATED, 2, true> : moe_gemm_kernel<GATED, 2, false>);
-    return launch_pdl(fn, dim3((unsigned)(ctas < resident ? ctas : resident)), dim3(32 * GW), smem, stream, p);
+    return launch_pdl(few ? moe_gemm_kernel<GATED, 1, 16> : moe_gemm_kernel<GATED, 2, 12>, dim3((unsigned)sm_count),
+                      dim3(32 * (few ? 16 : 12)), smem, stream, p);
 }
 
 struct Workspace {
-    size_t xf, h, y, plan, weights, part, arrived, bytes;
-    int warps;
+    size_t xf, h, y, plan, weights, bytes;
 };
-Workspace layout(int tokens, int hidden, int inter, int topk, int sm_count)
+Workspace layout(int tokens, int hidden, int inter, int topk)
 {
     Workspace w;
     size_t at = 0;
@@ -812,33 +728,28 @@ Workspace layout(int tokens, int hidden, int inter, int topk, int sm_count)
     w.y = take((size_t)tokens * topk * hidden * 4);
     w.plan = take(sizeof(Plan));
     w.weights = take((size_t)tokens * topk * 4);
-    w.warps = 4 * GW * sm_count;
-    w.part = take((size_t)2 * w.warps * ((tokens + 7) / 8) * 256 * 4);
-    w.arrived = take((size_t)2 * w.warps * 4);  // of either product
     w.bytes = at;
     return w;
 }
 
 }  // namespace
 
-size_t moe_workspace(int tokens, int hidden, int inter, int topk, int sm_count)
+size_t moe_workspace(int tokens, int hidden, int inter, int topk)
 {
-    return layout(tokens, hidden, inter, topk, sm_count).bytes;
+    return layout(tokens, hidden, inter, topk).bytes;
 }
 
 cudaError_t launch_moe(const Moe &a, int sm_count, void *workspace, cudaStream_t stream)
 {
-    const Workspace w = layout(a.tokens, a.hidden, a.inter, a.topk, sm_count);
+    const Workspace w = layout(a.tokens, a.hidden, a.inter, a.topk);
     char *base = static_cast<char *>(workspace);
     uint16_t *xf = reinterpret_cast<uint16_t *>(base + w.xf), *h = reinterpret_cast<uint16_t *>(base + w.h);
     float *y = reinterpret_cast<float *>(base + w.y), *weights = reinterpret_cast<float *>(base + w.weights);
     Plan *plan = reinterpret_cast<Plan *>(base + w.plan);
-    float *part = reinterpret_cast<float *>(base + w.part);
-    unsigned *arrived = reinterpret_cast<unsigned *>(base + w.arrived);
 
     RouteParams r = {static_cast<const __nv_bfloat16 *>(a.x), static_cast<const __nv_bfloat16 *>(a.router), a.bias, xf,
                      plan, weights, a.ids_out, a.weights_out, a.tokens, a.hidden, a.experts, a.topk, a.sigmoid,
-                     a.renormalize, a.scale, arrived, 2 * w.warps};
+                     a.renormalize, a.scale};
     cudaLaunchConfig_t cfg = {};
     const long long items = (long long)a.tokens * a.hidden / 16, per_cluster = ROUTE_CTAS * 32 * ROUTE_WARPS;
     const int others = (int)(items <= per_cluster ? 1 : items >= 8 * per_cluster ? 8 : items / per_cluster);
@@ -864,9 +775,9 @@ cudaError_t launch_moe(const Moe &a, int sm_count, void *workspace, cudaStream_t
         return e;
 
     GemmParams up = {static_cast<const uint8_t *>(a.w13), xf, plan, h, nullptr, a.tokens * a.topk, a.topk, a.experts,
-                     a.hidden, a.inter, 1, 1, part, arrived};
+                     a.hidden, a.inter};
     GemmParams down = {static_cast<const uint8_t *>(a.w2), h, plan, nullptr, y, a.tokens * a.topk, a.topk, a.experts,
-                       a.inter, a.hidden, 1, 1, part, arrived + w.warps};
+                       a.inter, a.hidden};
     e = launch_gemm<true>(up, sm_count, stream);
     if (e == cudaSuccess)
         e = launch_gemm<false>(down, sm_count, stream);
