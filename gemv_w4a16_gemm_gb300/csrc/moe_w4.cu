@@ -50,6 +50,8 @@
 #include "decode.h"
 #include "kernels.h"
 
+#include <atomic>
+
 namespace cg = cooperative_groups;
 
 namespace w4q {
@@ -346,18 +348,21 @@ struct GemmParams {
     int rows_out;  // rows per expert of the result
 };
 
-__device__ __forceinline__ uint4 ldg_weight(const uint8_t *p)
+__device__ __forceinline__ void copy16(uint32_t dst, const void *src, uint64_t policy)
 {
-    uint4 v;
-    asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
-                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-                 : "l"(p));
-    return v;
+    asm volatile("cp.async.cg.shared.global.L2::cache_hint [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "l"(policy)
+                 : "memory");
 }
 
-// As mma_bf16, but free to be moved: the scheduler interleaves the four or eight
-// independent chains of a sub-block.
-__device__ __forceinline__ void mma_free(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1)
+// d = a b and d += a b; not volatile, so that independent chains interleave.
+__device__ __forceinline__ void mma_first(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1)
+{
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 "
+        "{%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%10, %10, %10, %10};"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
+}
+__device__ __forceinline__ void mma_more(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1)
 {
     asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 "
         "{%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
@@ -374,12 +379,6 @@ __device__ __forceinline__ uint4 ldg_row(const uint4 *p)
                  : "l"(p));
     return v;
 }
-
-// A lane's part of a pair of tiles: the four sub-blocks' codes, the bf16 scale
-// pairs of rows g, g + 8 for the 8 groups, and their zero points.
-struct Pair {
-    uint4 q[2][4], s[2][2], z[2];
-};
 
 template <int V>
 struct Count {
@@ -399,16 +398,16 @@ __device__ __forceinline__ void tile_step(const uint4 &q, uint32_t s0, uint32_t 
         const uint32_t z1 = bf16x2_mul(prmt(zz, 0u, gr ? 0x4343u : 0x4141u), NEG_2P127);
         float d[NT][4];
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-            d[nt][0] = d[nt][1] = d[nt][2] = d[nt][3] = 0.f;
-#pragma unroll
         for (int k = 0; k < 2; ++k) {
             const uint32_t w = (&q.x)[2 * gr + k], wh = w >> 8;
             const uint32_t a[4] = {bf16x2_fma(w & 0x000F000Fu, BF_2P127, z0), bf16x2_fma(wh & 0x000F000Fu, BF_2P127, z1),
                                    bf16x2_fma(w & 0x00F000F0u, BF_2P123, z0), bf16x2_fma(wh & 0x00F000F0u, BF_2P123, z1)};
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
-                mma_free(d[nt], a, k ? x[nt][gr].z : x[nt][gr].x, k ? x[nt][gr].w : x[nt][gr].y);
+                if (k == 0)
+                    mma_first(d[nt], a, x[nt][gr].x, x[nt][gr].y);
+                else
+                    mma_more(d[nt], a, x[nt][gr].z, x[nt][gr].w);
         }
         const uint32_t sc = gr ? s1 : s0;
         const float sa = bf16lo_to_f32(sc), sb = bf16hi_to_f32(sc);
@@ -426,9 +425,10 @@ __device__ __forceinline__ void tile_step(const uint4 &q, uint32_t s0, uint32_t 
 template <bool GATED, int NT, int W>
 __global__ void __launch_bounds__(32 * W, 1) moe_gemm_kernel(const GemmParams p)
 {
-    extern __shared__ int s_before[];  // [experts + 1] each: costs before, offsets, numbers of the active experts
+    extern __shared__ __align__(16) int s_before[];  // [experts + 1] each: costs before, offsets, numbers of the active experts
     int *s_offset = s_before + p.experts + 1, *s_expert = s_offset + p.experts + 1;
     __shared__ __align__(16) float s_sum[W][2 * NT][128];
+    uint8_t *s_ring = reinterpret_cast<uint8_t *>(s_before) + (12 * (p.experts + 1) + 15) / 16 * 16;  // [W][2][2 tiles]
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
 
     pdl_wait();
@@ -492,7 +492,6 @@ __global__ void __launch_bounds__(32 * W, 1) moe_gemm_kernel(const GemmParams p)
     Round round = round_at(at);
     if (round.units == 0)
         return;  // the whole CTA
-    const uint8_t *codes = p.packed + 16 * lane, *scales = p.packed + 2048 + 16 * g;
 
     // Where this warp's first pair of tiles of a round lies, in 16 bytes (32 bits reach 64 GB);
     // rows_out / 16 is a multiple of 16, so the pair's second tile lies `second`, and the next
@@ -506,30 +505,27 @@ __global__ void __launch_bounds__(32 * W, 1) moe_gemm_kernel(const GemmParams p)
         const int tl = s_expert[r.first.a] * 2 * blocks + (GATED ? blk : 2 * blk);
         return (uint32_t)(tl >> 3) * KB * NEXT_SB + (tl & 7) * TILE16 + (warp - group * r.KW) * NEXT_SB;
     };
-    Pair w;
-    auto load_codes = [&](uint32_t at, int r, int sb) {
-        w.q[r][sb] = ldg_weight(codes + (uint64_t)(at + r * second) * 16 + 512 * sb);
-    };
-    auto load_scales = [&](uint32_t at, int r, int half) {
-        w.s[r][half] = ldg_weight(scales + (uint64_t)(at + r * second) * 16 + 128 * half);
-    };
-    auto load_zeros = [&](uint32_t at, int r) { w.z[r] = ldg_weight(scales + (uint64_t)(at + r * second) * 16 + 256); };
-    uint32_t here = place_of(next_active(round));
-    if (here != NONE) {
+    // The pair at `at` into one half of the warp's ring: 16 bytes a lane, 4864 in all.
+    const uint64_t policy = policy_evict_first();
+    const uint32_t ring = smem_addr(s_ring) + warp * (4 * TILE_BYTES);
+    auto copy = [&](uint32_t at, int half) {
+        if (at != NONE) {
+            const uint8_t *src = p.packed + (uint64_t)at * 16 + 16 * lane;
+            const uint32_t dst = ring + half * 2 * TILE_BYTES + 16 * lane;
 #pragma unroll
-        for (int r = 0; r < 2; ++r) {
-            load_zeros(here, r);
-            load_scales(here, r, 0);
+            for (int r = 0; r < 2; ++r, src += (uint64_t)second * 16) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    copy16(dst + r * TILE_BYTES + 512 * i, src + 512 * i, policy);
+                if (lane < 24)
+                    copy16(dst + r * TILE_BYTES + 2048, src + 2048, policy);
+            }
         }
-#pragma unroll
-        for (int sb = 0; sb < 4; ++sb)
-#pragma unroll
-            for (int r = 0; r < 2; ++r)
-                load_codes(here, r, sb);
-#pragma unroll
-        for (int r = 0; r < 2; ++r)
-            load_scales(here, r, 1);
-    }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+    uint32_t here = place_of(next_active(round));
+    int half = 0;
+    copy(here, 0);
 
     for (; round.units > 0; round = round_at(after(round))) {
         const int KW = round.KW, group = warp / KW, kw = warp - group * KW, blk = round.first.blk + group;
@@ -571,10 +567,18 @@ __global__ void __launch_bounds__(32 * W, 1) moe_gemm_kernel(const GemmParams p)
             for (int b = kw; b < KB; b += KW, at += KW * NEXT_SB) {
                 const bool more = b + KW < KB;
                 const uint32_t next = more ? at + KW * NEXT_SB : again ? here : there;
-                const uint4 z[2] = {w.z[0], w.z[1]};
-                if (next != NONE) {
-                    load_zeros(next, 0);
-                    load_zeros(next, 1);
+                // this pair has come, and every lane has read the one before
+                asm volatile("cp.async.wait_group 0;" ::: "memory");
+                __syncwarp();
+                const uint32_t tiles = ring + half * 2 * TILE_BYTES;
+                half ^= 1;
+                copy(next, half);
+                uint4 sc[2][2], z[2];
+#pragma unroll
+                for (int r = 0; r < 2; ++r) {
+                    sc[r][0] = lds128(tiles + r * TILE_BYTES + 2048 + 16 * g);
+                    sc[r][1] = lds128(tiles + r * TILE_BYTES + 2048 + 128 + 16 * g);
+                    z[r] = lds128(tiles + r * TILE_BYTES + 2304 + 16 * g);
                 }
 #pragma unroll
                 for (int sb = 0; sb < 4; ++sb) {
@@ -591,13 +595,9 @@ __global__ void __launch_bounds__(32 * W, 1) moe_gemm_kernel(const GemmParams p)
                     }
 #pragma unroll
                     for (int r = 0; r < 2; ++r) {
-                        const uint4 &sc = w.s[r][sb >> 1];
-                        tile_step<N>(w.q[r][sb], sb & 1 ? sc.z : sc.x, sb & 1 ? sc.w : sc.y, (&z[r].x)[sb], x, acc[r]);
-                        if (next != NONE) {
-                            load_codes(next, r, sb);
-                            if (sb & 1)
-                                load_scales(next, r, sb >> 1);
-                        }
+                        const uint4 &c = sc[r][sb >> 1];
+                        tile_step<N>(lds128(tiles + r * TILE_BYTES + 512 * sb + 16 * lane), sb & 1 ? c.z : c.x,
+                                     sb & 1 ? c.w : c.y, (&z[r].x)[sb], x, acc[r]);
                     }
 #pragma unroll
                     for (int nt = 0; nt < N; ++nt) {
@@ -706,9 +706,14 @@ cudaError_t launch_gemm(const GemmParams &p, int sm_count, cudaStream_t stream)
 {
     // with up to 8 tokens no expert has more
     const bool few = p.entries <= 8 * p.topk;
-    const size_t smem = (size_t)3 * (p.experts + 1) * 4;
-    return launch_pdl(few ? moe_gemm_kernel<GATED, 1, 16> : moe_gemm_kernel<GATED, 2, 12>, dim3((unsigned)sm_count),
-                      dim3(32 * (few ? 16 : 12)), smem, stream, p);
+    constexpr int W = 16;
+    const int smem = (12 * (p.experts + 1) + 15) / 16 * 16 + W * 4 * TILE_BYTES;
+    static std::atomic<unsigned long long> done[2];
+    auto fn = few ? moe_gemm_kernel<GATED, 1, W> : moe_gemm_kernel<GATED, 2, W>;
+    const cudaError_t e = smem_opt_in_once(done[few], fn, 12 * (MAX_EXPERTS + 1) + 16 + W * 4 * TILE_BYTES);
+    if (e != cudaSuccess)
+        return e;
+    return launch_pdl(fn, dim3((unsigned)sm_count), dim3(32 * W), smem, stream, p);
 }
 
 struct Workspace {
