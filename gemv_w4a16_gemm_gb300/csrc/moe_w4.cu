@@ -24,19 +24,13 @@
 // the gate and the up tile of the same rows, for down two neighbours) times that
 // expert's tokens.  The line of all units of the active experts, weighted by
 // what their numbers of tokens cost, is cut into equal ranges, one per SM (one
-// CTA of 16 warps, or 12 with more registers).  A CTA takes its units in rounds:
-// a warp each while there are as many as warps, and a unit's K split over as
-// many warps as there are for the rest (their sums meet in shared memory), so
-// the warps end together.  All warps of a round walk along K side by side, so
-// that L1 serves their tokens' rows: an expert with 16 tokens of 6656 elements
-// has 213 KB of them, more than L1 holds (with warps at places of their own on
-// K, such experts took twice as long as those with 8).  A tile goes
-// from global memory to registers: a lane's 16-byte chunk of codes is four MMAs'
-// A fragments, its rows' scales and zero points are three more loads, and each
-// register is loaded again for the next super-block (of the next unit, too) as
-// soon as it is used up.  The tokens' rows, in the order of the B fragments (two
-// 16-byte loads a lane per 64 columns, for both tiles), are loaded one sub-block
-// ahead.
+// CTA of W warps).  A CTA takes the units of its range an expert at a time: their
+// 256-column super-blocks, one after the other, are cut into W equal ranges, one
+// per warp, and the units that warps share are joined in shared memory at the
+// end, in the line's order.  A warp's tiles come through a ring of two pairs of
+// its own in shared memory (cp.async; tiles loaded straight to registers left
+// the tokens' rows, which come through L1 one sub-block ahead, waiting on the
+// same few scoreboards).
 //
 // Arithmetic.  A word of packed codes, masked, is a pair of bf16 subnormals
 // q 2^-133 (low nibbles) or q 2^-129 (high nibbles); one bf16x2 fma with 2^127
@@ -427,8 +421,9 @@ __global__ void __launch_bounds__(32 * W, 1) moe_gemm_kernel(const GemmParams p)
 {
     extern __shared__ __align__(16) int s_before[];  // [experts + 1] each: costs before, offsets, numbers of the active experts
     int *s_offset = s_before + p.experts + 1, *s_expert = s_offset + p.experts + 1;
-    __shared__ __align__(16) float s_sum[W][2 * NT][128];
     uint8_t *s_ring = reinterpret_cast<uint8_t *>(s_before) + (12 * (p.experts + 1) + 15) / 16 * 16;  // [W][2][2 tiles]
+    // a warp's parts of the unit that it continues and of the one that it begins: [W][2][2 * NT][128]
+    float *s_part = reinterpret_cast<float *>(s_ring + W * 4 * TILE_BYTES);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
 
     pdl_wait();
@@ -464,46 +459,38 @@ __global__ void __launch_bounds__(32 * W, 1) moe_gemm_kernel(const GemmParams p)
     };
     const Unit at = cut_at(blockIdx.x), end = cut_at(blockIdx.x + 1);
 
-    // Rounds: the units that the CTA takes at once, all of one expert, and the warps of each.  All
-    // warps go through all rounds (their barriers are the whole CTA's), a warp without a unit idle.
-    struct Round {
+    // Segments: the units of one expert in the range.  Warp w's part of a segment of S steps (its
+    // units' super-blocks) is S w / W .. S (w + 1) / W - 1.  All warps go through all segments.
+    struct Segment {
         Unit first;
-        int units, KW;  // units = 0: no round left
+        int units;  // 0: no segment left
     };
-    auto round_at = [&](Unit at) -> Round {
+    auto segment_at = [&](Unit at) -> Segment {
         if (at.a > end.a || (at.a == end.a && at.blk >= end.blk))
-            return {at, 0, 1};
-        const int left = (at.a == end.a ? end.blk : blocks) - at.blk;
-        int KW = 1;
-        while (W / KW > left && KW < KB)
-            ++KW;
-        return {at, min(left, W / KW), KW};
+            return {at, 0};
+        return {at, (at.a == end.a ? end.blk : blocks) - at.blk};
     };
-    auto after = [&](const Round &r) -> Unit {
-        const int blk = r.first.blk + r.units;
-        return blk == blocks ? Unit{r.first.a + 1, 0} : Unit{r.first.a, blk};
-    };
-    // this warp's next round with a unit, from r on
-    auto next_active = [&](Round r) -> Round {
-        while (r.units > 0 && warp / r.KW >= r.units)
-            r = round_at(after(r));
-        return r;
-    };
-    Round round = round_at(at);
-    if (round.units == 0)
+    auto after = [&](const Segment &s) -> Segment { return segment_at({s.first.a + 1, 0}); };
+    auto cut_of = [&](const Segment &s, int w) -> int { return s.units * KB * w / W; };  // < 2^22
+    Segment seg = segment_at(at);
+    if (seg.units == 0)
         return;  // the whole CTA
-
-    // Where this warp's first pair of tiles of a round lies, in 16 bytes (32 bits reach 64 GB);
+    // Where the pair of unit u, super-block b of a segment lies, in 16 bytes (32 bits reach 64 GB);
     // rows_out / 16 is a multiple of 16, so the pair's second tile lies `second`, and the next
     // super-block 8 tiles, from it.
     constexpr uint32_t TILE16 = TILE_BYTES / 16, NEXT_SB = 8 * TILE16, NONE = ~0u;
     const uint32_t second = GATED ? (uint32_t)(blocks >> 3) * KB * NEXT_SB : TILE16;
-    auto place_of = [&](const Round &r) -> uint32_t {
-        if (r.units == 0)
+    auto place = [&](const Segment &s, int u, int b) -> uint32_t {
+        const int blk = s.first.blk + u, tl = s_expert[s.first.a] * 2 * blocks + (GATED ? blk : 2 * blk);
+        return ((uint32_t)(tl >> 3) * KB + b) * NEXT_SB + (tl & 7) * TILE16;
+    };
+    auto first_place = [&](Segment s) -> uint32_t {  // of this warp's, from segment s on
+        while (s.units > 0 && cut_of(s, warp) == cut_of(s, warp + 1))
+            s = after(s);
+        if (s.units == 0)
             return NONE;
-        const int group = warp / r.KW, blk = r.first.blk + group;
-        const int tl = s_expert[r.first.a] * 2 * blocks + (GATED ? blk : 2 * blk);
-        return (uint32_t)(tl >> 3) * KB * NEXT_SB + (tl & 7) * TILE16 + (warp - group * r.KW) * NEXT_SB;
+        const int c = cut_of(s, warp), u = (unsigned)c / (unsigned)KB;
+        return place(s, u, c - u * KB);
     };
     // The pair at `at` into one half of the warp's ring: 16 bytes a lane, 4864 in all.
     const uint64_t policy = policy_evict_first();
@@ -523,149 +510,158 @@ __global__ void __launch_bounds__(32 * W, 1) moe_gemm_kernel(const GemmParams p)
         }
         asm volatile("cp.async.commit_group;" ::: "memory");
     };
-    uint32_t here = place_of(next_active(round));
+    uint32_t here = first_place(seg);
     int half = 0;
     copy(here, 0);
 
-    for (; round.units > 0; round = round_at(after(round))) {
-        const int KW = round.KW, group = warp / KW, kw = warp - group * KW, blk = round.first.blk + group;
-        const bool active = group < round.units;
-        const int *list = p.plan->entries + s_offset[round.first.a];
-        const int n = s_offset[round.first.a + 1] - s_offset[round.first.a];
-        const uint32_t there = active ? place_of(next_active(round_at(after(round)))) : here;
+    for (; seg.units > 0; seg = after(seg)) {
+        const int *list = p.plan->entries + s_offset[seg.first.a];
+        const int n = s_offset[seg.first.a + 1] - s_offset[seg.first.a];
+        const int c0 = cut_of(seg, warp), c1 = cut_of(seg, warp + 1);
+        const uint32_t there = c0 < c1 ? first_place(after(seg)) : here;
+        // the result of unit u for the 8 tokens from col0 on
+        auto store = [&](const float (&v)[2][4], int col0, int u) {
+            const int blk = seg.first.blk + u;
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const int col = col0 + 2 * t + i;
+                if (col >= n)
+                    continue;
+                const int entry = __ldg(list + col);
+                if constexpr (GATED) {
+                    // rows g and g + 8 of the 16, in fragment order
+                    uint16_t *dst = p.h + (int64_t)entry * p.rows_out + (blk >> 2) * 64 + (g >> 1) * 16 + (blk & 3) * 4 + (g & 1);
+#pragma unroll
+                    for (int e8 = 0; e8 < 2; ++e8) {
+                        const float gate = v[0][2 * e8 + i] * 64.f, up = v[1][2 * e8 + i] * 64.f;
+                        const __nv_bfloat16 hb = __float2bfloat16_rn(gate / (1.f + __expf(-gate)) * up);
+                        dst[2 * e8] = *reinterpret_cast<const uint16_t *>(&hb);
+                    }
+                } else {
+                    float *dst = p.y + (int64_t)entry * p.rows_out + blk * 32 + g;
+#pragma unroll
+                    for (int r = 0; r < 2; ++r) {
+                        dst[16 * r] = v[r][i] * 64.f;
+                        dst[16 * r + 8] = v[r][2 + i] * 64.f;
+                    }
+                }
+            }
+        };
         // an expert with more than 8 NT tokens takes several passes over its tiles
         auto pass = [&](auto groups_of_8, int n0) {
             constexpr int N = decltype(groups_of_8)::value;
-            if (!active) {
-                if (KW > 1) {
-                    __syncthreads();
-                    __syncthreads();
+            if (c0 < c1) {
+                const bool again = n0 + 8 * N < n;
+                const uint4 *row[N];  // tokens past the last are its copies, and are not stored
+#pragma unroll
+                for (int nt = 0; nt < N; ++nt) {
+                    const int entry = __ldg(list + min(n0 + nt * 8 + g, n - 1));
+                    row[nt] = reinterpret_cast<const uint4 *>(
+                        p.xf + (int64_t)(GATED ? (unsigned)entry / (unsigned)p.topk : entry) * p.K + 16 * t);
                 }
-                return;
-            }
-            const bool again = n0 + 8 * N < n;
-            const uint4 *row[N];  // tokens past the last are its copies, and are not stored
+                int u = (unsigned)c0 / (unsigned)KB, b = c0 - u * KB;
+                bool begun = b == 0;  // the unit's first super-block is this warp's
+                uint32_t at = here;
+                float acc[2][N][4];
+                uint4 x[N][2];
 #pragma unroll
-            for (int nt = 0; nt < N; ++nt) {
-                const int entry = __ldg(list + min(n0 + nt * 8 + g, n - 1));
-                row[nt] = reinterpret_cast<const uint4 *>(
-                    p.xf + (int64_t)(GATED ? (unsigned)entry / (unsigned)p.topk : entry) * p.K + kw * 256 + 16 * t);
-            }
-            float acc[2][N][4];
+                for (int nt = 0; nt < N; ++nt) {
+                    x[nt][0] = ldg_row(row[nt] + b * 32);
+                    x[nt][1] = ldg_row(row[nt] + b * 32 + 1);
 #pragma unroll
-            for (int r = 0; r < 2; ++r)
-#pragma unroll
-                for (int nt = 0; nt < N; ++nt)
-                    acc[r][nt][0] = acc[r][nt][1] = acc[r][nt][2] = acc[r][nt][3] = 0.f;
-            uint4 x[N][2];
-#pragma unroll
-            for (int nt = 0; nt < N; ++nt) {
-                x[nt][0] = ldg_row(row[nt]);
-                x[nt][1] = ldg_row(row[nt] + 1);
-            }
-            uint32_t at = here;
-            for (int b = kw; b < KB; b += KW, at += KW * NEXT_SB) {
-                const bool more = b + KW < KB;
-                const uint32_t next = more ? at + KW * NEXT_SB : again ? here : there;
-                // this pair has come, and every lane has read the one before
-                asm volatile("cp.async.wait_group 0;" ::: "memory");
-                __syncwarp();
-                const uint32_t tiles = ring + half * 2 * TILE_BYTES;
-                half ^= 1;
-                copy(next, half);
-                uint4 sc[2][2], z[2];
-#pragma unroll
-                for (int r = 0; r < 2; ++r) {
-                    sc[r][0] = lds128(tiles + r * TILE_BYTES + 2048 + 16 * g);
-                    sc[r][1] = lds128(tiles + r * TILE_BYTES + 2048 + 128 + 16 * g);
-                    z[r] = lds128(tiles + r * TILE_BYTES + 2304 + 16 * g);
+                    for (int r = 0; r < 2; ++r)
+                        acc[r][nt][0] = acc[r][nt][1] = acc[r][nt][2] = acc[r][nt][3] = 0.f;
                 }
+                for (int c = c0; c < c1; ++c) {
+                    const bool more = c + 1 < c1, inside = b + 1 < KB;
+                    const uint32_t next = more ? (inside ? at + NEXT_SB : place(seg, u + 1, 0)) : again ? here : there;
+                    // this pair has come, and every lane has read the one before
+                    asm volatile("cp.async.wait_group 0;" ::: "memory");
+                    __syncwarp();
+                    const uint32_t tiles = ring + half * 2 * TILE_BYTES;
+                    half ^= 1;
+                    copy(next, half);
+                    uint4 sc[2][2], z[2];
 #pragma unroll
-                for (int sb = 0; sb < 4; ++sb) {
-                    uint4 ahead[N][2];
+                    for (int r = 0; r < 2; ++r) {
+                        sc[r][0] = lds128(tiles + r * TILE_BYTES + 2048 + 16 * g);
+                        sc[r][1] = lds128(tiles + r * TILE_BYTES + 2048 + 128 + 16 * g);
+                        z[r] = lds128(tiles + r * TILE_BYTES + 2304 + 16 * g);
+                    }
 #pragma unroll
-                    for (int nt = 0; nt < N; ++nt) {
-                        ahead[nt][0] = x[nt][0];
-                        ahead[nt][1] = x[nt][1];
-                        if (sb < 3 || more) {
-                            const uint4 *src = row[nt] + (sb < 3 ? 8 * (sb + 1) : KW * 32);
+                    for (int sb = 0; sb < 4; ++sb) {
+                        uint4 ahead[N][2];
+#pragma unroll
+                        for (int nt = 0; nt < N; ++nt) {
+                            // (of a last step, the unit's first columns once more)
+                            const uint4 *src = row[nt] + (sb < 3 ? b * 32 + 8 * (sb + 1) : inside ? b * 32 + 32 : 0);
                             ahead[nt][0] = ldg_row(src);
                             ahead[nt][1] = ldg_row(src + 1);
                         }
-                    }
 #pragma unroll
-                    for (int r = 0; r < 2; ++r) {
-                        const uint4 &c = sc[r][sb >> 1];
-                        tile_step<N>(lds128(tiles + r * TILE_BYTES + 512 * sb + 16 * lane), sb & 1 ? c.z : c.x,
-                                     sb & 1 ? c.w : c.y, (&z[r].x)[sb], x, acc[r]);
-                    }
+                        for (int r = 0; r < 2; ++r) {
+                            const uint4 &s = sc[r][sb >> 1];
+                            tile_step<N>(lds128(tiles + r * TILE_BYTES + 512 * sb + 16 * lane), sb & 1 ? s.z : s.x,
+                                         sb & 1 ? s.w : s.y, (&z[r].x)[sb], x, acc[r]);
+                        }
 #pragma unroll
-                    for (int nt = 0; nt < N; ++nt) {
-                        x[nt][0] = ahead[nt][0];
-                        x[nt][1] = ahead[nt][1];
+                        for (int nt = 0; nt < N; ++nt) {
+                            x[nt][0] = ahead[nt][0];
+                            x[nt][1] = ahead[nt][1];
+                        }
+                    }
+                    at = next;
+                    ++b;
+                    if (!inside || !more) {
+#pragma unroll
+                        for (int nt = 0; nt < N; ++nt) {
+                            if (begun && !inside) {
+                                const float v[2][4] = {{acc[0][nt][0], acc[0][nt][1], acc[0][nt][2], acc[0][nt][3]},
+                                                       {acc[1][nt][0], acc[1][nt][1], acc[1][nt][2], acc[1][nt][3]}};
+                                store(v, n0 + nt * 8, u);
+                            } else {
+#pragma unroll
+                                for (int r = 0; r < 2; ++r)
+                                    *reinterpret_cast<float4 *>(s_part + (((warp * 2 + begun) * NT + nt) * 2 + r) * 128 + lane * 4) =
+                                        make_float4(acc[r][nt][0], acc[r][nt][1], acc[r][nt][2], acc[r][nt][3]);
+                            }
+#pragma unroll
+                            for (int r = 0; r < 2; ++r)
+                                acc[r][nt][0] = acc[r][nt][1] = acc[r][nt][2] = acc[r][nt][3] = 0.f;
+                        }
+                        ++u;
+                        b = 0;
+                        begun = true;
                     }
                 }
-#pragma unroll
-                for (int nt = 0; nt < N; ++nt)
-                    row[nt] += KW * 32;
             }
-            // --- the sums of the warps that share the unit, and the result
-            if (KW > 1) {
-#pragma unroll
-                for (int r = 0; r < 2; ++r)
-#pragma unroll
-                    for (int nt = 0; nt < N; ++nt)
-                        *reinterpret_cast<float4 *>(&s_sum[warp][r * N + nt][lane * 4]) =
-                            make_float4(acc[r][nt][0], acc[r][nt][1], acc[r][nt][2], acc[r][nt][3]);
-                __syncthreads();
-            }
-#pragma unroll
-            for (int nt = 0; nt < N; ++nt) {
-                if (nt % KW != kw)
+            // --- the units that warps share: step x is warp ((x + 1) W - 1) / S's
+            const int S = seg.units * KB;
+            __syncthreads();
+            for (int u = warp; u < seg.units; u += W) {
+                const int w0 = (unsigned)((u * KB + 1) * W - 1) / (unsigned)S, w1 = (unsigned)((u + 1) * KB * W - 1) / (unsigned)S;
+                if (w0 == w1)
                     continue;
-                float v[2][4];
 #pragma unroll
-                for (int r = 0; r < 2; ++r) {
-                    v[r][0] = acc[r][nt][0], v[r][1] = acc[r][nt][1], v[r][2] = acc[r][nt][2], v[r][3] = acc[r][nt][3];
-                    if (KW > 1) {
-                        v[r][0] = v[r][1] = v[r][2] = v[r][3] = 0.f;
-#pragma unroll 4
-                        for (int q = 0; q < KW; ++q) {
-                            const float4 y = *reinterpret_cast<const float4 *>(&s_sum[warp - kw + q][r * N + nt][lane * 4]);
+                for (int nt = 0; nt < N; ++nt) {
+                    float v[2][4] = {};
+                    for (int w = w0; w <= w1; ++w) {
+                        if (cut_of(seg, w) == cut_of(seg, w + 1))
+                            continue;  // fewer steps than warps
+#pragma unroll
+                        for (int r = 0; r < 2; ++r) {
+                            const float4 y = *reinterpret_cast<const float4 *>(
+                                s_part + (((w * 2 + (w == w0)) * NT + nt) * 2 + r) * 128 + lane * 4);
                             v[r][0] += y.x;
                             v[r][1] += y.y;
                             v[r][2] += y.z;
                             v[r][3] += y.w;
                         }
                     }
-                }
-#pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    const int col = n0 + nt * 8 + 2 * t + i;
-                    if (col >= n)
-                        continue;
-                    const int entry = __ldg(list + col);
-                    if constexpr (GATED) {
-                        // rows g and g + 8 of the 16, in fragment order
-                        uint16_t *dst = p.h + (int64_t)entry * p.rows_out + (blk >> 2) * 64 + (g >> 1) * 16 + (blk & 3) * 4 + (g & 1);
-#pragma unroll
-                        for (int e8 = 0; e8 < 2; ++e8) {
-                            const float gate = v[0][2 * e8 + i] * 64.f, up = v[1][2 * e8 + i] * 64.f;
-                            const __nv_bfloat16 hb = __float2bfloat16_rn(gate / (1.f + __expf(-gate)) * up);
-                            dst[2 * e8] = *reinterpret_cast<const uint16_t *>(&hb);
-                        }
-                    } else {
-                        float *dst = p.y + (int64_t)entry * p.rows_out + blk * 32 + g;
-#pragma unroll
-                        for (int r = 0; r < 2; ++r) {
-                            dst[16 * r] = v[r][i] * 64.f;
-                            dst[16 * r + 8] = v[r][2 + i] * 64.f;
-                        }
-                    }
+                    store(v, n0 + nt * 8, u);
                 }
             }
-            if (KW > 1)  // the sums are read
-                __syncthreads();
+            __syncthreads();  // the parts are read
         };
         int n0 = 0;
         if constexpr (NT > 1)
@@ -706,14 +702,14 @@ cudaError_t launch_gemm(const GemmParams &p, int sm_count, cudaStream_t stream)
 {
     // with up to 8 tokens no expert has more
     const bool few = p.entries <= 8 * p.topk;
-    constexpr int W = 16;
-    const int smem = (12 * (p.experts + 1) + 15) / 16 * 16 + W * 4 * TILE_BYTES;
+    constexpr int W1 = 16, W2 = 12;
+    const int W = few ? W1 : W2, fixed = W * (4 * TILE_BYTES + (few ? 1 : 2) * 2048);
     static std::atomic<unsigned long long> done[2];
-    auto fn = few ? moe_gemm_kernel<GATED, 1, W> : moe_gemm_kernel<GATED, 2, W>;
-    const cudaError_t e = smem_opt_in_once(done[few], fn, 12 * (MAX_EXPERTS + 1) + 16 + W * 4 * TILE_BYTES);
+    auto fn = few ? moe_gemm_kernel<GATED, 1, W1> : moe_gemm_kernel<GATED, 2, W2>;
+    const cudaError_t e = smem_opt_in_once(done[few], fn, 12 * (MAX_EXPERTS + 1) + 16 + fixed);
     if (e != cudaSuccess)
         return e;
-    return launch_pdl(fn, dim3((unsigned)sm_count), dim3(32 * W), smem, stream, p);
+    return launch_pdl(fn, dim3((unsigned)sm_count), dim3(32 * W), (12 * (p.experts + 1) + 15) / 16 * 16 + fixed, stream, p);
 }
 
 struct Workspace {
