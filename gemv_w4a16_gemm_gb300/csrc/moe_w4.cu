@@ -81,15 +81,22 @@ struct RouteParams {
     int tokens, hidden, experts, topk;
     bool sigmoid, renormalize;
     float scale;
+    int groups;  // of 8 tokens that the products take at a time, at most
 };
 
-// What a super-block of a unit of an expert with n tokens costs, in quarters of
-// one with up to 8: one pass over its tiles for every 16 tokens (with more than
-// 8 tokens in all), or 8.
-__device__ __forceinline__ int step_cost(int n, bool sixteens)
+// What a super-block of a unit of an expert with n tokens costs, in eighths of
+// a pass with up to 8: passes of 32 (with `most` = 4 groups of 8 at a time), 16
+// (2) and 8 tokens.
+__device__ __forceinline__ int step_cost(int n, int most)
 {
-    const int full = sixteens ? (n + 7) / 16 : 0, left = n - 16 * full;
-    return 5 * full + (left > 0 ? (left + 7) / 8 * 4 : 0);
+    int cost = 0;
+    if (most >= 4)
+        for (; n > 16; n -= 32)
+            cost += 18;
+    if (most >= 2)
+        for (; n > 8; n -= 16)
+            cost += 12;
+    return cost + (n > 0 ? (n + 7) / 8 * 8 : 0);
 }
 
 __device__ __forceinline__ uint32_t order_key(float v)  // larger for larger v, at least 1; NaN is the least
@@ -282,7 +289,7 @@ __global__ void __launch_bounds__(32 * ROUTE_WARPS) moe_route_kernel(const Route
         for (int i = 0; i < PER; ++i) {
             const int e = 32 * i + lane, n = __popc(s_mask[e][0]) + __popc(s_mask[e][1]);
             const uint32_t active = __ballot_sync(~0u, n > 0);
-            const int c = step_cost(n, p.tokens > 8);
+            const int c = step_cost(n, p.groups);
             int xc = c, xn = n;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
@@ -374,6 +381,15 @@ __device__ __forceinline__ uint4 ldg_row(const uint4 *p)
     return v;
 }
 
+// a += s x, b += s y
+__device__ __forceinline__ void fma_pair(float &a, float &b, float s, float x, float y)
+{
+    asm("{\n\t.reg .b64 s, x, c;\n\tmov.b64 s, {%2, %2};\n\tmov.b64 x, {%3, %4};\n\tmov.b64 c, {%0, %1};\n\t"
+        "fma.rn.f32x2 c, s, x, c;\n\tmov.b64 {%0, %1}, c;\n\t}"
+        : "+f"(a), "+f"(b)
+        : "f"(s), "f"(x), "f"(y));
+}
+
 template <int V>
 struct Count {
     static constexpr int value = V;
@@ -407,10 +423,8 @@ __device__ __forceinline__ void tile_step(const uint4 &q, uint32_t s0, uint32_t 
         const float sa = bf16lo_to_f32(sc), sb = bf16hi_to_f32(sc);
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
-            acc[nt][0] = fmaf(sa, d[nt][0], acc[nt][0]);
-            acc[nt][1] = fmaf(sa, d[nt][1], acc[nt][1]);
-            acc[nt][2] = fmaf(sb, d[nt][2], acc[nt][2]);
-            acc[nt][3] = fmaf(sb, d[nt][3], acc[nt][3]);
+            fma_pair(acc[nt][0], acc[nt][1], sa, d[nt][0], d[nt][1]);
+            fma_pair(acc[nt][2], acc[nt][3], sb, d[nt][2], d[nt][3]);
         }
     }
 }
@@ -437,7 +451,7 @@ __global__ void __launch_bounds__(32 * W, 1) moe_gemm_kernel(const GemmParams p)
     __syncthreads();
 
     // A unit: an active expert's block of rows.  Share r of the whole cost ends at share * r +
-    // min(r, extra).  (At most 512 experts, 64 x 16 choices, 2048 blocks: less than 2^23.)
+    // min(r, extra).  (At most 512 experts, 64 x 16 choices, 2048 blocks: less than 2^24.)
     struct Unit {
         int a, blk;
     };
@@ -664,6 +678,9 @@ __global__ void __launch_bounds__(32 * W, 1) moe_gemm_kernel(const GemmParams p)
             __syncthreads();  // the parts are read
         };
         int n0 = 0;
+        if constexpr (NT > 2)
+            for (; n - n0 > 16; n0 += 32)
+                pass(Count<4>(), n0);
         if constexpr (NT > 1)
             for (; n - n0 > 8; n0 += 16)
                 pass(Count<2>(), n0);
@@ -697,19 +714,31 @@ __global__ void __launch_bounds__(128) moe_combine_kernel(const float *y, const 
     reinterpret_cast<uint2 *>(out + (int64_t)m * hidden)[d] = *reinterpret_cast<const uint2 *>(o);
 }
 
-template <bool GATED>
-cudaError_t launch_gemm(const GemmParams &p, int sm_count, cudaStream_t stream)
+template <bool GATED, int NT, int W>
+cudaError_t launch_variant(const GemmParams &p, int sm_count, cudaStream_t stream)
 {
-    // with up to 8 tokens no expert has more
-    const bool few = p.entries <= 8 * p.topk;
-    constexpr int W1 = 16, W2 = 12;
-    const int W = few ? W1 : W2, fixed = W * (4 * TILE_BYTES + (few ? 1 : 2) * 2048);
-    static std::atomic<unsigned long long> done[2];
-    auto fn = few ? moe_gemm_kernel<GATED, 1, W1> : moe_gemm_kernel<GATED, 2, W2>;
-    const cudaError_t e = smem_opt_in_once(done[few], fn, 12 * (MAX_EXPERTS + 1) + 16 + fixed);
+    constexpr int fixed = W * (4 * TILE_BYTES + NT * 2048);
+    static std::atomic<unsigned long long> done{0};
+    auto fn = moe_gemm_kernel<GATED, NT, W>;
+    const cudaError_t e = smem_opt_in_once(done, fn, 12 * (MAX_EXPERTS + 1) + 16 + fixed);
     if (e != cudaSuccess)
         return e;
     return launch_pdl(fn, dim3((unsigned)sm_count), dim3(32 * W), (12 * (p.experts + 1) + 15) / 16 * 16 + fixed, stream, p);
+}
+
+// Groups of 8 tokens at a time, and warps for their registers: with up to 8 tokens no expert has
+// more; 32 at a time pay where the experts have more than 16 on average.
+int groups_of(int tokens, int topk, int experts)
+{
+    return tokens <= 8 ? 1 : tokens * topk <= 16 * experts ? 2 : 4;
+}
+
+template <bool GATED>
+cudaError_t launch_gemm(const GemmParams &p, int groups, int sm_count, cudaStream_t stream)
+{
+    return groups == 1   ? launch_variant<GATED, 1, 16>(p, sm_count, stream)
+           : groups == 2 ? launch_variant<GATED, 2, 12>(p, sm_count, stream)
+                         : launch_variant<GATED, 4, 8>(p, sm_count, stream);
 }
 
 struct Workspace {
@@ -748,9 +777,10 @@ cudaError_t launch_moe(const Moe &a, int sm_count, void *workspace, cudaStream_t
     float *y = reinterpret_cast<float *>(base + w.y), *weights = reinterpret_cast<float *>(base + w.weights);
     Plan *plan = reinterpret_cast<Plan *>(base + w.plan);
 
+    const int groups = groups_of(a.tokens, a.topk, a.experts);
     RouteParams r = {static_cast<const __nv_bfloat16 *>(a.x), static_cast<const __nv_bfloat16 *>(a.router), a.bias, xf,
                      plan, weights, a.ids_out, a.weights_out, a.tokens, a.hidden, a.experts, a.topk, a.sigmoid,
-                     a.renormalize, a.scale};
+                     a.renormalize, a.scale, groups};
     cudaLaunchConfig_t cfg = {};
     const long long items = (long long)a.tokens * a.hidden / 16, per_cluster = ROUTE_CTAS * 32 * ROUTE_WARPS;
     const int others = (int)(items <= per_cluster ? 1 : items >= 8 * per_cluster ? 8 : items / per_cluster);
@@ -779,9 +809,9 @@ cudaError_t launch_moe(const Moe &a, int sm_count, void *workspace, cudaStream_t
                      a.hidden, a.inter};
     GemmParams down = {static_cast<const uint8_t *>(a.w2), h, plan, nullptr, y, a.tokens * a.topk, a.topk, a.experts,
                        a.inter, a.hidden};
-    e = launch_gemm<true>(up, sm_count, stream);
+    e = launch_gemm<true>(up, groups, sm_count, stream);
     if (e == cudaSuccess)
-        e = launch_gemm<false>(down, sm_count, stream);
+        e = launch_gemm<false>(down, groups, sm_count, stream);
     if (e != cudaSuccess)
         return e;
     const long long threads = (long long)a.tokens * (a.hidden / 4);
