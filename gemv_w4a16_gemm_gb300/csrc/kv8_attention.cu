@@ -99,10 +99,19 @@ __device__ __forceinline__ uint2 ldg_stream8(const void *p)
 __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
                                         uint32_t b0, uint32_t b1)
 {
-    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 "
-                 "{%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
-                 : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-                 : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 "
+        "{%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+// d = a b
+__device__ __forceinline__ void mma_f16_first(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                              uint32_t b0, uint32_t b1)
+{
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 "
+        "{%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%10, %10, %10, %10};"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
 }
 
 __device__ __forceinline__ uint32_t transpose8x8(uint32_t a)
@@ -330,20 +339,20 @@ __global__ void __launch_bounds__(32 * W * G, 1) kv8_attention_kernel(const Attn
         };
         const uint8_t *k_lane = p.c.k + h * page_bytes + g * D + 16 * t;
         const uint8_t *v_lane = p.c.v + h * page_bytes + 2 * t * D + VB * g;
-        const int64_t page_stride = page_bytes * p.c.kv_heads;
-        auto offset_of = [&](int i, int pg) -> int64_t {
-            return (pg < 0 ? 0 : pg) * page_stride + (((tile0 + i * W) & ((1 << per_page) - 1)) << 4) * D;
+        const uint32_t page_stride = (uint32_t)page_bytes * p.c.kv_heads;  // at most 2^25
+        auto offset_of = [&](int i, int pg) -> uint64_t {
+            return (uint64_t)(uint32_t)max(pg, 0) * page_stride + (((tile0 + i * W) & ((1 << per_page) - 1)) << 4) * D;
         };
         uint4 kr[KC][2];       // positions g, g + 8
         uint32_t vr[4][VW];    // positions 2t, 2t + 1, 2t + 8, 2t + 9
-        auto load_k = [&](int64_t at) {
+        auto load_k = [&](uint64_t at) {
 #pragma unroll
             for (int c = 0; c < KC; ++c) {
                 kr[c][0] = ldg_stream(k_lane + at + 64 * c);
                 kr[c][1] = ldg_stream(k_lane + at + 8 * D + 64 * c);
             }
         };
-        auto load_v = [&](int64_t at) {
+        auto load_v = [&](uint64_t at) {
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 const uint8_t *src = v_lane + at + ((i & 1) + (i >> 1) * 8) * D;
@@ -364,11 +373,27 @@ __global__ void __launch_bounds__(32 * W * G, 1) kv8_attention_kernel(const Attn
             }
         };
 
+        // The tile after the next goes to L2 already: a lane prefetches 128 bytes of its K or V.
+        // (64 x 16000 x 8 heads: 349 us without, 318 with two tiles ahead, 354 with eight.)
+        constexpr int LINES = D / 8;  // of a tile's K
+        const uint8_t *line = (lane & (LINES < 16 ? LINES : 16) ? p.c.v : p.c.k) + h * page_bytes +
+                              (lane & (LINES < 16 ? LINES - 1 : 15)) * 128;
+        auto prefetch = [&](uint64_t at) {
+            if (lane < 2 * LINES)
+                asm volatile("prefetch.global.L2 [%0];" ::"l"(line + at));
+            if constexpr (LINES > 16)
+                asm volatile("prefetch.global.L2 [%0];" ::"l"(line + at + 16 * 128));
+        };
+
         int pages = page_of(lane), pages_next = -1;
+        int page = __shfl_sync(~0u, pages, 0), page_next = __shfl_sync(~0u, pages, 1);  // of this tile, of the next
+        uint64_t next = offset_of(1, page_next);
         if (n > 0) {
-            const int64_t at = offset_of(0, __shfl_sync(~0u, pages, 0));
+            const uint64_t at = offset_of(0, page);
             load_k(at);
             load_v(at);
+            if (n > 1)
+                prefetch(next);
         }
         float sks = scale_of(p.c.k_scale, pages), svs = scale_of(p.c.v_scale, pages);
         float sks_next = 0.f, svs_next = 0.f;
@@ -427,7 +452,6 @@ __global__ void __launch_bounds__(32 * W * G, 1) kv8_attention_kernel(const Attn
                 o[nt][j][0] = o[nt][j][1] = o[nt][j][2] = o[nt][j][3] = 0.f;
         }
 
-        float lsvs = fmaxf(__log2f(svs), -64.f);
         for (int i = 0; i < n; ++i) {
             const int at32 = i & 31;
             if (at32 == 0)
@@ -436,19 +460,15 @@ __global__ void __launch_bounds__(32 * W * G, 1) kv8_attention_kernel(const Attn
                 sks_next = scale_of(p.c.k_scale, pages_next);
                 svs_next = scale_of(p.c.v_scale, pages_next);
             }
-            const bool hole = __shfl_sync(~0u, pages, at32) < 0;
+            const bool hole = page < 0;
             const float sk = __shfl_sync(~0u, sks, at32), sv = __shfl_sync(~0u, svs, at32);
-            const float lsv = __shfl_sync(~0u, lsvs, at32);
-            const int64_t next = offset_of(i + 1, __shfl_sync(~0u, at32 == 31 ? pages_next : pages, (i + 1) & 31));
+            const float lsv = fmaxf(__log2f(sv), -64.f);
+            const int page_far = __shfl_sync(~0u, at32 >= 30 ? pages_next : pages, (i + 2) & 31);
+            const uint64_t far = offset_of(i + 2, page_far);
 
             // S^T, in two chains of MMAs where one would be long
             constexpr int CH = NT == 1 && KC > 1 ? 2 : 1;
             float s[CH][NT][4];
-#pragma unroll
-            for (int ch = 0; ch < CH; ++ch)
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
-                    s[ch][nt][0] = s[ch][nt][1] = s[ch][nt][2] = s[ch][nt][3] = 0.f;
 #pragma unroll
             for (int w = 0; w < 4; ++w)
 #pragma unroll
@@ -458,29 +478,41 @@ __global__ void __launch_bounds__(32 * W * G, 1) kv8_attention_kernel(const Attn
                     codes_to_f16<FP8>((&kr[c][1].x)[w], a1, a3);
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt)
-                        mma_f16(s[c % CH][nt], a0, a1, a2, a3, qf[nt][c][2 * w], qf[nt][c][2 * w + 1]);
+                        if (w == 0 && c < CH)
+                            mma_f16_first(s[c % CH][nt], a0, a1, a2, a3, qf[nt][c][2 * w], qf[nt][c][2 * w + 1]);
+                        else
+                            mma_f16(s[c % CH][nt], a0, a1, a2, a3, qf[nt][c][2 * w], qf[nt][c][2 * w + 1]);
                 }
             if (i + 1 < n)
                 load_k(next);
+            if (i + 2 < n)
+                prefetch(far);
             const int pos = (tile0 + i * W) << 4;
             const bool edge = pos + 16 > lim_min || pos < lo_max || hole;
-            bool grow = false;
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                    float x = s[0][nt][e];
                     if constexpr (CH == 2)
-                        x += s[CH - 1][nt][e];
-                    x *= factor[nt][e & 1] * sk;
-                    if (edge) {
+                        s[0][nt][e] += s[CH - 1][nt][e];
+                    s[0][nt][e] *= factor[nt][e & 1] * sk;
+                }
+            if (edge) {
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
                         const int at = pos + g + 8 * (e >> 1), lim = limit[nt][e & 1];
                         if (at >= lim || (p.window > 0 && at < lim - p.window) || hole)
-                            x = -INFINITY;
+                            s[0][nt][e] = -INFINITY;
                     }
-                    s[0][nt][e] = x;
-                    grow |= x + lsv > m[nt][e & 1] + SLACK;
-                }
+            }
+            bool grow = false;
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int e = 0; e < 2; ++e)
+                    grow |= fmaxf(s[0][nt][e], s[0][nt][e + 2]) > m[nt][e] + (SLACK - lsv);
             if (__any_sync(~0u, grow)) {
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
@@ -538,11 +570,13 @@ __global__ void __launch_bounds__(32 * W * G, 1) kv8_attention_kernel(const Attn
                 }
             if (i + 1 < n)
                 load_v(next);
+            page = page_next;
+            page_next = page_far;
+            next = far;
             if (at32 == 31) {
                 pages = pages_next;
                 sks = sks_next;
                 svs = svs_next;
-                lsvs = fmaxf(__log2f(svs), -64.f);
             }
         }
 
