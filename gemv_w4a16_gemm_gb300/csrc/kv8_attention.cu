@@ -73,6 +73,7 @@ struct AttnParams {
     __nv_bfloat16 *out;
     float *lse;
     int queries, heads, group, rows, row_tiles, window;
+    int group_inv;  // row / group = row * group_inv >> 16 for the at most 64 rows
     float scale_log2;
     // Arrivals, zero between calls, by the CTA that starts the unit (at most one of a CTA's units
     // starts in it without ending in it) and by the first slot of a join.
@@ -278,18 +279,27 @@ __global__ void __launch_bounds__(32 * W * G, 1) kv8_attention_kernel(const Attn
     const int from = begin + (int)((long long)(end - begin) * grp / G);
     const int to = begin + (int)((long long)(end - begin) * (grp + 1) / G);
 
-    // row r of a unit, permuted index at (see where the sums are stored), of the joined sums
-    auto finish = [&](const Unit &x, int r, int at, float2 v, float mm, float ll) {
-        const int h = x.hr / p.row_tiles, rr = (x.hr % p.row_tiles) * ROWS + r;
+    // Row r of a unit, with its joined reference and sum: where it goes and what its sums are
+    // multiplied by; dims are stored by store_dims, two at permuted index `at` (see where the warps
+    // leave their sums).
+    struct RowOut {
+        __nv_bfloat16 *to;  // null: no such row
+        float inv;
+    };
+    auto row_out = [&](const Unit &x, int r, float mm, float ll, bool first) -> RowOut {
+        const int h = (unsigned)x.hr / (unsigned)p.row_tiles, rr = (x.hr - h * p.row_tiles) * ROWS + r;
         if (rr >= p.rows)
-            return;
-        const int qi = rr / p.group, head = h * p.group + rr % p.group;
-        const int d = VB * ((at & 15) >> 1) + 2 * (at >> 4);
-        const float inv = ll > 0.f ? 1.f / ll * (1.f / P_SCALE) : 0.f;
-        const int64_t row = ((int64_t)x.b * p.queries + qi) * p.heads + head;
-        *reinterpret_cast<__nv_bfloat162 *>(p.out + row * D + d) = __floats2bfloat162_rn(v.x * inv, v.y * inv);
-        if (at == 0 && p.lse != nullptr)
+            return {nullptr, 0.f};
+        const int qi = (rr * p.group_inv) >> 16;
+        const int64_t row = ((int64_t)x.b * p.queries + qi) * p.heads + h * p.group + (rr - qi * p.group);
+        if (first && p.lse != nullptr)
             p.lse[row] = ll > 0.f ? (mm + log2f(ll)) * 0.6931471805599453f : -INFINITY;
+        return {p.out + row * D, ll > 0.f ? __fdividef(1.f / P_SCALE, ll) : 0.f};
+    };
+    auto store_dims = [&](const RowOut &o, int at, float2 v) {
+        if (o.to != nullptr)
+            *reinterpret_cast<__nv_bfloat162 *>(o.to + VB * ((at & 15) >> 1) + 2 * (at >> 4)) =
+                __floats2bfloat162_rn(v.x * o.inv, v.y * o.inv);
     };
 
     int b = from < to ? sequence_at(from) : 0;
@@ -308,7 +318,7 @@ __global__ void __launch_bounds__(32 * W * G, 1) kv8_attention_kernel(const Attn
         uint4 raw[NT][KC][2];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
-            const unsigned r = min(row0 + nt * 8 + g, p.rows - 1), qi = r / (unsigned)p.group;
+            const int r = min(row0 + nt * 8 + g, p.rows - 1), qi = (r * p.group_inv) >> 16;
             const __nv_bfloat16 *src = p.q + ((int64_t)b * p.queries + qi) * p.q_stride +
                                        (int64_t)(h * p.group + (r - qi * p.group)) * D + 16 * t;
 #pragma unroll
@@ -433,7 +443,7 @@ __global__ void __launch_bounds__(32 * W * G, 1) kv8_attention_kernel(const Attn
                 const int upc = __shfl_sync(~0u, up, (2 * t + e) * 4);
                 factor[nt][e] = p.scale_log2 * __uint_as_float((uint32_t)(127 - upc / 2) << 23) *
                                 __uint_as_float((uint32_t)(127 - (upc - upc / 2)) << 23);
-                limit[nt][e] = len - p.queries + min(rr, p.rows - 1) / p.group + 1;
+                limit[nt][e] = len - p.queries + ((min(rr, p.rows - 1) * p.group_inv) >> 16) + 1;
                 lim_min = min(lim_min, limit[nt][e]);
             }
         }
@@ -611,32 +621,39 @@ __global__ void __launch_bounds__(32 * W * G, 1) kv8_attention_kernel(const Attn
         asm volatile("bar.sync %0, %1;" ::"r"(1 + grp), "n"(32 * W) : "memory");
         const bool whole = j0 == 0 && u == unit.end;
         const int cut = 2 * grp + (j0 == 0 ? 1 : 0);
-#pragma unroll
-        for (int it = 0; it < ROWS * (D / 2) / (32 * W); ++it) {
-            const int i = tid % (32 * W) + it * 32 * W;
-            const int r = i / (D / 2), at = 2 * (i % (D / 2));
-            float mm = NEG, ll = 0.f;
-            float2 x = make_float2(0.f, 0.f);
+        {
+            constexpr int TPR = 32 * W / ROWS;  // threads of a row
+            const int r = tid % (32 * W) / TPR, first = tid % TPR;
+            float mm = NEG, ll = 0.f, a[W];
 #pragma unroll
             for (int w = 0; w < W; ++w)
                 mm = fmaxf(mm, s_m[w * ROWS + r]);
 #pragma unroll
             for (int w = 0; w < W; ++w) {
-                const float a = ex2(s_m[w * ROWS + r] - mm);
-                const float2 y = *reinterpret_cast<const float2 *>(s_o + (w * ROWS + r) * SM::PITCH + at);
-                ll += a * s_l[w * ROWS + r];
-                x.x += a * y.x;
-                x.y += a * y.y;
+                a[w] = ex2(s_m[w * ROWS + r] - mm);
+                ll += a[w] * s_l[w * ROWS + r];
             }
+            float *part = part_of(cut);
+            RowOut out = {};
             if (whole) {
-                finish(unit, r, at, x, mm, ll);
-            } else {
-                float *dst = part_of(cut);
-                *reinterpret_cast<float2 *>(dst + r * D + at) = x;
-                if (at == 0) {
-                    dst[ROWS * D + r] = mm;
-                    dst[ROWS * D + ROWS + r] = ll;
+                out = row_out(unit, r, mm, ll, first == 0);
+            } else if (first == 0) {
+                part[ROWS * D + r] = mm;
+                part[ROWS * D + ROWS + r] = ll;
+            }
+#pragma unroll 4
+            for (int at = 2 * first; at < D; at += 2 * TPR) {
+                float2 x = make_float2(0.f, 0.f);
+#pragma unroll
+                for (int w = 0; w < W; ++w) {
+                    const float2 y = *reinterpret_cast<const float2 *>(s_o + (w * ROWS + r) * SM::PITCH + at);
+                    x.x += a[w] * y.x;
+                    x.y += a[w] * y.y;
                 }
+                if (whole)
+                    store_dims(out, at, x);
+                else
+                    *reinterpret_cast<float2 *>(part + r * D + at) = x;
             }
         }
         if (!whole && tid % (32 * W) == 0)
@@ -660,31 +677,37 @@ __global__ void __launch_bounds__(32 * W * G, 1) kv8_attention_kernel(const Attn
         const int c0 = whole ? cta : (int)(((long long)(unit.begin + 1) * P - 1) / U);
         const int c1 = whole ? cta : (int)(((long long)unit.end * P - 1) / U);
         auto slot_of = [&](int c) { return p.part + (int64_t)(2 * c + (c == c0 ? 1 : 0)) * SM::PART; };
-        for (int i = tid; i < ROWS * (D / 2); i += THREADS) {
-            const int r = i / (D / 2), at = 2 * (i % (D / 2));
+        constexpr int TPR = THREADS / ROWS;
+        const int r = tid / TPR, first = tid % TPR;  // this thread's row, r < ROWS but for the remainder of THREADS
+        if (r < ROWS) {
             float mm = NEG, ll = 0.f;
-            float2 x = make_float2(0.f, 0.f);
             for (int q = k0; q < k; ++q)
                 if (s_cut[q].begin >= 0)
                     mm = fmaxf(mm, part_of(q)[ROWS * D + r]);
             for (int q = k0; q < k; ++q)
-                if (s_cut[q].begin >= 0) {
-                    const float *src = part_of(q);
-                    const float a = ex2(src[ROWS * D + r] - mm);
-                    const float2 y = *reinterpret_cast<const float2 *>(src + r * D + at);
-                    ll += a * src[ROWS * D + ROWS + r];
-                    x.x += a * y.x;
-                    x.y += a * y.y;
-                }
+                if (s_cut[q].begin >= 0)
+                    ll += ex2(part_of(q)[ROWS * D + r] - mm) * part_of(q)[ROWS * D + ROWS + r];
+            float *dst = slot_of(cta);
+            RowOut out = {};
             if (whole) {
-                finish(unit, r, at, x, mm, ll);
-            } else {
-                float *dst = slot_of(cta);
-                *reinterpret_cast<float2 *>(dst + r * D + at) = x;
-                if (at == 0) {
-                    dst[ROWS * D + r] = mm;
-                    dst[ROWS * D + ROWS + r] = ll;
-                }
+                out = row_out(unit, r, mm, ll, first == 0);
+            } else if (first == 0) {
+                dst[ROWS * D + r] = mm;
+                dst[ROWS * D + ROWS + r] = ll;
+            }
+            for (int at = 2 * first; at < D; at += 2 * TPR) {
+                float2 x = make_float2(0.f, 0.f);
+                for (int q = k0; q < k; ++q)
+                    if (s_cut[q].begin >= 0) {
+                        const float a = ex2(part_of(q)[ROWS * D + r] - mm);
+                        const float2 y = *reinterpret_cast<const float2 *>(part_of(q) + r * D + at);
+                        x.x += a * y.x;
+                        x.y += a * y.y;
+                    }
+                if (whole)
+                    store_dims(out, at, x);
+                else
+                    *reinterpret_cast<float2 *>(dst + r * D + at) = x;
             }
         }
         if (whole)
@@ -705,58 +728,65 @@ __global__ void __launch_bounds__(32 * W * G, 1) kv8_attention_kernel(const Attn
         };
         // joins `of` slots, `step` CTAs apart from CTA f on, into the first of them or the result
         auto join = [&](int f, int step, int of, bool last) {
-            constexpr int ITEMS = (ROWS * (D / 2) + THREADS - 1) / THREADS, AT_ONCE = 16;
-            float row_m[ITEMS], row_l[ITEMS];
-#pragma unroll
-            for (int it = 0; it < ITEMS; ++it) {
-                const int i = tid + it * THREADS;
-                if (i >= ROWS * (D / 2))
-                    continue;
-                const int r = i / (D / 2), at = 2 * (i % (D / 2));
-                float mm = NEG, ll = 0.f;
-                float2 x = make_float2(0.f, 0.f);
+            constexpr int ITEMS = (D / 2 + TPR - 1) / TPR, AT_ONCE = 16;
+            float mm = NEG, ll = 0.f;
+            float2 x[ITEMS] = {};
+            if (r < ROWS)
                 for (int q0 = 0; q0 < of; q0 += AT_ONCE) {
                     float pm[AT_ONCE], pl[AT_ONCE];
-                    float2 y[AT_ONCE];
 #pragma unroll
                     for (int q = 0; q < AT_ONCE; ++q) {  // all loads before any use
-                        const float *src = slot_of(f + min(q0 + q, of - 1) * step);
-                        pm[q] = __ldcg(src + ROWS * D + r);
-                        pl[q] = __ldcg(src + ROWS * D + ROWS + r);
-                        y[q] = __ldcg(reinterpret_cast<const float2 *>(src + r * D + at));
+                        const float *src = slot_of(f + min(q0 + q, of - 1) * step) + ROWS * D + r;
+                        pm[q] = __ldcg(src);
+                        pl[q] = __ldcg(src + ROWS);
                     }
+                    float2 y[ITEMS][AT_ONCE];
+#pragma unroll
+                    for (int i = 0; i < ITEMS; ++i)
+#pragma unroll
+                        for (int q = 0; q < AT_ONCE; ++q)
+                            y[i][q] = __ldcg(reinterpret_cast<const float2 *>(
+                                slot_of(f + min(q0 + q, of - 1) * step) + r * D + 2 * min(first + i * TPR, D / 2 - 1)));
                     float top = mm;
 #pragma unroll
                     for (int q = 0; q < AT_ONCE; ++q)
                         top = fmaxf(top, pm[q]);
                     const float keep = ex2(mm - top);
-                    ll *= keep;
-                    x.x *= keep;
-                    x.y *= keep;
                     mm = top;
+                    ll *= keep;
+#pragma unroll
+                    for (int i = 0; i < ITEMS; ++i) {
+                        x[i].x *= keep;
+                        x[i].y *= keep;
+                    }
 #pragma unroll
                     for (int q = 0; q < AT_ONCE; ++q) {
                         const float a = q0 + q < of ? ex2(pm[q] - mm) : 0.f;
                         ll += a * pl[q];
-                        x.x += a * y[q].x;
-                        x.y += a * y[q].y;
+#pragma unroll
+                        for (int i = 0; i < ITEMS; ++i) {
+                            x[i].x += a * y[i][q].x;
+                            x[i].y += a * y[i][q].y;
+                        }
                     }
                 }
-                if (last)
-                    finish(unit, r, at, x, mm, ll);
-                else
-                    *reinterpret_cast<float2 *>(slot_of(f) + r * D + at) = x;
-                row_m[it] = mm;
-                row_l[it] = ll;
-            }
-            if (!last) {
-                __syncthreads();  // every thread has read the first slot's m and l
+            if (last) {
+                const RowOut out = r < ROWS ? row_out(unit, r, mm, ll, first == 0) : RowOut{nullptr, 0.f};
 #pragma unroll
-                for (int it = 0; it < ITEMS; ++it) {
-                    const int i = tid + it * THREADS;
-                    if (i < ROWS * (D / 2) && i % (D / 2) == 0) {
-                        slot_of(f)[ROWS * D + i / (D / 2)] = row_m[it];
-                        slot_of(f)[ROWS * D + ROWS + i / (D / 2)] = row_l[it];
+                for (int i = 0; i < ITEMS; ++i)
+                    if (first + i * TPR < D / 2)
+                        store_dims(out, 2 * (first + i * TPR), x[i]);
+            } else {
+                __syncthreads();  // every thread has read the first slot
+                if (r < ROWS) {
+                    float *dst = slot_of(f);
+#pragma unroll
+                    for (int i = 0; i < ITEMS; ++i)
+                        if (first + i * TPR < D / 2)
+                            *reinterpret_cast<float2 *>(dst + r * D + 2 * (first + i * TPR)) = x[i];
+                    if (first == 0) {
+                        dst[ROWS * D + r] = mm;
+                        dst[ROWS * D + ROWS + r] = ll;
                     }
                 }
             }
@@ -828,6 +858,7 @@ cudaError_t launch_kv8_attention(const Kv8 &c, const void *q, int64_t q_stride, 
     p.heads = heads;
     p.group = heads / c.kv_heads;
     p.rows = queries * p.group;
+    p.group_inv = 65536 / p.group + 1;
     const int tr = tile_rows(p.rows, c.head_dim);
     p.row_tiles = (p.rows + tr - 1) / tr;
     p.window = window;
