@@ -187,9 +187,10 @@ int kv8_attention(const w4q_kv8_cache *cache, const void *q, int64_t q_stride, v
         return W4Q_ERR_INVALID_ARG;
     if (heads % c.kv_heads != 0 || queries > MAX_ROWS || (int64_t)queries * (heads / c.kv_heads) > MAX_ROWS)
         return W4Q_ERR_UNSUPPORTED;
-    // the pieces of 64 positions of all (sequence, kv head, 8 query rows) are counted in 32 bits
+    // the pieces of 64 positions of all (sequence, kv head, 8 query rows), and their beginnings, are
+    // counted in 32 bits
     const int64_t tiles = ((int64_t)queries * (heads / c.kv_heads) + 7) / 8;
-    if ((((int64_t)c.width << c.page_log2) / 64 + 2) * c.seqs * c.kv_heads * tiles >= 0x7fffffffLL)
+    if ((((int64_t)c.width << c.page_log2) / 64 + 8) * c.seqs * c.kv_heads * tiles >= 0x7fffffffLL)
         return W4Q_ERR_UNSUPPORTED;
     st = check_stride(q_stride, heads, c.head_dim);
     if (st != W4Q_OK)

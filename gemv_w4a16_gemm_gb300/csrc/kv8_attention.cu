@@ -61,6 +61,7 @@ constexpr float NEG = -1e30f;      // the reference before any position was seen
 constexpr float SLACK = 8.f;       // the reference may lag this far (log2) behind the largest term
 constexpr float P_SCALE = 128.f;   // 2^7: P <= 2^8 becomes at most 2^15 in f16
 constexpr int W = 4;               // warps of a group
+constexpr int START = 3;           // a unit's beginning costs about as much as this many chunks
 constexpr int SNAP = 16;           // units up to this many chunks stay in one CTA
 constexpr int JOIN = 16;           // neighbours whose partial sums are joined first ...
 constexpr int JOIN_ONCE = 48;      // ... where a unit has more parts than this
@@ -170,7 +171,7 @@ __device__ __forceinline__ Span span_of(const AttnParams &p, int len)
 
 // Dynamic shared memory of a CTA: the warps' sums, the groups' sums of the two
 // units that a group's range can cut (0: the one that it continues, 1: the one
-// that it begins), then the sequences' lengths and their chunks' prefix sums.
+// that it begins), then the sequences' lengths and their places' prefix sums.
 template <int D, int NT, int G>
 struct Smem {
     static constexpr int ROWS = 8 * NT;
@@ -181,9 +182,9 @@ struct Smem {
     static size_t bytes(int seqs) { return BASE + (size_t)(2 * seqs + 1) * 4; }
 };
 
-// A unit of the line.
+// A unit of the line: START places for its beginning, then its chunks.
 struct Unit {
-    int begin, end;  // its chunks in the line; begin < 0: none
+    int begin, end;  // its places in the line; begin < 0: none
     int b, hr;
 };
 
@@ -197,7 +198,7 @@ __global__ void __launch_bounds__(32 * W * G, 1) kv8_attention_kernel(const Attn
     __shared__ int s_warp[W * G];
     __shared__ Unit s_cut[2 * G];
     int *s_len = reinterpret_cast<int *>(smem + SM::BASE);  // [seqs]
-    int *s_prefix = s_len + p.c.seqs;                       // [seqs + 1] chunks before a sequence
+    int *s_prefix = s_len + p.c.seqs;                       // [seqs + 1] places (of one unit) before a sequence
 
     const int tid = threadIdx.x, lane = tid & 31, grp = tid / (32 * W), warp = (tid >> 5) % W;
     const int g = lane >> 2, t = lane & 3;
@@ -211,7 +212,7 @@ __global__ void __launch_bounds__(32 * W * G, 1) kv8_attention_kernel(const Attn
     pdl_wait();
     pdl_launch_dependents();
 
-    // --- prefix sums of the sequences' chunks
+    // --- prefix sums of the sequences' places
     {
         int base = 0;
         for (int b0 = 0; b0 < p.c.seqs; b0 += THREADS) {
@@ -220,7 +221,7 @@ __global__ void __launch_bounds__(32 * W * G, 1) kv8_attention_kernel(const Attn
             if (b < p.c.seqs) {
                 const int len = min(max(p.c.lens[b], 0), p.c.width << p.c.page_log2);
                 s_len[b] = len;
-                n = span_of(p, len).chunks;
+                n = span_of(p, len).chunks + START;
             }
             int x = n;
 #pragma unroll
@@ -270,8 +271,8 @@ __global__ void __launch_bounds__(32 * W * G, 1) kv8_attention_kernel(const Attn
         if (u >= U)
             return U;
         const int b = sequence_at(u), seq0 = s_prefix[b] * HR;
-        const unsigned chunks = s_prefix[b + 1] - s_prefix[b];
-        return chunks <= SNAP ? seq0 + (unsigned)(u - seq0) / chunks * chunks : u;
+        const unsigned places = s_prefix[b + 1] - s_prefix[b];
+        return places <= START + SNAP ? seq0 + (unsigned)(u - seq0) / places * places : u;
     };
     const int begin = snapped((int)((long long)U * cta / P)), end = snapped((int)((long long)U * (cta + 1) / P));
     if (begin >= end)
@@ -308,11 +309,14 @@ __global__ void __launch_bounds__(32 * W * G, 1) kv8_attention_kernel(const Attn
             ++b;
         const int len = s_len[b], seq0 = s_prefix[b] * HR;
         const Span sp = span_of(p, len);
-        const int hr = (int)((unsigned)(u - seq0) / (unsigned)sp.chunks);
-        const Unit unit = {seq0 + hr * sp.chunks, seq0 + (hr + 1) * sp.chunks, b, hr};
-        const int j0 = u - unit.begin, j1 = min(to, unit.end) - unit.begin;
+        const int places = sp.chunks + START;
+        const int hr = (int)((unsigned)(u - seq0) / (unsigned)places);
+        const Unit unit = {seq0 + hr * places, seq0 + (hr + 1) * places, b, hr};
+        const int j0 = max(0, u - unit.begin - START), j1 = max(0, min(to, unit.end) - unit.begin - START);
+        u = min(to, unit.end);
+        if (j0 == j1)
+            continue;  // nothing but a unit's beginning
         const int h = (int)((unsigned)hr / (unsigned)p.row_tiles), row0 = (hr - h * p.row_tiles) * ROWS;
-        u = unit.begin + j1;
 
         // --- the query rows' loads: rows beyond the last are its copies, and are dropped at the end
         uint4 raw[NT][KC][2];
@@ -619,11 +623,11 @@ __global__ void __launch_bounds__(32 * W * G, 1) kv8_attention_kernel(const Attn
                     *reinterpret_cast<float2 *>(s_o + (warp * ROWS + nt * 8 + 2 * t + e) * SM::PITCH + 16 * i + 2 * g) =
                         make_float2(o[nt][i][e], o[nt][i][e + 2]);
         asm volatile("bar.sync %0, %1;" ::"r"(1 + grp), "n"(32 * W) : "memory");
-        const bool whole = j0 == 0 && u == unit.end;
+        const bool whole = j0 == 0 && j1 == sp.chunks;
         const int cut = 2 * grp + (j0 == 0 ? 1 : 0);
         {
             constexpr int TPR = 32 * W / ROWS;  // threads of a row
-            const int r = tid % (32 * W) / TPR, first = tid % TPR;
+            const int me = tid % (32 * W), r = min(me / TPR, ROWS - 1), first = me < TPR * ROWS ? me % TPR : D;
             float mm = NEG, ll = 0.f, a[W];
 #pragma unroll
             for (int w = 0; w < W; ++w)
@@ -672,9 +676,9 @@ __global__ void __launch_bounds__(32 * W * G, 1) kv8_attention_kernel(const Attn
         const int k0 = k;  // this unit's parts in the CTA: those of its cuts k0 .. k - 1
         while (k < 2 * G && (s_cut[k].begin < 0 || s_cut[k].begin == unit.begin))
             ++k;
-        const bool whole = unit.begin >= begin && unit.end <= end;
+        const bool whole = unit.begin + START >= begin && unit.end <= end;
         // a CTA's slot 1 in the workspace holds the unit that begins in it, slot 0 the one that it continues
-        const int c0 = whole ? cta : (int)(((long long)(unit.begin + 1) * P - 1) / U);
+        const int c0 = whole ? cta : (int)(((long long)(unit.begin + START + 1) * P - 1) / U);
         const int c1 = whole ? cta : (int)(((long long)unit.end * P - 1) / U);
         auto slot_of = [&](int c) { return p.part + (int64_t)(2 * c + (c == c0 ? 1 : 0)) * SM::PART; };
         constexpr int TPR = THREADS / ROWS;
@@ -821,17 +825,21 @@ cudaError_t launch_variant(AttnParams &p, int sm_count, cudaStream_t stream)
         return e;
     // no more CTAs than the longest sequences that the table can hold give chunks
     const long long most = (((long long)p.c.width << p.c.page_log2) + 16 * W - 1) / (16 * W);
-    const long long units = (long long)p.c.seqs * p.c.kv_heads * p.row_tiles * (most > 0 ? most : 1);
+    const long long units = (long long)p.c.seqs * p.c.kv_heads * p.row_tiles * most;
     const long long grid = units < (long long)sm_count ? units : (long long)sm_count;
     return launch_pdl(fn, dim3((unsigned)grid), dim3(32 * W * G), SM::bytes(p.c.seqs), stream, p);
 }
 
-// Query rows of a tile: the accumulators (D / 4 registers per 8 rows) have to fit.
+// Query rows of a tile: the accumulators (D / 4 registers per 8 rows) have to
+// fit.  Of 24 and 32 (head_dim 64) what leaves fewer rows empty: 20 rows take
+// 42 us in a tile of 32, 32 in one of 24 (48 sequences, a window of 1024).
 int tile_rows(int rows, int D)
 {
     if (rows <= 8 || D == 256)
         return 8;
-    return rows <= 16 || D == 128 ? 16 : 32;
+    if (rows <= 16 || D == 128)
+        return 16;
+    return (rows + 23) / 24 * 24 < (rows + 31) / 32 * 32 ? 24 : 32;
 }
 
 }  // namespace
@@ -875,6 +883,8 @@ cudaError_t launch_kv8_attention(const Kv8 &c, const void *q, int64_t q_stride, 
             W4Q_ATTN(64, 1, 5);
         if (tr == 16)
             W4Q_ATTN(64, 2, 4);
+        if (tr == 24)
+            W4Q_ATTN(64, 3, 3);
         W4Q_ATTN(64, 4, 3);
     }
     if (c.head_dim == 128) {
