@@ -31,9 +31,10 @@
 // pages stay row-major, and a lane only ever uses bytes that it has loaded
 // itself.  So the cache goes from global memory to registers and nowhere else:
 // the next tile's K is loaded as soon as this tile's is used up, its V likewise,
-// which keeps 2 to 4 KB a warp on the way.  (The same bytes through a ring of
-// cp.async in shared memory took 466 instructions a tile instead of 3xx and half
-// as long again: 434 us instead of xxx for 64 x 16000 x 8 heads.)
+// and the one after it is on its way to L2.  (The same bytes through a ring of
+// cp.async in shared memory: 434 us instead of 347 for 64 x 16000 x 8 heads of
+// 128; without the prefetch to L2 349, with it 319, without spills 311: 2.1 GB
+// at 6.76 TB/s, 99% of the measured copy bandwidth.)
 //
 // Work.  One chunk = 64 positions (a 16-position tile for each of 4 warps) of
 // one (sequence, kv head, row tile), its unit.  All chunks of a call lie in one
@@ -874,23 +875,26 @@ cudaError_t launch_kv8_attention(const Kv8 &c, const void *q, int64_t q_stride, 
     p.unit_count = static_cast<unsigned *>(workspace);
     p.join_count = p.unit_count + sm_count;
     p.part = reinterpret_cast<float *>(static_cast<char *>(workspace) + counter_bytes(sm_count));
-// Groups per CTA: as many as the registers allow (128 a thread with 4 groups, 96 with 5, 168 with 3, 255 with 2).
+// Groups per CTA: as many as leave every accumulator, query fragment and load in registers (168 a
+// thread with 3 groups, 255 with 2).  One group more spills 10 to 80 words and costs more than its
+// warps bring: head_dim 128, 8 rows, 64 x 16000: 320 us with 4 groups, 311 with 3; 16 rows, 64 x
+// 8000: 242 with 3, 181 with 2; head_dim 64, 32 rows, 64 x 8000: 207 with 3, 165 with 2.
 #define W4Q_ATTN(D, NT, G)                                                        \
     return c.fp8 ? launch_variant<D, NT, true, G>(p, sm_count, stream)           \
                  : launch_variant<D, NT, false, G>(p, sm_count, stream)
     if (c.head_dim == 64) {
         if (tr == 8)
-            W4Q_ATTN(64, 1, 5);
+            W4Q_ATTN(64, 1, 4);
         if (tr == 16)
-            W4Q_ATTN(64, 2, 4);
+            W4Q_ATTN(64, 2, 3);
         if (tr == 24)
-            W4Q_ATTN(64, 3, 3);
-        W4Q_ATTN(64, 4, 3);
+            W4Q_ATTN(64, 3, 2);
+        W4Q_ATTN(64, 4, 2);
     }
     if (c.head_dim == 128) {
         if (tr == 8)
-            W4Q_ATTN(128, 1, 4);
-        W4Q_ATTN(128, 2, 3);
+            W4Q_ATTN(128, 1, 3);
+        W4Q_ATTN(128, 2, 2);
     }
     W4Q_ATTN(256, 1, 2);
 #undef W4Q_ATTN
