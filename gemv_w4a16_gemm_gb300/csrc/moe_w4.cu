@@ -473,8 +473,9 @@ __global__ void __launch_bounds__(32 * W, 1) moe_gemm_kernel(const GemmParams p)
     };
     const Unit at = cut_at(blockIdx.x), end = cut_at(blockIdx.x + 1);
 
-    // Segments: the units of one expert in the range.  Warp w's part of a segment of S steps (its
-    // units' super-blocks) is S w / W .. S (w + 1) / W - 1.  All warps go through all segments.
+    // Segments: the units of one expert in the range, or, where no expert has more than 8 tokens and
+    // each takes one pass, all of them.  Warp w's part of a segment of S steps (its units'
+    // super-blocks) is S w / W .. S (w + 1) / W - 1.  All warps go through all segments.
     struct Segment {
         Unit first;
         int units;  // 0: no segment left
@@ -482,9 +483,15 @@ __global__ void __launch_bounds__(32 * W, 1) moe_gemm_kernel(const GemmParams p)
     auto segment_at = [&](Unit at) -> Segment {
         if (at.a > end.a || (at.a == end.a && at.blk >= end.blk))
             return {at, 0};
+        if constexpr (NT == 1)
+            return {at, (end.a - at.a) * blocks + end.blk - at.blk};
         return {at, (at.a == end.a ? end.blk : blocks) - at.blk};
     };
-    auto after = [&](const Segment &s) -> Segment { return segment_at({s.first.a + 1, 0}); };
+    auto after = [&](const Segment &s) -> Segment { return segment_at(NT == 1 ? end : Unit{s.first.a + 1, 0}); };
+    auto unit_of = [&](const Segment &s, int u) -> Unit {
+        const int blk = s.first.blk + u, more = NT == 1 ? (unsigned)blk / (unsigned)blocks : 0;
+        return {s.first.a + more, blk - more * blocks};
+    };
     auto cut_of = [&](const Segment &s, int w) -> int { return s.units * KB * w / W; };  // < 2^22
     Segment seg = segment_at(at);
     if (seg.units == 0)
@@ -495,7 +502,8 @@ __global__ void __launch_bounds__(32 * W, 1) moe_gemm_kernel(const GemmParams p)
     constexpr uint32_t TILE16 = TILE_BYTES / 16, NEXT_SB = 8 * TILE16, NONE = ~0u;
     const uint32_t second = GATED ? (uint32_t)(blocks >> 3) * KB * NEXT_SB : TILE16;
     auto place = [&](const Segment &s, int u, int b) -> uint32_t {
-        const int blk = s.first.blk + u, tl = s_expert[s.first.a] * 2 * blocks + (GATED ? blk : 2 * blk);
+        const Unit at = unit_of(s, u);
+        const int tl = s_expert[at.a] * 2 * blocks + (GATED ? at.blk : 2 * at.blk);
         return ((uint32_t)(tl >> 3) * KB + b) * NEXT_SB + (tl & 7) * TILE16;
     };
     auto first_place = [&](Segment s) -> uint32_t {  // of this warp's, from segment s on
@@ -529,13 +537,14 @@ __global__ void __launch_bounds__(32 * W, 1) moe_gemm_kernel(const GemmParams p)
     copy(here, 0);
 
     for (; seg.units > 0; seg = after(seg)) {
-        const int *list = p.plan->entries + s_offset[seg.first.a];
-        const int n = s_offset[seg.first.a + 1] - s_offset[seg.first.a];
         const int c0 = cut_of(seg, warp), c1 = cut_of(seg, warp + 1);
         const uint32_t there = c0 < c1 ? first_place(after(seg)) : here;
+        auto tokens_of = [&](int a) -> int { return s_offset[a + 1] - s_offset[a]; };
         // the result of unit u for the 8 tokens from col0 on
         auto store = [&](const float (&v)[2][4], int col0, int u) {
-            const int blk = seg.first.blk + u;
+            const Unit unit = unit_of(seg, u);
+            const int blk = unit.blk, n = tokens_of(unit.a);
+            const int *list = p.plan->entries + s_offset[unit.a];
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
                 const int col = col0 + 2 * t + i;
@@ -565,15 +574,18 @@ __global__ void __launch_bounds__(32 * W, 1) moe_gemm_kernel(const GemmParams p)
         auto pass = [&](auto groups_of_8, int n0) {
             constexpr int N = decltype(groups_of_8)::value;
             if (c0 < c1) {
-                const bool again = n0 + 8 * N < n;
+                int u = (unsigned)c0 / (unsigned)KB, b = c0 - u * KB, a = unit_of(seg, u).a;
+                const bool again = NT > 1 && n0 + 8 * N < tokens_of(a);
                 const uint4 *row[N];  // tokens past the last are its copies, and are not stored
+                auto find_rows = [&]() {
 #pragma unroll
-                for (int nt = 0; nt < N; ++nt) {
-                    const int entry = __ldg(list + min(n0 + nt * 8 + g, n - 1));
-                    row[nt] = reinterpret_cast<const uint4 *>(
-                        p.xf + (int64_t)(GATED ? (unsigned)entry / (unsigned)p.topk : entry) * p.K + 16 * t);
-                }
-                int u = (unsigned)c0 / (unsigned)KB, b = c0 - u * KB;
+                    for (int nt = 0; nt < N; ++nt) {
+                        const int entry = __ldg(p.plan->entries + s_offset[a] + min(n0 + nt * 8 + g, tokens_of(a) - 1));
+                        row[nt] = reinterpret_cast<const uint4 *>(
+                            p.xf + (int64_t)(GATED ? (unsigned)entry / (unsigned)p.topk : entry) * p.K + 16 * t);
+                    }
+                };
+                find_rows();
                 bool begun = b == 0;  // the unit's first super-block is this warp's
                 uint32_t at = here;
                 float acc[2][N][4];
@@ -646,6 +658,12 @@ __global__ void __launch_bounds__(32 * W, 1) moe_gemm_kernel(const GemmParams p)
                         ++u;
                         b = 0;
                         begun = true;
+                        if (NT == 1 && more && unit_of(seg, u).a != a) {
+                            a = unit_of(seg, u).a;
+                            find_rows();
+                            x[0][0] = ldg_row(row[0]);
+                            x[0][1] = ldg_row(row[0] + 1);
+                        }
                     }
                 }
             }
@@ -677,6 +695,7 @@ __global__ void __launch_bounds__(32 * W, 1) moe_gemm_kernel(const GemmParams p)
             }
             __syncthreads();  // the parts are read
         };
+        const int n = NT == 1 ? 8 : tokens_of(seg.first.a);
         int n0 = 0;
         if constexpr (NT > 2)
             for (; n - n0 > 16; n0 += 32)
