@@ -111,6 +111,22 @@ __device__ __forceinline__ Angles load_angles(const Row &p, int64_t pos, int sub
     return a;
 }
 
+// Two fp32 operations in one instruction, rounded as one by one: (a, b) = (a x, b y) and (a, b) = (x u + a, y v + b).
+__device__ __forceinline__ void mul2(float &a, float &b, float x, float y)
+{
+    asm("{\n\t.reg .b64 p, q;\n\tmov.b64 p, {%0, %1};\n\tmov.b64 q, {%2, %3};\n\tmul.rn.f32x2 p, p, q;\n\t"
+        "mov.b64 {%0, %1}, p;\n\t}"
+        : "+f"(a), "+f"(b)
+        : "f"(x), "f"(y));
+}
+__device__ __forceinline__ void fma2(float &a, float &b, float x, float y, float u, float v)
+{
+    asm("{\n\t.reg .b64 p, q, r;\n\tmov.b64 p, {%2, %3};\n\tmov.b64 q, {%4, %5};\n\tmov.b64 r, {%0, %1};\n\t"
+        "fma.rn.f32x2 r, p, q, r;\n\tmov.b64 {%0, %1}, r;\n\t}"
+        : "+f"(a), "+f"(b)
+        : "f"(x), "f"(y), "f"(u), "f"(v));
+}
+
 // The lane's 8 elements of a head row, normed and rotated.  All lanes of the
 // warp call it together.
 template <int D>
@@ -118,17 +134,20 @@ __device__ __forceinline__ void turn(const Row &p, const Weights &w, const Angle
 {
     constexpr int LANES = D / 8;
     if (p.weight != nullptr) {
-        float ss = 0.f;
+        float ss = 0.f, st = 0.f;
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-            ss = fmaf(y[i], y[i], ss);
+        for (int i = 0; i < 8; i += 2)
+            fma2(ss, st, y[i], y[i + 1], y[i], y[i + 1]);
+        ss += st;
 #pragma unroll
         for (int o = LANES / 2; o > 0; o >>= 1)
             ss += __shfl_xor_sync(~0u, ss, o);
         const float f = rsqrtf(ss * (1.f / D) + p.eps);
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-            y[i] = y[i] * f * w.w[i];
+        for (int i = 0; i < 8; i += 2) {
+            mul2(y[i], y[i + 1], f, f);
+            mul2(y[i], y[i + 1], w.w[i], w.w[i + 1]);
+        }
     }
     if (p.cos_sin != nullptr && 8 * sub < p.rot) {
         const float c[4] = {a.c.x, a.c.y, a.c.z, a.c.w}, s[4] = {a.s.x, a.s.y, a.s.z, a.s.w};
@@ -141,10 +160,12 @@ __device__ __forceinline__ void turn(const Row &p, const Weights &w, const Angle
             }
         } else {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const float u = y[i], v = y[4 + i];
-                y[i] = u * c[i] - v * s[i];
-                y[4 + i] = v * c[i] + u * s[i];
+            for (int i = 0; i < 4; i += 2) {
+                const float u0 = y[i], u1 = y[i + 1], v0 = y[4 + i], v1 = y[5 + i];
+                mul2(y[i], y[i + 1], c[i], c[i + 1]);
+                fma2(y[i], y[i + 1], v0, v1, -s[i], -s[i + 1]);
+                mul2(y[4 + i], y[5 + i], c[i], c[i + 1]);
+                fma2(y[4 + i], y[5 + i], u0, u1, s[i], s[i + 1]);
             }
         }
     }
