@@ -29,8 +29,13 @@
 // per warp, and the units that warps share are joined in shared memory at the
 // end, in the line's order.  A warp's tiles come through a ring of two pairs of
 // its own in shared memory (cp.async; tiles loaded straight to registers left
-// the tokens' rows, which come through L1 one sub-block ahead, waiting on the
-// same few scoreboards).
+// the tokens' rows waiting on the same few scoreboards).  The tokens' rows come
+// from L2 through L1, which hardly keeps them: a register of them is loaded
+// again, for the sub-block after the next, as soon as its group of 32 columns
+// is done.  (Loaded one sub-block ahead, 64 tokens of 16 experts of 6656 x 4096
+// took 198 us, now 182, and 32 of 128 experts of 2048 x 768 61 us, now 60; if
+// all of these loads hit L1 the former would take 158.  Whole units per warp,
+// so that the warps read the same columns at the same time, changed neither.)
 //
 // Arithmetic.  A word of packed codes, masked, is a pair of bf16 subnormals
 // q 2^-133 (low nibbles) or q 2^-129 (high nibbles); one bf16x2 fma with 2^127
@@ -92,10 +97,10 @@ __device__ __forceinline__ int step_cost(int n, int most)
     int cost = 0;
     if (most >= 4)
         for (; n > 16; n -= 32)
-            cost += 18;
+            cost += 20;
     if (most >= 2)
         for (; n > 8; n -= 16)
-            cost += 12;
+            cost += 14;
     return cost + (n > 0 ? (n + 7) / 8 * 8 : 0);
 }
 
@@ -279,9 +284,12 @@ __global__ void __launch_bounds__(32 * ROUTE_WARPS) moe_route_kernel(const Route
                 p.weights_out[m * p.topk + lane] = w;
         }
     }
-    cluster.sync();
+    if constexpr (TT > 1)
+        cluster.sync();
     if (rank != 0)
         return;
+    if constexpr (TT == 1)  // the first CTA has chosen for all tokens
+        __syncthreads();
     // the choices by expert: an expert's tokens are bits of its mask
     if (warp == 0) {
         int count = 0, cost = 0, entries = 0;
@@ -395,37 +403,33 @@ struct Count {
     static constexpr int value = V;
 };
 
-// One sub-block (64 columns, two groups of 32) of a tile times NT groups of 8
-// tokens: acc += s * sum (q - z) x 2^-6.
+// A group of 32 columns of a tile times NT groups of 8 tokens: acc += s * sum (q - z) x 2^-6.  `zz`
+// holds the zeros of rows g, g + 8 of this group in its lower (gr = 0) or upper half.
 template <int NT>
-__device__ __forceinline__ void tile_step(const uint4 &q, uint32_t s0, uint32_t s1, uint32_t zz, const uint4 (&x)[NT][2],
-                                          float (&acc)[NT][4])
+__device__ __forceinline__ void group_step(uint32_t q0, uint32_t q1, uint32_t sc, uint32_t zz, int gr, const uint4 (&x)[NT],
+                                           float (&acc)[NT][4])
 {
+    // -z 2^-6 of rows g, g + 8
+    const uint32_t z0 = bf16x2_mul(prmt(zz, 0u, gr ? 0x4242u : 0x4040u), NEG_2P127);
+    const uint32_t z1 = bf16x2_mul(prmt(zz, 0u, gr ? 0x4343u : 0x4141u), NEG_2P127);
+    float d[NT][4];
 #pragma unroll
-    for (int gr = 0; gr < 2; ++gr) {
-        // -z 2^-6 of rows g, g + 8
-        const uint32_t z0 = bf16x2_mul(prmt(zz, 0u, gr ? 0x4242u : 0x4040u), NEG_2P127);
-        const uint32_t z1 = bf16x2_mul(prmt(zz, 0u, gr ? 0x4343u : 0x4141u), NEG_2P127);
-        float d[NT][4];
+    for (int k = 0; k < 2; ++k) {
+        const uint32_t w = k ? q1 : q0, wh = w >> 8;
+        const uint32_t a[4] = {bf16x2_fma(w & 0x000F000Fu, BF_2P127, z0), bf16x2_fma(wh & 0x000F000Fu, BF_2P127, z1),
+                               bf16x2_fma(w & 0x00F000F0u, BF_2P123, z0), bf16x2_fma(wh & 0x00F000F0u, BF_2P123, z1)};
 #pragma unroll
-        for (int k = 0; k < 2; ++k) {
-            const uint32_t w = (&q.x)[2 * gr + k], wh = w >> 8;
-            const uint32_t a[4] = {bf16x2_fma(w & 0x000F000Fu, BF_2P127, z0), bf16x2_fma(wh & 0x000F000Fu, BF_2P127, z1),
-                                   bf16x2_fma(w & 0x00F000F0u, BF_2P123, z0), bf16x2_fma(wh & 0x00F000F0u, BF_2P123, z1)};
+        for (int nt = 0; nt < NT; ++nt)
+            if (k == 0)
+                mma_first(d[nt], a, x[nt].x, x[nt].y);
+            else
+                mma_more(d[nt], a, x[nt].z, x[nt].w);
+    }
+    const float sa = bf16lo_to_f32(sc), sb = bf16hi_to_f32(sc);
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-                if (k == 0)
-                    mma_first(d[nt], a, x[nt][gr].x, x[nt][gr].y);
-                else
-                    mma_more(d[nt], a, x[nt][gr].z, x[nt][gr].w);
-        }
-        const uint32_t sc = gr ? s1 : s0;
-        const float sa = bf16lo_to_f32(sc), sb = bf16hi_to_f32(sc);
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-            fma_pair(acc[nt][0], acc[nt][1], sa, d[nt][0], d[nt][1]);
-            fma_pair(acc[nt][2], acc[nt][3], sb, d[nt][2], d[nt][3]);
-        }
+    for (int nt = 0; nt < NT; ++nt) {
+        fma_pair(acc[nt][0], acc[nt][1], sa, d[nt][0], d[nt][1]);
+        fma_pair(acc[nt][2], acc[nt][3], sb, d[nt][2], d[nt][3]);
     }
 }
 
@@ -589,17 +593,25 @@ __global__ void __launch_bounds__(32 * W, 1) moe_gemm_kernel(const GemmParams p)
                 bool begun = b == 0;  // the unit's first super-block is this warp's
                 uint32_t at = here;
                 float acc[2][N][4];
-                uint4 x[N][2];
+                // the tokens' rows: a register is loaded again, for the sub-block after the next, as soon
+                // as its group is done
+                uint4 x[2][2][N];
+                auto begin_rows = [&]() {
 #pragma unroll
-                for (int nt = 0; nt < N; ++nt) {
-                    x[nt][0] = ldg_row(row[nt] + b * 32);
-                    x[nt][1] = ldg_row(row[nt] + b * 32 + 1);
+                    for (int i = 0; i < 4; ++i)
 #pragma unroll
-                    for (int r = 0; r < 2; ++r)
+                        for (int nt = 0; nt < N; ++nt)
+                            x[i >> 1][i & 1][nt] = ldg_row(row[nt] + b * 32 + 8 * (i >> 1) + (i & 1));
+                };
+                begin_rows();
+#pragma unroll
+                for (int r = 0; r < 2; ++r)
+#pragma unroll
+                    for (int nt = 0; nt < N; ++nt)
                         acc[r][nt][0] = acc[r][nt][1] = acc[r][nt][2] = acc[r][nt][3] = 0.f;
-                }
                 for (int c = c0; c < c1; ++c) {
                     const bool more = c + 1 < c1, inside = b + 1 < KB;
+                    const int b_next = inside ? b + 1 : 0;
                     const uint32_t next = more ? (inside ? at + NEXT_SB : place(seg, u + 1, 0)) : again ? here : there;
                     // this pair has come, and every lane has read the one before
                     asm volatile("cp.async.wait_group 0;" ::: "memory");
@@ -616,24 +628,24 @@ __global__ void __launch_bounds__(32 * W, 1) moe_gemm_kernel(const GemmParams p)
                     }
 #pragma unroll
                     for (int sb = 0; sb < 4; ++sb) {
-                        uint4 ahead[N][2];
+                        uint4 q[2];
 #pragma unroll
-                        for (int nt = 0; nt < N; ++nt) {
-                            // (of a last step, the unit's first columns once more)
-                            const uint4 *src = row[nt] + (sb < 3 ? b * 32 + 8 * (sb + 1) : inside ? b * 32 + 32 : 0);
-                            ahead[nt][0] = ldg_row(src);
-                            ahead[nt][1] = ldg_row(src + 1);
-                        }
+                        for (int r = 0; r < 2; ++r)
+                            q[r] = lds128(tiles + r * TILE_BYTES + 512 * sb + 16 * lane);
 #pragma unroll
-                        for (int r = 0; r < 2; ++r) {
-                            const uint4 &s = sc[r][sb >> 1];
-                            tile_step<N>(lds128(tiles + r * TILE_BYTES + 512 * sb + 16 * lane), sb & 1 ? s.z : s.x,
-                                         sb & 1 ? s.w : s.y, (&z[r].x)[sb], x, acc[r]);
-                        }
+                        for (int gr = 0; gr < 2; ++gr) {
 #pragma unroll
-                        for (int nt = 0; nt < N; ++nt) {
-                            x[nt][0] = ahead[nt][0];
-                            x[nt][1] = ahead[nt][1];
+                            for (int r = 0; r < 2; ++r) {
+                                const uint4 &s = sc[r][sb >> 1];
+                                group_step<N>(gr ? q[r].z : q[r].x, gr ? q[r].w : q[r].y,
+                                              sb & 1 ? (gr ? s.w : s.z) : (gr ? s.y : s.x), (&z[r].x)[sb], gr, x[sb & 1][gr],
+                                              acc[r]);
+                            }
+                            // (of a last step, columns that are not used)
+#pragma unroll
+                            for (int nt = 0; nt < N; ++nt)
+                                x[sb & 1][gr][nt] =
+                                    ldg_row(row[nt] + (sb < 2 ? b * 32 + 8 * (sb + 2) : b_next * 32 + 8 * (sb - 2)) + gr);
                         }
                     }
                     at = next;
@@ -661,8 +673,7 @@ __global__ void __launch_bounds__(32 * W, 1) moe_gemm_kernel(const GemmParams p)
                         if (NT == 1 && more && unit_of(seg, u).a != a) {
                             a = unit_of(seg, u).a;
                             find_rows();
-                            x[0][0] = ldg_row(row[0]);
-                            x[0][1] = ldg_row(row[0] + 1);
+                            begin_rows();
                         }
                     }
                 }
@@ -745,8 +756,8 @@ cudaError_t launch_variant(const GemmParams &p, int sm_count, cudaStream_t strea
     return launch_pdl(fn, dim3((unsigned)sm_count), dim3(32 * W), (12 * (p.experts + 1) + 15) / 16 * 16 + fixed, stream, p);
 }
 
-// Groups of 8 tokens at a time, and warps for their registers: with up to 8 tokens no expert has
-// more; 32 at a time pay where the experts have more than 16 on average.
+// Groups of 8 tokens at a time: with up to 8 tokens no expert has more; 32 at a time pay where the
+// experts have more than 16 on average (64 tokens, 8 of 16 experts of 2048 x 768: 65 us, 73 by 16).
 int groups_of(int tokens, int topk, int experts)
 {
     return tokens <= 8 ? 1 : tokens * topk <= 16 * experts ? 2 : 4;
@@ -755,7 +766,7 @@ int groups_of(int tokens, int topk, int experts)
 template <bool GATED>
 cudaError_t launch_gemm(const GemmParams &p, int groups, int sm_count, cudaStream_t stream)
 {
-    return groups == 1   ? launch_variant<GATED, 1, 16>(p, sm_count, stream)
+    return groups == 1   ? launch_variant<GATED, 1, 12>(p, sm_count, stream)
            : groups == 2 ? launch_variant<GATED, 2, 12>(p, sm_count, stream)
                          : launch_variant<GATED, 4, 8>(p, sm_count, stream);
 }
