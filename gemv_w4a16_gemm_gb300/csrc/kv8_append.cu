@@ -20,7 +20,12 @@
 // tokens.  Layout: D / 8 lanes hold a head row.  A lane has two groups of 4
 // elements, one from each half of the rotated part (or 8 beyond it), so both
 // partners of its pairs and their 4 angles are its own: the norm's sum is the
-// only thing that lanes exchange.
+// only thing that lanes exchange.  Measured: 8191 tokens of 56 heads of 128
+// rotated in 42.9 us, 81% of the measured copy bandwidth; 5 x 2000 tokens (8 kv
+// heads, 32 query heads) written in 37 us and read in 10, bound by the
+// quantization's instructions; 64 x 1 written and read in 8.5 us, bound by the
+// chain of dependent loads.  (Query heads in a launch of their own after the
+// pages': 55 us for 5 x 2000; a warp going through several heads of a page: 50.)
 #include <cuda_fp16.h>
 
 #include "common.cuh"

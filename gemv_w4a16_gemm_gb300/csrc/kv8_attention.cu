@@ -33,8 +33,10 @@
 // the next tile's K is loaded as soon as this tile's is used up, its V likewise,
 // and the one after it is on its way to L2.  (The same bytes through a ring of
 // cp.async in shared memory: 434 us instead of 347 for 64 x 16000 x 8 heads of
-// 128; without the prefetch to L2 349, with it 319, without spills 311: 2.1 GB
-// at 6.76 TB/s, 99% of the measured copy bandwidth.)
+// 128; without the prefetch to L2 349, with it 319, without spills 311, now 308:
+// 2.1 GB at 6.8 TB/s, the measured copy bandwidth.  Shorter calls are bound by
+// their start, 3 us to the first tile, and by the joins, 5 us after the last:
+// 32 x 4000 takes 35 us for the 22 of its bytes, 1 x 131071 32 for 20.)
 //
 // Work.  One chunk = 64 positions (a 16-position tile for each of 4 warps) of
 // one (sequence, kv head, row tile), its unit.  All chunks of a call lie in one
@@ -45,7 +47,8 @@
 // joined in shared memory; one that CTAs share leaves partial sums in the
 // workspace, joined by the last CTA to arrive (for many parts, first among
 // every JOIN neighbours), in the order of the line: results do not depend on
-// the order of arrival.
+// the order of arrival.  A CTA arrives at once for the two units that it can
+// share (one after the other: 32 x 4000 36.4 us instead of 35.2).
 #include <cuda_fp16.h>
 
 #include <atomic>
@@ -64,8 +67,7 @@ constexpr float P_SCALE = 128.f;   // 2^7: P <= 2^8 becomes at most 2^15 in f16
 constexpr int W = 4;               // warps of a group
 constexpr int START = 3;           // a unit's beginning costs about as much as this many chunks
 constexpr int SNAP = 16;           // units up to this many chunks stay in one CTA
-constexpr int JOIN = 16;           // neighbours whose partial sums are joined first ...
-constexpr int JOIN_ONCE = 48;      // ... where a unit has more parts than this
+constexpr int JOIN = 16;           // neighbours whose partial sums are joined first, of a unit with more parts
 constexpr int MAX_SEQS = 4096;
 
 struct AttnParams {
@@ -195,7 +197,7 @@ __global__ void __launch_bounds__(32 * W * G, 1) kv8_attention_kernel(const Attn
     using SM = Smem<D, NT, G>;
     constexpr int ROWS = SM::ROWS, THREADS = 32 * W * G, KC = D / 64, VB = D / 8, VW = VB / 4, NM = D / 16;
     extern __shared__ __align__(16) uint8_t smem[];
-    __shared__ unsigned s_last;
+    __shared__ bool s_last[2], s_final;
     __shared__ int s_warp[W * G];
     __shared__ Unit s_cut[2 * G];
     int *s_len = reinterpret_cast<int *>(smem + SM::BASE);  // [seqs]
@@ -667,6 +669,16 @@ __global__ void __launch_bounds__(32 * W * G, 1) kv8_attention_kernel(const Attn
     }
 
     // --- join the units that the CTA's groups, or CTAs, share
+    // Of those that CTAs share: the one that this CTA continues, and the one that begins in it.
+    struct Shared {
+        Unit unit;
+        int c0, parts;  // its CTAs c0 .. c0 + parts - 1
+    };
+    Shared old = {}, young = {};
+    // a CTA's slot 1 in the workspace holds the unit that begins in it, slot 0 the one that it continues
+    auto slot_of = [&](int c, int c0) { return p.part + (int64_t)(2 * c + (c == c0 ? 1 : 0)) * SM::PART; };
+    constexpr int TPR = THREADS / ROWS;
+    const int r = tid / TPR, first = tid % TPR;  // this thread's row, r < ROWS but for the remainder of THREADS
     __syncthreads();
     for (int k = 0; k < 2 * G;) {
         const Unit unit = s_cut[k];
@@ -678,12 +690,8 @@ __global__ void __launch_bounds__(32 * W * G, 1) kv8_attention_kernel(const Attn
         while (k < 2 * G && (s_cut[k].begin < 0 || s_cut[k].begin == unit.begin))
             ++k;
         const bool whole = unit.begin + START >= begin && unit.end <= end;
-        // a CTA's slot 1 in the workspace holds the unit that begins in it, slot 0 the one that it continues
         const int c0 = whole ? cta : (int)(((long long)(unit.begin + START + 1) * P - 1) / U);
         const int c1 = whole ? cta : (int)(((long long)unit.end * P - 1) / U);
-        auto slot_of = [&](int c) { return p.part + (int64_t)(2 * c + (c == c0 ? 1 : 0)) * SM::PART; };
-        constexpr int TPR = THREADS / ROWS;
-        const int r = tid / TPR, first = tid % TPR;  // this thread's row, r < ROWS but for the remainder of THREADS
         if (r < ROWS) {
             float mm = NEG, ll = 0.f;
             for (int q = k0; q < k; ++q)
@@ -692,7 +700,7 @@ __global__ void __launch_bounds__(32 * W * G, 1) kv8_attention_kernel(const Attn
             for (int q = k0; q < k; ++q)
                 if (s_cut[q].begin >= 0)
                     ll += ex2(part_of(q)[ROWS * D + r] - mm) * part_of(q)[ROWS * D + ROWS + r];
-            float *dst = slot_of(cta);
+            float *dst = slot_of(cta, c0);
             RowOut out = {};
             if (whole) {
                 out = row_out(unit, r, mm, ll, first == 0);
@@ -715,22 +723,37 @@ __global__ void __launch_bounds__(32 * W * G, 1) kv8_attention_kernel(const Attn
                     *reinterpret_cast<float2 *>(dst + r * D + at) = x;
             }
         }
-        if (whole)
-            continue;
+        if (!whole)
+            (cta == c0 ? young : old) = {unit, c0, c1 - c0 + 1};
+    }
+    if (old.parts + young.parts == 0)
+        return;  // the whole CTA
 
-        auto arrive = [&](unsigned *count, int of) -> bool {
-            __syncthreads();
-            if (tid == 0) {
-                __threadfence();
-                const unsigned before = atomic_add_acq_rel(count, 1u);
-                s_last = before + 1 == (unsigned)of;
-                if (s_last)
-                    *count = 0;  // as the next call expects it
-                __threadfence();
-            }
-            __syncthreads();
-            return s_last != 0;
-        };
+    // Arrivals.  The barrier before puts the CTA's partial sums before its thread's release, the one after
+    // puts the other CTAs' after its acquire.
+    auto arrive = [&](unsigned *count, int of) -> bool {  // one thread
+        const unsigned before = atomic_add_acq_rel(count, 1u);
+        if (before + 1 != (unsigned)of)
+            return false;
+        *count = 0;  // as the next call expects it
+        return true;
+    };
+    // many parts are joined by neighbours first
+    auto first_of = [&](const Shared &u) { return u.parts <= JOIN ? u.c0 : u.c0 + (cta - u.c0) / JOIN * JOIN; };
+    auto members_of = [&](const Shared &u) { return u.parts <= JOIN ? u.parts : min(JOIN, u.c0 + u.parts - first_of(u)); };
+    __syncthreads();
+    if (tid == 0 || tid == 32) {  // both at a time
+        const Shared u = tid == 0 ? old : young;
+        const int f = first_of(u);
+        s_last[tid / 32] = u.parts > 0 && arrive(u.parts <= JOIN ? p.unit_count + f : p.join_count + 2 * f + (f == u.c0 ? 1 : 0),
+                                                 members_of(u));
+    }
+    __syncthreads();
+#pragma unroll 1
+    for (int which = 0; which < 2; ++which) {
+        if (!s_last[which])
+            continue;
+        const Shared u = which == 0 ? old : young;
         // joins `of` slots, `step` CTAs apart from CTA f on, into the first of them or the result
         auto join = [&](int f, int step, int of, bool last) {
             constexpr int ITEMS = (D / 2 + TPR - 1) / TPR, AT_ONCE = 16;
@@ -741,7 +764,7 @@ __global__ void __launch_bounds__(32 * W * G, 1) kv8_attention_kernel(const Attn
                     float pm[AT_ONCE], pl[AT_ONCE];
 #pragma unroll
                     for (int q = 0; q < AT_ONCE; ++q) {  // all loads before any use
-                        const float *src = slot_of(f + min(q0 + q, of - 1) * step) + ROWS * D + r;
+                        const float *src = slot_of(f + min(q0 + q, of - 1) * step, u.c0) + ROWS * D + r;
                         pm[q] = __ldcg(src);
                         pl[q] = __ldcg(src + ROWS);
                     }
@@ -751,7 +774,7 @@ __global__ void __launch_bounds__(32 * W * G, 1) kv8_attention_kernel(const Attn
 #pragma unroll
                         for (int q = 0; q < AT_ONCE; ++q)
                             y[i][q] = __ldcg(reinterpret_cast<const float2 *>(
-                                slot_of(f + min(q0 + q, of - 1) * step) + r * D + 2 * min(first + i * TPR, D / 2 - 1)));
+                                slot_of(f + min(q0 + q, of - 1) * step, u.c0) + r * D + 2 * min(first + i * TPR, D / 2 - 1)));
                     float top = mm;
 #pragma unroll
                     for (int q = 0; q < AT_ONCE; ++q)
@@ -776,7 +799,7 @@ __global__ void __launch_bounds__(32 * W * G, 1) kv8_attention_kernel(const Attn
                     }
                 }
             if (last) {
-                const RowOut out = r < ROWS ? row_out(unit, r, mm, ll, first == 0) : RowOut{nullptr, 0.f};
+                const RowOut out = r < ROWS ? row_out(u.unit, r, mm, ll, first == 0) : RowOut{nullptr, 0.f};
 #pragma unroll
                 for (int i = 0; i < ITEMS; ++i)
                     if (first + i * TPR < D / 2)
@@ -784,7 +807,7 @@ __global__ void __launch_bounds__(32 * W * G, 1) kv8_attention_kernel(const Attn
             } else {
                 __syncthreads();  // every thread has read the first slot
                 if (r < ROWS) {
-                    float *dst = slot_of(f);
+                    float *dst = slot_of(f, u.c0);
 #pragma unroll
                     for (int i = 0; i < ITEMS; ++i)
                         if (first + i * TPR < D / 2)
@@ -796,21 +819,15 @@ __global__ void __launch_bounds__(32 * W * G, 1) kv8_attention_kernel(const Attn
                 }
             }
         };
-        const int parts = c1 - c0 + 1;
-        unsigned *unit_count = p.unit_count + c0;
-        if (parts <= JOIN_ONCE) {
-            if (arrive(unit_count, parts))
-                join(c0, 1, parts, true);
-        } else {
-            const int mine0 = (cta - c0) / JOIN * JOIN;
-            const int members = min(JOIN, parts - mine0);
-            const int f = c0 + mine0;
-            if (arrive(p.join_count + 2 * f + (f == c0 ? 1 : 0), members)) {
-                join(f, 1, members, false);
-                const int joins = (parts + JOIN - 1) / JOIN;
-                if (arrive(unit_count, joins))
-                    join(c0, JOIN, joins, true);
-            }
+        join(first_of(u), 1, members_of(u), u.parts <= JOIN);
+        if (u.parts > JOIN) {
+            const int joins = (u.parts + JOIN - 1) / JOIN;
+            __syncthreads();
+            if (tid == 0)
+                s_final = arrive(p.unit_count + u.c0, joins);
+            __syncthreads();
+            if (s_final)
+                join(u.c0, JOIN, joins, true);
         }
     }
 }
