@@ -35,8 +35,8 @@
 // cp.async in shared memory: 434 us instead of 347 for 64 x 16000 x 8 heads of
 // 128; without the prefetch to L2 349, with it 319, without spills 311, now 308:
 // 2.1 GB at 6.8 TB/s, the measured copy bandwidth.  Shorter calls are bound by
-// their start, 3 us to the first tile, and by the joins, 5 us after the last:
-// 32 x 4000 takes 35 us for the 22 of its bytes, 1 x 131071 32 for 20.)
+// their start, 3 us to the first tile, and by the joins, 4 us after the last:
+// 32 x 4000 takes 34 us for the 22 of its bytes, 1 x 131071 31 for 20.)
 //
 // Work.  One chunk = 64 positions (a 16-position tile for each of 4 warps) of
 // one (sequence, kv head, row tile), its unit.  All chunks of a call lie in one
@@ -48,10 +48,11 @@
 // workspace, joined by the last CTA to arrive (for many parts, first among
 // every JOIN neighbours), in the order of the line: results do not depend on
 // the order of arrival.  A CTA arrives at once for the two units that it can
-// share (one after the other: 32 x 4000 36.4 us instead of 35.2).
+// share (one after the other: 1.2 us more for 32 x 4000).
 #include <cuda_fp16.h>
 
 #include <atomic>
+#include <type_traits>
 
 #include "common.cuh"
 #include "decode.h"
@@ -65,9 +66,14 @@ constexpr float NEG = -1e30f;      // the reference before any position was seen
 constexpr float SLACK = 8.f;       // the reference may lag this far (log2) behind the largest term
 constexpr float P_SCALE = 128.f;   // 2^7: P <= 2^8 becomes at most 2^15 in f16
 constexpr int W = 4;               // warps of a group
-constexpr int START = 3;           // a unit's beginning costs about as much as this many chunks
-constexpr int SNAP = 16;           // units up to this many chunks stay in one CTA
+// With START 3 and 5 in place of 4, 1 x 130 takes 6.8 and 5.8 us instead of 5.8, 16 x 1000 with 2
+// queries 14.6 and 14.9 instead of 15.4, 8 x 6000 with head_dim 256 22.1 and 18.1 instead of 20.9; with
+// SNAP 16 and 24 in place of 20, drafts over a window of 1024 29.5 and 25.9 instead of 26.3, 32 x 4000
+// 33.8 and 34.9 instead of 33.8.
+constexpr int START = 4;           // a unit's beginning costs about as much as this many chunks
+constexpr int SNAP = 20;           // units up to this many chunks stay in one CTA
 constexpr int JOIN = 16;           // neighbours whose partial sums are joined first, of a unit with more parts
+constexpr int FEW = 4;             // so many or fewer have loads of their own (32 x 4000 35.1 -> 33.9 us)
 constexpr int MAX_SEQS = 4096;
 
 struct AttnParams {
@@ -755,8 +761,8 @@ __global__ void __launch_bounds__(32 * W * G, 1) kv8_attention_kernel(const Attn
             continue;
         const Shared u = which == 0 ? old : young;
         // joins `of` slots, `step` CTAs apart from CTA f on, into the first of them or the result
-        auto join = [&](int f, int step, int of, bool last) {
-            constexpr int ITEMS = (D / 2 + TPR - 1) / TPR, AT_ONCE = 16;
+        auto join_by = [&](auto at_once, int f, int step, int of, bool last) {
+            constexpr int ITEMS = (D / 2 + TPR - 1) / TPR, AT_ONCE = decltype(at_once)::value;
             float mm = NEG, ll = 0.f;
             float2 x[ITEMS] = {};
             if (r < ROWS)
@@ -818,6 +824,12 @@ __global__ void __launch_bounds__(32 * W * G, 1) kv8_attention_kernel(const Attn
                     }
                 }
             }
+        };
+        auto join = [&](int f, int step, int of, bool last) {
+            if (of <= FEW)
+                join_by(std::integral_constant<int, FEW>(), f, step, of, last);
+            else
+                join_by(std::integral_constant<int, JOIN>(), f, step, of, last);
         };
         join(first_of(u), 1, members_of(u), u.parts <= JOIN);
         if (u.parts > JOIN) {
