@@ -111,6 +111,16 @@ __device__ __forceinline__ uint32_t order_key(float v)  // larger for larger v, 
     return v != v ? 1u : max(k, 1u);
 }
 
+// volatile: the compiler is not to move it down to its use
+__device__ __forceinline__ uint4 ldg_row(const uint4 *p)
+{
+    uint4 v;
+    asm volatile("ld.global.nc.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "l"(p));
+    return v;
+}
+
 // TT groups of 8 tokens, up to 32 PER experts.
 template <int TT, int PER>
 __global__ void __launch_bounds__(32 * ROUTE_WARPS) moe_route_kernel(const RouteParams p)
@@ -150,6 +160,10 @@ __global__ void __launch_bounds__(32 * ROUTE_WARPS) moe_route_kernel(const Route
     pdl_wait();
     pdl_launch_dependents();
 
+    float bias[PER];  // loaded long before it is used
+#pragma unroll
+    for (int i = 0; i < PER; ++i)
+        bias[i] = p.sigmoid && p.bias && 32 * i + lane < p.experts ? __ldg(p.bias + 32 * i + lane) : 0.f;
     const int mt = (p.experts + 15) / 16;
     const int slices = ROUTE_CTAS * ROUTE_WARPS / mt;
     const int gw = rank * ROUTE_WARPS + warp;
@@ -168,17 +182,17 @@ __global__ void __launch_bounds__(32 * ROUTE_WARPS) moe_route_kernel(const Route
             rx[n] = reinterpret_cast<const uint4 *>(p.x + (int64_t)min(n * 8 + g, p.tokens - 1) * p.hidden) + t;
             acc[n][0] = acc[n][1] = acc[n][2] = acc[n][3] = 0.f;
         }
-        constexpr int U = TT == 1 ? 8 : (TT == 8 ? 2 : 4);  // chunks whose loads go out together
+        constexpr int U = TT == 8 ? 2 : 4;  // chunks whose loads go out together
         for (int c = c0; c < c1; c += U) {
             uint4 a[U], b[U], x[U][TT];
 #pragma unroll
             for (int i = 0; i < U; ++i) {
                 const int at = 4 * min(c + i, c1 - 1);
-                a[i] = __ldg(ra + at);
-                b[i] = __ldg(rb + at);
+                a[i] = ldg_row(ra + at);
+                b[i] = ldg_row(rb + at);
 #pragma unroll
                 for (int n = 0; n < TT; ++n)
-                    x[i][n] = __ldg(rx[n] + at);
+                    x[i][n] = ldg_row(rx[n] + at);
             }
 #pragma unroll
             for (int i = 0; i < U; ++i)
@@ -228,7 +242,7 @@ __global__ void __launch_bounds__(32 * ROUTE_WARPS) moe_route_kernel(const Route
                 const int e = 32 * i + lane;
                 if (e < p.experts) {
                     score[i] = 1.f / (1.f + expf(-score[i]));
-                    key[i] = order_key(score[i] + (p.bias ? __ldg(p.bias + e) : 0.f));
+                    key[i] = order_key(score[i] + bias[i]);
                 }
             }
         } else {
@@ -377,16 +391,6 @@ __device__ __forceinline__ void mma_more(float (&d)[4], const uint32_t (&a)[4], 
         "{%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
-
-// volatile: the compiler is not to move it down to its use
-__device__ __forceinline__ uint4 ldg_row(const uint4 *p)
-{
-    uint4 v;
-    asm volatile("ld.global.nc.v4.u32 {%0, %1, %2, %3}, [%4];"
-                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-                 : "l"(p));
-    return v;
 }
 
 // a += s x, b += s y
