@@ -7,7 +7,11 @@
 //
 // What bounds it: the chosen experts' weights, 19/32 bytes each, are read once
 // from HBM; with one token that is a few microseconds, so launches and the
-// depth of dependent loads count as much.
+// depth of dependent loads count more (8 of 128 experts of 2048 x 768: 20.6 us,
+// 6.3 of them routing, for 3.4 of bytes).  With more tokens the products' 2.2
+// instructions a weight and lane, at the latency of 3 warps a scheduler, take
+// longer than the bytes (64 tokens, 2 of 16 experts of 6656 x 4096: 183 us for
+// 115, half of the issue slots in use).
 //
 // Four launches, each started while its predecessor finishes:
 //   route    one cluster of 8 CTAs: the logits as m16n8k16 MMAs (bf16 products,
@@ -33,7 +37,7 @@
 // from L2 through L1, which hardly keeps them: a register of them is loaded
 // again, for the sub-block after the next, as soon as its group of 32 columns
 // is done.  (Loaded one sub-block ahead, 64 tokens of 16 experts of 6656 x 4096
-// took 198 us, now 182, and 32 of 128 experts of 2048 x 768 61 us, now 60; if
+// took 198 us instead of 183, and 32 of 128 experts of 2048 x 768 61 instead of 60; if
 // all of these loads hit L1 the former would take 158.  Whole units per warp,
 // so that the warps read the same columns at the same time, changed neither.)
 //
