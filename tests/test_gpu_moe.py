@@ -177,6 +177,23 @@ def test_repeated_calls_and_graph_replay_are_bitwise_equal(cuda):
         assert torch.equal(out, a)
 
 
+@pytest.mark.parametrize("tokens,topk,inter", [(1, 1, 256), (1, 3, 256), (5, 1, 768), (8, 2, 256), (2, 4, 512)])
+def test_few_terms_are_not_rounded_between_the_products(cuda, tokens, topk, inter):
+    """tokens * topk * inter up to 4096: the bound of check() without the 2^-8 of h's rounding."""
+    layer = Layer(512, inter, 6)
+    x = layer.x(tokens)
+    ids, weights = torch.empty(tokens, topk, dtype=torch.int32, device=cuda), torch.empty(tokens, topk, device=cuda)
+    out = w4q.moe_w4a16(x, layer.router, layer.w13, layer.w2, inter, topk, ids=ids, weights=weights)
+    ref, mag = layer.reference(x, ids.long(), weights)
+    assert ((out.double() - ref).abs() <= 2.0 ** -8 * ref.abs() + 2.0 ** -13 * mag).all()
+
+
+@pytest.mark.parametrize("topk,hidden,inter", [(1, 256, 256), (2, 256, 512), (8, 512, 256)])
+def test_workspace_grows_with_the_tokens(cuda, topk, hidden, inter):
+    sizes = [w4q.moe_workspace_bytes(m, hidden, inter, 16, topk) for m in range(1, 65)]
+    assert sizes == sorted(sizes)
+
+
 def test_on_a_stream_of_its_own(cuda):
     layer = Layer(512, 256, 8)
     x = layer.x(4)
