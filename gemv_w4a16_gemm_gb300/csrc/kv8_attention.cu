@@ -303,8 +303,8 @@ __global__ void __launch_bounds__(32 * W * G, 1) kv8_attention_kernel(const Attn
         const int qi = (rr * p.group_inv) >> 16;
         const int64_t row = ((int64_t)x.b * p.queries + qi) * p.heads + h * p.group + (rr - qi * p.group);
         if (first && p.lse != nullptr)
-            p.lse[row] = ll > 0.f ? (mm + log2f(ll)) * 0.6931471805599453f : -INFINITY;
-        return {p.out + row * D, ll > 0.f ? __fdividef(1.f / P_SCALE, ll) : 0.f};
+            p.lse[row] = ll == 0.f ? -INFINITY : (mm + log2f(ll)) * 0.6931471805599453f;  // NaN stays NaN
+        return {p.out + row * D, ll == 0.f ? 0.f : __fdividef(1.f / P_SCALE, ll)};
     };
     auto store_dims = [&](const RowOut &o, int at, float2 v) {
         if (o.to != nullptr)
