@@ -52,6 +52,7 @@
 #include <cuda_fp16.h>
 
 #include <atomic>
+#include <cfloat>
 #include <type_traits>
 
 #include "common.cuh"
@@ -161,6 +162,12 @@ __device__ __forceinline__ void codes_to_f16(uint32_t w, uint32_t &lo, uint32_t 
         asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(lo) : "r"(a), "r"(0x64806480u));
         asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(hi) : "r"(b), "r"(0x64806480u));
     }
+}
+
+// Bit 7 of each byte that is e4m3's NaN, 0x7F or 0xFF.
+__device__ __forceinline__ uint32_t nan_codes(uint32_t w)
+{
+    return ((w & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u;
 }
 
 // The chunks of a sequence of that length: its first 16-position tile that
@@ -485,7 +492,8 @@ __global__ void __launch_bounds__(32 * W * G, 1) kv8_attention_kernel(const Attn
             }
             const bool hole = page < 0;
             const float sk = __shfl_sync(~0u, sks, at32), sv = __shfl_sync(~0u, svs, at32);
-            const float lsv = fmaxf(__log2f(sv), -64.f);
+            // (a scale that is infinite makes its own page's terms so and leaves the reference alone)
+            const float lsv = sv <= FLT_MAX ? fmaxf(__log2f(sv), -64.f) : 0.f;
             const int page_far = __shfl_sync(~0u, at32 >= 30 ? pages_next : pages, (i + 2) & 31);
             const uint64_t far = offset_of(i + 2, page_far);
 
@@ -512,6 +520,7 @@ __global__ void __launch_bounds__(32 * W * G, 1) kv8_attention_kernel(const Attn
                 prefetch(far);
             const int pos = (tile0 + i * W) << 4;
             const bool edge = pos + 16 > lim_min || pos < lo_max || hole;
+            float svp = sv * P_SCALE;
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -529,6 +538,56 @@ __global__ void __launch_bounds__(32 * W * G, 1) kv8_attention_kernel(const Attn
                         if (at >= lim || (p.window > 0 && at < lim - p.window) || hole)
                             s[0][nt][e] = -INFINITY;
                     }
+                // What is not finite among the values must not reach a query that does not see it, as 0 * inf or
+                // 0 * NaN: a page's scale, and e4m3's NaN, which a page may also hold anywhere beyond the
+                // sequence's end.  It counts as 0 here and as NaN in the sums of the queries that see it.
+                const bool odd_scale = !(sv <= FLT_MAX);
+                uint32_t odd = odd_scale;
+                if (FP8)
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+#pragma unroll
+                        for (int w = 0; w < VW; ++w)
+                            odd |= nan_codes(vr[k][w]);
+                if (__any_sync(~0u, odd != 0)) {
+                    uint32_t sees[NT][2];  // of the tile's positions, bits, by the lane's columns
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            const int lim = limit[nt][e] - pos, hi = min(max(lim, 0), 16);
+                            const int lo = p.window > 0 ? min(max(lim - p.window, 0), 16) : 0;
+                            sees[nt][e] = hole ? 0u : ((1u << hi) - 1) & ~((1u << lo) - 1);
+                        }
+                    if (odd_scale)
+                        svp = 0.f;
+#pragma unroll
+                    for (int w = 0; w < VW; ++w) {
+                        uint32_t found[4];
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            found[k] = FP8 ? nan_codes(vr[k][w]) : 0u;
+                            vr[k][w] &= ~((found[k] >> 7) * 0xFFu);
+                        }
+#pragma unroll
+                        for (int byte = 0; byte < 4; ++byte) {  // dim 4w + byte: positions that hold NaN, of all four lanes
+                            uint32_t at = 0;
+#pragma unroll
+                            for (int k = 0; k < 4; ++k)
+                                at |= ((found[k] >> (8 * byte + 7)) & 1u) << (2 * t + (k & 1) + 8 * (k >> 1));
+                            at |= __shfl_xor_sync(~0u, at, 1);
+                            at |= __shfl_xor_sync(~0u, at, 2);
+                            if (odd_scale)
+                                at = 0xFFFFu;
+#pragma unroll
+                            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                                for (int e = 0; e < 2; ++e)
+                                    if (at & sees[nt][e])
+                                        o[nt][2 * w + (byte >> 1)][2 * (byte & 1) + e] = NAN;
+                        }
+                    }
+                }
             }
             bool grow = false;
 #pragma unroll
@@ -557,7 +616,6 @@ __global__ void __launch_bounds__(32 * W * G, 1) kv8_attention_kernel(const Attn
                     }
             }
             uint32_t pf[NT][2];
-            const float svp = sv * P_SCALE;
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
                 float x[4];
@@ -569,15 +627,6 @@ __global__ void __launch_bounds__(32 * W * G, 1) kv8_attention_kernel(const Attn
                 }
                 pf[nt][0] = transpose8x8(f16x2(x[0], x[1]));
                 pf[nt][1] = transpose8x8(f16x2(x[2], x[3]));
-            }
-            // beyond the sequence's end a page may hold anything, e4m3's NaN too
-            if (FP8 && edge) {
-#pragma unroll
-                for (int k = 0; k < 4; ++k)
-                    if (hole || pos + 2 * t + (k & 1) + 8 * (k >> 1) >= len)
-#pragma unroll
-                        for (int w = 0; w < VW; ++w)
-                            vr[k][w] = 0;
             }
 #pragma unroll
             for (int w = 0; w < VW; ++w)

@@ -465,7 +465,8 @@ int kv8_read(const w4q_kv8_cache *cache, const int32_t *cu_tokens,
  *   o = sum_p softmax_p(scale * q . k_p) v_p,  k_p, v_p the cache's values;
  * heads = group * kv_heads, query head h reads kv head h / group.  A query
  * that sees nothing (an idle sequence, a negative position) gives zeros and
- * lse = -inf; one that sees a score that is NaN gives NaN in both.
+ * lse = -inf; one that sees a score that is NaN gives NaN in both.  What a
+ * query does not see has no effect on it, NaN and infinity included.
  *   q    device, bf16 [seqs * queries][heads][head_dim], rows q_stride apart
  *   out  device, bf16 [seqs][queries][heads][head_dim] (written)
  *   lse  device, fp32 [seqs][queries][heads], natural log of the softmax's
