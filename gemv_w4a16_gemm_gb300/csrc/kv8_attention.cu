@@ -63,7 +63,7 @@ namespace w4q {
 
 namespace {
 
-constexpr float NEG = -1e30f;      // the reference before any position was seen
+constexpr float NEG = -FLT_MAX;    // the reference before any position was seen: no finite score is below it
 constexpr float SLACK = 8.f;       // the reference may lag this far (log2) behind the largest term
 constexpr float P_SCALE = 128.f;   // 2^7: P <= 2^8 becomes at most 2^15 in f16
 constexpr int W = 4;               // warps of a group
