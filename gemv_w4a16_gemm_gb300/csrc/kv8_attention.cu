@@ -20,7 +20,8 @@
 // reference m follows max(s log2 e + log2 s_V) and is at most 8 below it: P is
 // then at most 2^8 and is held times 2^7, so that f16 loses nothing above 2^-21
 // of the largest term of the output and rounds the rest to 2^-32 of it,
-// whatever the pages' scales are.  The sum of the row, the reference and O stay
+// whatever the pages' scales from 2^-84 on are (of smaller ones P is smaller, by
+// as much, and keeps fewer bits).  The sum of the row, the reference and O stay
 // in fp32.
 //
 // Fragments without a shuffle.  The order of a product's inner index is free
@@ -65,6 +66,9 @@ namespace {
 
 constexpr float NEG = -FLT_MAX;    // the reference before any position was seen: no finite score is below it
 constexpr float SLACK = 8.f;       // the reference may lag this far (log2) behind the largest term
+// log2 of the least s_V that the reference follows: a row's sum of n terms is then at most
+// 2^(SLACK + 84) n, and stays below the 2^126 from which __fdividef returns 0.
+constexpr float LEAST_LSV = -84.f;
 constexpr float P_SCALE = 128.f;   // 2^7: P <= 2^8 becomes at most 2^15 in f16
 constexpr int W = 4;               // warps of a group
 // With START 3 and 5 in place of 4, 1 x 130 takes 6.8 and 5.8 us instead of 5.8, 16 x 1000 with 2
@@ -493,7 +497,7 @@ __global__ void __launch_bounds__(32 * W * G, 1) kv8_attention_kernel(const Attn
             const bool hole = page < 0;
             const float sk = __shfl_sync(~0u, sks, at32), sv = __shfl_sync(~0u, svs, at32);
             // (a scale that is infinite makes its own page's terms so and leaves the reference alone)
-            const float lsv = sv <= FLT_MAX ? fmaxf(__log2f(sv), -64.f) : 0.f;
+            const float lsv = sv <= FLT_MAX ? fmaxf(__log2f(sv), LEAST_LSV) : 0.f;
             const int page_far = __shfl_sync(~0u, at32 >= 30 ? pages_next : pages, (i + 2) & 31);
             const uint64_t far = offset_of(i + 2, page_far);
 

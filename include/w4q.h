@@ -476,7 +476,8 @@ int kv8_read(const w4q_kv8_cache *cache, const int32_t *cu_tokens,
  *        buffer serves any calls of at most its size, one after the other
  *        on the GPU (not two at a time).
  * Sums, the running reference and the softmax's sum in fp32; the softmax's
- * weights enter the second product with 11 bits.  queries * group <= 64;
+ * weights enter the second product with 11 bits, for v_scale from 2^-80 to
+ * 2^80 or 0 (fewer where a page's scale lies beyond).  queries * group <= 64;
  * width * page < 2^31 - 128, and the table's positions times kv_heads times
  * queries * group / 8 (rounded up) are below about 2^37.  One launch. */
 int kv8_attention(const w4q_kv8_cache *cache, const void *q, int64_t q_stride,
