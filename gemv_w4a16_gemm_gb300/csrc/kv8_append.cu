@@ -13,7 +13,9 @@
 //     s' = max(s, max |y| / top)   (s = 0 for a page without earlier tokens;
 //                                   top = 127 for int8, 448 for e4m3)
 // and the codes rnd(y / s'); where s' > s the earlier codes become
-// rnd(code * (s / s')).  Every quotient is the correctly rounded fp32 one.
+// rnd(code * (s / s')).  Every quotient is the correctly rounded fp32 one.  A NaN
+// or infinite element: e4m3 keeps it as its code NaN and leaves it out of the
+// maximum; int8 has no such code, so s' is NaN and the page's head reads as NaN.
 //
 // What bounds it: each element is read and written once, some fifty
 // instructions for a lane's 8 of them; HBM for prompts, one launch for single
@@ -27,6 +29,8 @@
 // chain of dependent loads.  (Query heads in a launch of their own after the
 // pages': 55 us for 5 x 2000; a warp going through several heads of a page: 50.)
 #include <cuda_fp16.h>
+
+#include <cfloat>
 
 #include "common.cuh"
 #include "decode.h"
@@ -300,7 +304,7 @@ __device__ __forceinline__ uint2 encode8(const float (&y)[8])
     return make_uint2(w[0], w[1]);
 }
 
-// The codes of the correctly rounded quotients y / s, for |y| / top <= s.  A
+// The codes of the correctly rounded quotients y / s, for |y| / top <= s or y NaN (e4m3).  A
 // quotient costs a dozen instructions; y times the rounded reciprocal lies
 // within 2^-22 of it and gives the same code except next to a rounding's edge,
 // where the quotient decides (int8: act_code8; e4m3: both ends of the interval
@@ -308,9 +312,15 @@ __device__ __forceinline__ uint2 encode8(const float (&y)[8])
 template <bool FP8>
 __device__ __forceinline__ uint2 encode8(const float (&y)[8], float s)
 {
-    if (!(s > 0.f))
-        return make_uint2(0u, 0u);
     float q[8];
+    if (!(s > 0.f)) {
+        if constexpr (!FP8)
+            return make_uint2(0u, 0u);
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            q[i] = fabsf(y[i]) * 0.f;  // 0, and NaN's code
+        return encode8<FP8>(q);
+    }
 #pragma unroll
     for (int i = 0; i < 8; ++i)
         q[i] = y[i];
@@ -367,16 +377,38 @@ __device__ __forceinline__ uint2 recode8(uint2 c, float r)
     return encode8<FP8>(y);
 }
 
-template <int LANES>
+// Infinities become NaN.
+__device__ __forceinline__ void mark(float (&y)[8])
+{
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        y[i] = fabsf(y[i]) <= FLT_MAX ? y[i] : NAN;
+}
+
+// max(a, b), NaN if either is
+__device__ __forceinline__ float max_nan(float a, float b)
+{
+    float m;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(m) : "f"(a), "f"(b));
+    return m;
+}
+
+// The largest |y| of a lane's elements and of a group of lanes: NaN if one is (with IGNORE, of the others).
+template <bool IGNORE>
 __device__ __forceinline__ float max_abs(const float (&y)[8])
 {
     float a = 0.f;
 #pragma unroll
     for (int i = 0; i < 8; ++i)
-        a = fmaxf(a, fabsf(y[i]));
+        a = IGNORE ? fmaxf(a, fabsf(y[i])) : max_nan(a, fabsf(y[i]));
+    return a;
+}
+template <int LANES>
+__device__ __forceinline__ float max_of(float a)
+{
 #pragma unroll
     for (int o = LANES / 2; o > 0; o >>= 1)
-        a = fmaxf(a, __shfl_xor_sync(~0u, a, o));
+        a = max_nan(a, __shfl_xor_sync(~0u, a, o));
     return a;
 }
 
@@ -468,7 +500,12 @@ __global__ void __launch_bounds__(32 * HEAD_WARPS) kv8_append_one_kernel(const A
     if (!value)
         turn<D>(p.krow, load_weights(p.krow, at), load_angles(p.krow, pos, sub), sub, y);
     old = __shfl_sync(~0u, old, 0);
-    const float s = fmaxf(__fdiv_rn(max_abs<LANES>(y), FP8 ? 448.f : 127.f), old);
+    float top = max_of<LANES>(max_abs<false>(y));
+    if (!(top <= FLT_MAX)) {  // (of the whole warp: its groups of lanes hold the same row)
+        mark(y);
+        top = FP8 ? max_of<LANES>(max_abs<true>(y)) : NAN;
+    }
+    const float s = max_nan(__fdiv_rn(top, FP8 ? 448.f : 127.f), old);
     uint8_t *codes = (value ? p.c.v : p.c.k) + ((ph << p.c.page_log2) * D);
     if (lane < LANES)
         store_codes(codes + (int64_t)slot * D, at, encode8<FP8>(y, s));
@@ -562,12 +599,32 @@ __global__ void __launch_bounds__(32 * PAGE_WARPS, 4) kv8_append_kernel(const Ap
     float old = 0.f;
     if (lane == 0 && lo > 0 && hi > 0)
         old = *scale;
+    const bool kept = !any(1, 0);
     float top = 0.f;
     for (int n = 0; n == 0 || any(n, 0); ++n) {
         batch(n);
 #pragma unroll
         for (int i = 0; i < R; ++i)
-            top = fmaxf(top, max_abs<32>(y[i]));
+            top = max_nan(top, max_abs<false>(y[i]));
+    }
+    top = max_of<32>(top);
+    const bool odd = !(top <= FLT_MAX);  // a row of this warp holds NaN or infinity
+    auto mark_all = [&]() {
+#pragma unroll
+        for (int i = 0; i < R; ++i)
+            mark(y[i]);
+    };
+    if (odd) {
+        top = FP8 ? 0.f : NAN;
+        for (int n = 0; FP8 && (n == 0 || any(n, 0)); ++n) {
+            if (!kept)
+                batch(n);
+            mark_all();
+#pragma unroll
+            for (int i = 0; i < R; ++i)
+                top = fmaxf(top, max_abs<true>(y[i]));
+        }
+        top = max_of<32>(top);
     }
     old = __shfl_sync(~0u, old, 0);
     if (share > 1) {
@@ -575,16 +632,18 @@ __global__ void __launch_bounds__(32 * PAGE_WARPS, 4) kv8_append_kernel(const Ap
             s_max[warp] = top;
         __syncthreads();
         for (int w = 0; w < share; ++w)
-            top = fmaxf(top, s_max[warp - part + w]);
+            top = max_nan(top, s_max[warp - part + w]);
     }
     if (hi == 0)
         return;
-    const float s = fmaxf(__fdiv_rn(top, FP8 ? 448.f : 127.f), old);
+    const float s = max_nan(__fdiv_rn(top, FP8 ? 448.f : 127.f), old);
     uint8_t *codes = (value ? p.c.v : p.c.k) + ((ph << page_log2) * D);
-    const bool kept = !any(1, 0);
     for (int n = 0; n == 0 || any(n, 0); ++n) {
-        if (!kept)
+        if (!kept) {
             batch(n);
+            if (FP8 && odd)
+                mark_all();
+        }
 #pragma unroll
         for (int i = 0; i < R; ++i)
             if (is_token(slot_of(n, i)))

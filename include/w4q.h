@@ -45,7 +45,8 @@
  *   - W4 shapes: 1 <= M <= 64, N >= 1, K a positive multiple of 256
  *     ("test_int4_quantized_gemm.py", Int4QuantizedGemmLegalityTest: K must
  *     be a multiple of 256), group == 32 (the only supported group size).
- *   - Non-finite inputs give unspecified (but memory-safe) outputs.
+ *   - Non-finite inputs give unspecified (but memory-safe) outputs, except
+ *     where a call's own text says what they give.
  *
  * Packed W4 layout (this library's own; the pages' storage is prior art):
  *   Rows are grouped in tiles of 16 and tiles in groups of 8 (128 rows; N
@@ -440,6 +441,10 @@ typedef struct {
  *   code = rint(y / s') clamped to [-127, 127], or e4m3(y / s') (to nearest
  *   even, saturating); all codes 0 where s' = 0;
  *   where s' > s, earlier tokens' codes become the code of code * (s / s').
+ * An element of y that is NaN or infinite: e4m3 stores its code NaN there and
+ * leaves it out of the maximum.  int8 has no such code: s' is NaN, so that all
+ * of this page and head (of K or of V) reads as NaN, until the page begins
+ * anew with its first position.
  *   k, v        device, bf16 [tokens][kv_heads][head_dim]
  *   cu_tokens   device, int32 [seqs + 1], ascending from 0, or NULL
  *   q, q_out    optional (q_heads = 0, NULL): the queries of the same
