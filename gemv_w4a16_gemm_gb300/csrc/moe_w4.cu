@@ -291,8 +291,9 @@ __global__ void __launch_bounds__(32 * ROUTE_WARPS) moe_route_kernel(const Route
             }
         }
         if (lane < p.topk) {
-            const float all = p.renormalize ? chosen : (p.sigmoid ? 1.f : sum);
-            const float w = all > 0.f ? mine / all * p.scale : 0.f;
+            // a NaN logit makes every softmax score NaN (sum), whichever are chosen; a sigmoid's its own
+            const float all = !p.sigmoid && (!p.renormalize || sum != sum) ? sum : p.renormalize ? chosen : 1.f;
+            const float w = all == 0.f ? 0.f : mine / all * p.scale;
             p.weights[m * p.topk + lane] = w;
             cluster.map_shared_rank(s_ids, 0)[m * p.topk + lane] = (uint16_t)id;
             atomicOr(cluster.map_shared_rank(&s_mask[0][0], 0) + 2 * id + (m >> 5), 1u << (m & 31));

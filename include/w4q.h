@@ -500,7 +500,8 @@ size_t kv8_workspace_bytes(int64_t seqs, int queries, int heads, int kv_heads,
  *   l = x . router^T (fp32 sums);  score = softmax(l), or sigmoid(l);
  *   the topk experts with the largest l (softmax) or score + bias (sigmoid),
  *   equal ones by the lower number;
- *   weight = scale * score, divided by the chosen scores' sum if renormalize;
+ *   weight = scale * score, divided by the chosen scores' sum if renormalize
+ *   (0 if that sum is 0);
  *   out[m] = bf16( sum_k weight * W2_e . bf16(silu(gate_e . x) * up_e . x) ),
  * the sum over the choices in their order.  Weights are exact, sums fp32;
  * tokens * topk * inter <= 4096: the inner bf16() keeps 16 bits instead.
@@ -515,6 +516,8 @@ size_t kv8_workspace_bytes(int64_t seqs, int queries, int heads, int kv_heads,
  *            NULL: the choice and its weights
  *   workspace  device, >= moe_workspace_bytes(...) bytes; contents are
  *            clobbered
+ * A NaN logit is chosen last; a token whose scores are NaN has NaN weights and
+ * results, and no effect on the others.
  * hidden and inter are multiples of 256 up to 32768, experts <= 512,
  * topk <= 16.  Only the chosen experts' weights are read.  Four launches. */
 int moe_w4a16(const void *x, const void *router, const float *bias,

@@ -1,0 +1,41 @@
+"""moe_w4a16, row by row: what a token gets does not depend on the others of its batch."""
+import math
+
+import pytest
+import torch
+
+from gemv_w4a16_gemm_gb300 import w4q
+from test_gpu_moe import Layer
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.mark.parametrize("sigmoid", [False, True])
+@pytest.mark.parametrize("renormalize", [False, True])
+@pytest.mark.parametrize("experts", [8, 200])
+@pytest.mark.parametrize("value", [math.nan, math.inf])
+def test_weights_of_a_token_without_finite_scores(cuda, sigmoid, renormalize, experts, value):
+    layer = Layer(256, 256, experts)
+    x = layer.x(11)
+    want_ids, want = torch.empty(11, 2, dtype=torch.int32, device=cuda), torch.empty(11, 2, device=cuda)
+    w4q.moe_w4a16(x, layer.router, layer.w13, layer.w2, 256, 2, sigmoid=sigmoid, renormalize=renormalize, ids=want_ids, weights=want)
+    x[4, 7] = value
+    x[4, 8] = -value          # inf - inf in every logit
+    layer.router[:, 7:9] = 1.0
+    ids, w = torch.empty(11, 2, dtype=torch.int32, device=cuda), torch.empty(11, 2, device=cuda)
+    out = w4q.moe_w4a16(x, layer.router, layer.w13, layer.w2, 256, 2, sigmoid=sigmoid, renormalize=renormalize, ids=ids, weights=w)
+    assert torch.isnan(w[4]).all() and torch.isnan(out[4]).all()
+    keep = [i for i in range(11) if i != 4]
+    assert torch.isfinite(w[keep]).all() and torch.isfinite(out[keep]).all()
+    assert (ids >= 0).all() and (ids < experts).all() and (ids[:, 0] != ids[:, 1]).all()
+
+
+@pytest.mark.parametrize("sigmoid", [False, True])
+def test_softmax_with_one_nan_logit_is_nan(cuda, sigmoid):
+    """A NaN in one expert's router row: every softmax score is NaN, of the sigmoid scores that expert's alone."""
+    layer = Layer(256, 256, 8)
+    layer.router[3] = math.nan
+    ids, w = torch.empty(5, 2, dtype=torch.int32, device=cuda), torch.empty(5, 2, device=cuda)
+    w4q.moe_w4a16(layer.x(5), layer.router, layer.w13, layer.w2, 256, 2, sigmoid=sigmoid, ids=ids, weights=w)
+    assert (ids != 3).all()
+    assert torch.isfinite(w).all() if sigmoid else torch.isnan(w).all()
