@@ -447,10 +447,11 @@ __device__ __forceinline__ void group_step(uint32_t q0, uint32_t q1, uint32_t sc
     }
 }
 
-// NT groups of 8 tokens at a time, at most; W warps; LOW = 1 (down, NT = 1): h comes in two parts.
-template <bool GATED, int NT, int W, int LOW>
+// NT groups of 8 tokens at a time, at most; W warps; LOW = 1: h is in two parts.
+template <bool GATED, int NT, int W, int LOW_H>
 __global__ void __launch_bounds__(32 * W, 1) moe_gemm_kernel(const GemmParams p)
 {
+    constexpr int LOW = GATED ? 0 : LOW_H;  // parts of a row of xf beyond the first
     extern __shared__ __align__(16) int s_before[];  // [experts + 1] each: costs before, offsets, numbers of the active experts
     int *s_offset = s_before + p.experts + 1, *s_expert = s_offset + p.experts + 1;
     uint8_t *s_ring = reinterpret_cast<uint8_t *>(s_before) + (12 * (p.experts + 1) + 15) / 16 * 16;  // [W][2][2 tiles]
@@ -579,7 +580,7 @@ __global__ void __launch_bounds__(32 * W, 1) moe_gemm_kernel(const GemmParams p)
                         const float h = gate / (1.f + __expf(-gate)) * up;
                         const __nv_bfloat16 hb = __float2bfloat16_rn(h);
                         dst[2 * e8] = *reinterpret_cast<const uint16_t *>(&hb);
-                        if (NT == 1 && p.low != 0) {
+                        if constexpr (LOW_H != 0) {
                             const __nv_bfloat16 lb = __float2bfloat16_rn(__hisinf(hb) ? 0.f : h - __bfloat162float(hb));
                             dst[p.low + 2 * e8] = *reinterpret_cast<const uint16_t *>(&lb);
                         }
@@ -768,7 +769,7 @@ __global__ void __launch_bounds__(128) moe_combine_kernel(const float *y, const 
     reinterpret_cast<uint2 *>(out + (int64_t)m * hidden)[d] = *reinterpret_cast<const uint2 *>(o);
 }
 
-template <bool GATED, int NT, int W, int LOW = 0>
+template <bool GATED, int NT, int W, int LOW>
 cudaError_t launch_variant(const GemmParams &p, int sm_count, cudaStream_t stream)
 {
     constexpr int fixed = W * (4 * TILE_BYTES + NT * 2048);
@@ -787,25 +788,25 @@ int groups_of(int tokens, int topk, int experts)
     return tokens <= 8 ? 1 : tokens * topk <= 16 * experts ? 2 : 4;
 }
 
-// h's rounding adds as much to the result's error as the result's own.  Over few terms that is
-// uneven and reaches 1.5 times the latter, and the call is short: then what the rounding left goes
-// through the second product too (1 token, 3 of 6 experts of 2048 x 256: error 0.0016 of the result
-// instead of 0.0025).  Beyond, time counts more: 1 token, 8 of 128 experts of 2048 x 768, 21.5 us
-// instead of 20.6, 4 tokens, 2 of 16 of 6656 x 4096, 84 instead of 76.
-constexpr size_t TWO_PARTS = 4096;
-bool two_parts(int tokens, int topk, int inter)
-{
-    return tokens <= 8 && (size_t)tokens * topk * inter <= TWO_PARTS;
-}
+// h's rounding adds as much to the result's error as the result's own: the two
+// together are 1.41 times the latter on average.  Over few terms, the topk *
+// inter of an output's sum, that is uneven, because a few large h decide: one
+// row in a hundred has 1.7 times with 256 terms, 1.66 with 2048, 1.6 with 4096,
+// 1.56 with 8192 (gaussian weights).  Up to 4096 terms what the rounding left
+// goes through the second product too, for any number of tokens, so that a
+// row's precision does not depend on its batch.  (64 tokens, 2 of 8 experts of
+// 2048 x 256: 30 us instead of 28; 8 tokens, 4 of 64 of 2048 x 1024: 36 instead of
+// 33; 64 tokens, 8 of 16 of 2048 x 512: 66 instead of 58.  In every call it would
+// cost 64 tokens, 2 of 16 of 6656 x 4096, 209 us instead of 183.)
+constexpr int TWO_PARTS = 4096;
+bool two_parts(int topk, int inter) { return topk * inter <= TWO_PARTS; }
 
-template <bool GATED>
+template <bool GATED, int LOW>
 cudaError_t launch_gemm(const GemmParams &p, int groups, int sm_count, cudaStream_t stream)
 {
-    if (!GATED && p.low != 0)
-        return launch_variant<false, 1, 12, 1>(p, sm_count, stream);
-    return groups == 1   ? launch_variant<GATED, 1, 12>(p, sm_count, stream)
-           : groups == 2 ? launch_variant<GATED, 2, 12>(p, sm_count, stream)
-                         : launch_variant<GATED, 4, 8>(p, sm_count, stream);
+    return groups == 1   ? launch_variant<GATED, 1, 12, LOW>(p, sm_count, stream)
+           : groups == 2 ? launch_variant<GATED, 2, 12, LOW>(p, sm_count, stream)
+                         : launch_variant<GATED, 4, 8, LOW>(p, sm_count, stream);
 }
 
 struct Workspace {
@@ -821,8 +822,7 @@ Workspace layout(int tokens, int hidden, int inter, int topk)
         return was;
     };
     w.xf = take((size_t)tokens * hidden * 2);
-    const size_t terms = (size_t)tokens * topk * inter;
-    w.h = take(2 * (terms + (terms < TWO_PARTS ? terms : TWO_PARTS)));  // grows with the tokens
+    w.h = take((size_t)tokens * topk * inter * (two_parts(topk, inter) ? 4 : 2));
     w.y = take((size_t)tokens * topk * hidden * 4);
     w.plan = take(sizeof(Plan));
     w.weights = take((size_t)tokens * topk * 4);
@@ -873,14 +873,14 @@ cudaError_t launch_moe(const Moe &a, int sm_count, void *workspace, cudaStream_t
     if (e != cudaSuccess)
         return e;
 
-    const int low = two_parts(a.tokens, a.topk, a.inter) ? a.tokens * a.topk * a.inter : 0;
+    const int low = two_parts(a.topk, a.inter) ? a.tokens * a.topk * a.inter : 0;
     GemmParams up = {static_cast<const uint8_t *>(a.w13), xf, plan, h, nullptr, a.tokens * a.topk, a.topk, a.experts,
                      a.hidden, a.inter, low};
     GemmParams down = {static_cast<const uint8_t *>(a.w2), h, plan, nullptr, y, a.tokens * a.topk, a.topk, a.experts,
                        a.inter, a.hidden, low};
-    e = launch_gemm<true>(up, groups, sm_count, stream);
+    e = low ? launch_gemm<true, 1>(up, groups, sm_count, stream) : launch_gemm<true, 0>(up, groups, sm_count, stream);
     if (e == cudaSuccess)
-        e = launch_gemm<false>(down, groups, sm_count, stream);
+        e = low ? launch_gemm<false, 1>(down, groups, sm_count, stream) : launch_gemm<false, 0>(down, groups, sm_count, stream);
     if (e != cudaSuccess)
         return e;
     const long long threads = (long long)a.tokens * (a.hidden / 4);

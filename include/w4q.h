@@ -504,7 +504,7 @@ size_t kv8_workspace_bytes(int64_t seqs, int queries, int heads, int kv_heads,
  *   (0 if that sum is 0);
  *   out[m] = bf16( sum_k weight * W2_e . bf16(silu(gate_e . x) * up_e . x) ),
  * the sum over the choices in their order.  Weights are exact, sums fp32;
- * tokens * topk * inter <= 4096: the inner bf16() keeps 16 bits instead.
+ * topk * inter <= 4096: the inner bf16() keeps 16 bits instead.
  *   x        device, bf16 [tokens][hidden]
  *   router   device, bf16 [experts][hidden]
  *   bias     device, fp32 [experts], or NULL; only with sigmoid != 0

@@ -39,3 +39,16 @@ def test_softmax_with_one_nan_logit_is_nan(cuda, sigmoid):
     w4q.moe_w4a16(layer.x(5), layer.router, layer.w13, layer.w2, 256, 2, sigmoid=sigmoid, ids=ids, weights=w)
     assert (ids != 3).all()
     assert torch.isfinite(w).all() if sigmoid else torch.isnan(w).all()
+
+
+@pytest.mark.parametrize("topk,inter", [(1, 256), (3, 256), (4, 1024), (2, 2048)])
+@pytest.mark.parametrize("tokens", [1, 5, 8, 9, 12, 16, 17, 33, 64])
+def test_a_row_keeps_its_precision_in_any_batch(cuda, topk, inter, tokens):
+    """topk * inter up to 4096: h enters the second product with 16 bits, whatever the number of tokens is.  The bound of
+    test_gpu_moe without the 2^-8 of a bf16 h."""
+    layer = Layer(512, inter, 6)
+    x = layer.x(64)[:tokens]
+    ids, weights = torch.empty(tokens, topk, dtype=torch.int32, device=cuda), torch.empty(tokens, topk, device=cuda)
+    out = w4q.moe_w4a16(x, layer.router, layer.w13, layer.w2, inter, topk, ids=ids, weights=weights)
+    ref, mag = layer.reference(x, ids.long(), weights)
+    assert ((out.double() - ref).abs() <= 2.0 ** -8 * ref.abs() + 2.0 ** -13 * mag).all()
