@@ -51,7 +51,10 @@ def _run(cmd):
 
 def _torch_dir() -> str:
     import importlib.util
-    return os.path.dirname(importlib.util.find_spec("torch").origin)
+    spec = importlib.util.find_spec("torch")
+    if spec is None:
+        raise RuntimeError("_w4q_binding.so needs torch's headers: torch is not installed")
+    return os.path.dirname(spec.origin)
 
 
 def _compile_binding(force: bool) -> str:
@@ -89,14 +92,15 @@ def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) 
     with ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
         binding = ex.submit(_compile_binding, force)
         objs = list(ex.map(compile_one, SOURCES))
+        # the library needs neither torch nor its headers, and is there without them
+        if force or _stale(LIB, objs):
+            tmp = LIB + ".tmp%d" % os.getpid()
+            cmd = [cc, *ARCH, "-shared", "-o", tmp, *objs, "-cudart", "static"]
+            r = subprocess.run(cmd, capture_output=True, text=True)
+            if r.returncode != 0:
+                raise RuntimeError("link failed:\n%s\n%s" % (r.stdout, r.stderr))
+            os.replace(tmp, LIB)
         binding_obj = binding.result()
-    if force or _stale(LIB, objs):
-        tmp = LIB + ".tmp%d" % os.getpid()
-        cmd = [cc, *ARCH, "-shared", "-o", tmp, *objs, "-cudart", "static"]
-        r = subprocess.run(cmd, capture_output=True, text=True)
-        if r.returncode != 0:
-            raise RuntimeError("link failed:\n%s\n%s" % (r.stdout, r.stderr))
-        os.replace(tmp, LIB)
     if force or _stale(BINDING, [binding_obj, LIB]):
         tmp = BINDING + ".tmp%d" % os.getpid()
         lib = os.path.join(_torch_dir(), "lib")
