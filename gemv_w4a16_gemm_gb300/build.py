@@ -93,9 +93,9 @@ def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) 
         binding = ex.submit(_compile_binding, force)
         objs = list(ex.map(compile_one, SOURCES))
         # the library needs neither torch nor its headers, and is there without them
-        if force or _stale(LIB, objs):
+        if force or _stale(LIB, [*objs, os.path.abspath(__file__)]):
             tmp = LIB + ".tmp%d" % os.getpid()
-            cmd = [cc, *ARCH, "-shared", "-o", tmp, *objs, "-cudart", "static"]
+            cmd = [cc, *ARCH, "-shared", "-Xlinker", "-soname=" + os.path.basename(LIB), "-o", tmp, *objs, "-cudart", "static"]
             r = subprocess.run(cmd, capture_output=True, text=True)
             if r.returncode != 0:
                 raise RuntimeError("link failed:\n%s\n%s" % (r.stdout, r.stderr))
@@ -104,6 +104,7 @@ def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) 
     if force or _stale(BINDING, [binding_obj, LIB]):
         tmp = BINDING + ".tmp%d" % os.getpid()
         lib = os.path.join(_torch_dir(), "lib")
+        # the library is needed by its name, and found beside the module: a copied or moved package uses its own
         _run(["g++", "-shared", "-o", tmp, binding_obj, LIB, "-L" + lib, "-lc10", "-lc10_cuda", "-ltorch_cpu",
               "-ltorch_python", "-Wl,-rpath,$ORIGIN", "-Wl,-rpath," + lib])
         os.replace(tmp, BINDING)

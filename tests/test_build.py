@@ -1,5 +1,8 @@
 """The build: what each of the two shared objects needs, and when it is made anew."""
 import os
+import shutil
+import subprocess
+import sys
 
 import pytest
 
@@ -24,3 +27,15 @@ def test_the_library_is_built_without_the_python_module(elsewhere, monkeypatch):
     with pytest.raises(RuntimeError, match="no torch headers"):
         libbuild.build()
     assert os.path.exists(libbuild.LIB)
+
+
+def test_a_copy_of_the_package_loads_its_own_library(tmp_path):
+    """The Python module takes the library beside it, wherever the package lies."""
+    libbuild.build()
+    copy = tmp_path / os.path.basename(libbuild.PKG)
+    shutil.copytree(libbuild.PKG, copy, ignore=shutil.ignore_patterns("_build", "csrc", "__pycache__"))
+    code = ("from gemv_w4a16_gemm_gb300 import w4q; w4q._native(); "
+            "print('\\n'.join({l.split()[-1] for l in open('/proc/self/maps') if 'w4q' in l}))")
+    r = subprocess.run([sys.executable, "-c", code], cwd=tmp_path, capture_output=True, text=True)
+    assert r.returncode == 0, r.stderr
+    assert sorted(r.stdout.split()) == [str(copy / "_w4q_binding.so"), str(copy / "libw4q.so")]
