@@ -57,15 +57,27 @@ def _torch_dir() -> str:
     return os.path.dirname(spec.origin)
 
 
+def _torch_id() -> str:
+    """The installed torch that the Python module is compiled against."""
+    with open(os.path.join(_torch_dir(), "version.py")) as f:
+        return _torch_dir() + "\n" + f.read()
+
+
 def _compile_binding(force: bool) -> str:
     """The Python module of binding.cpp, compiled against the torch headers (no torch import)."""
-    src, obj = os.path.join(CSRC, "binding.cpp"), os.path.join(BUILD, "binding.o")
-    if force or _stale(obj, [src, os.path.join(INCLUDE, "w4q.h")]):
+    src, obj, stamp = os.path.join(CSRC, "binding.cpp"), os.path.join(BUILD, "binding.o"), os.path.join(BUILD, "binding.torch")
+    torch_id, was = _torch_id(), None
+    if os.path.exists(stamp):
+        with open(stamp) as f:
+            was = f.read()
+    if force or was != torch_id or _stale(obj, [src, os.path.join(INCLUDE, "w4q.h")]):
         inc = os.path.join(_torch_dir(), "include")
         cuda = os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(nvcc()))), "include")
         _run(["g++", "-O2", "-std=c++17", "-fPIC", "-I", INCLUDE, "-isystem", inc,
               "-isystem", os.path.join(inc, "torch", "csrc", "api", "include"), "-isystem", cuda,
               "-isystem", sysconfig.get_paths()["include"], "-c", src, "-o", obj])
+        with open(stamp, "w") as f:
+            f.write(torch_id)
     return obj
 
 

@@ -39,3 +39,20 @@ def test_a_copy_of_the_package_loads_its_own_library(tmp_path):
     r = subprocess.run([sys.executable, "-c", code], cwd=tmp_path, capture_output=True, text=True)
     assert r.returncode == 0, r.stderr
     assert sorted(r.stdout.split()) == [str(copy / "_w4q_binding.so"), str(copy / "libw4q.so")]
+
+
+def test_another_torch_makes_the_python_module_anew(elsewhere, monkeypatch):
+    runs = []
+    def run(cmd):  # a compiler that writes an empty output
+        runs.append(cmd)
+        open(cmd[cmd.index("-o") + 1], "w").close()
+    monkeypatch.setattr(libbuild, "_run", run)
+    libbuild.build()
+    assert len(runs) == 2          # compiled and linked
+    libbuild.build()
+    assert len(runs) == 2
+    monkeypatch.setattr(libbuild, "_torch_id", lambda: "another torch")
+    libbuild.build()
+    assert len(runs) == 4
+    libbuild.build()
+    assert len(runs) == 4
