@@ -417,8 +417,10 @@ int qk_norm_rope(const void *q, const void *k, int64_t tokens, int q_heads,
  *                [0, blocks) is a hole: nothing is written to it, the
  *                attention leaves its positions out.
  *   seq_lens     int32 [seqs]: the sequences' lengths, the tokens of the
- *                current step among them; 0 (or less) is an idle sequence;
- *                a length beyond width * page counts as width * page.
+ *                current step among them; 0 (or less) is an idle sequence.
+ *                Positions from width * page on are in no page: nothing is
+ *                written for them, they read as zeros, and the attention
+ *                takes such a length as width * page.
  * All device pointers.  page is 16, 32, 64 or 128; seqs <= 4096; a page
  * that a call appends to belongs to one sequence alone. */
 typedef struct {
