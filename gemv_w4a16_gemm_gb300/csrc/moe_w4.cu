@@ -371,7 +371,7 @@ struct GemmParams {
     const Plan *plan;
     uint16_t *h;         // gate/up: [entries][rows_out] in fragment order
     float *y;            // down: [entries][rows_out]
-    int entries, topk, experts;
+    int topk, experts;
     int K;         // columns
     int rows_out;  // rows per expert of the result
     int low;       // elements from h to what its rounding left, or 0
@@ -874,9 +874,9 @@ cudaError_t launch_moe(const Moe &a, int sm_count, void *workspace, cudaStream_t
         return e;
 
     const int low = two_parts(a.topk, a.inter) ? a.tokens * a.topk * a.inter : 0;
-    GemmParams up = {static_cast<const uint8_t *>(a.w13), xf, plan, h, nullptr, a.tokens * a.topk, a.topk, a.experts,
+    GemmParams up = {static_cast<const uint8_t *>(a.w13), xf, plan, h, nullptr, a.topk, a.experts,
                      a.hidden, a.inter, low};
-    GemmParams down = {static_cast<const uint8_t *>(a.w2), h, plan, nullptr, y, a.tokens * a.topk, a.topk, a.experts,
+    GemmParams down = {static_cast<const uint8_t *>(a.w2), h, plan, nullptr, y, a.topk, a.experts,
                        a.inter, a.hidden, low};
     e = low ? launch_gemm<true, 1>(up, groups, sm_count, stream) : launch_gemm<true, 0>(up, groups, sm_count, stream);
     if (e == cudaSuccess)
