@@ -3,8 +3,10 @@
 // of the C entry point of the same name.  No arithmetic.
 //
 // A call of these operators takes 2 to 10 us on the GPU for a few tokens; the
-// same checks made in Python took 20 to 35 us a call on the host.  Here they
-// read the tensors' fields directly: 3 to 8 us with the launch.
+// same checks made in Python took 25 to 37 us a call on the host.  Here they
+// read the tensors' fields directly: 2.3 to 2.7 us with the launch (7 with the
+// four of the experts), 1.5 to 3 more for each tensor that the call makes, and
+// 11 for an attention workspace, which has to be zeroed.
 //
 // Every function takes positional arguments from w4q.py and returns
 // (status, results...); a wrong type or shape raises ValueError.

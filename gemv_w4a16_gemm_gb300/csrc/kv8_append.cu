@@ -18,15 +18,17 @@
 // maximum; int8 has no such code, so s' is NaN and the page's head reads as NaN.
 //
 // What bounds it: each element is read and written once, some fifty
-// instructions for a lane's 8 of them; HBM for prompts, one launch for single
-// tokens.  Layout: D / 8 lanes hold a head row.  A lane has two groups of 4
+// instructions for a lane's 8 of them.  Rotation of prompts: HBM.  The writer of
+// prompts: no unit is full (64% of the issue slots, ALU 54%, HBM 40%), its warps
+// wait for loads and for each other's results.  Single tokens: one launch and
+// its chain of dependent loads.  Layout: D / 8 lanes hold a head row.  A lane has two groups of 4
 // elements, one from each half of the rotated part (or 8 beyond it), so both
 // partners of its pairs and their 4 angles are its own: the norm's sum is the
 // only thing that lanes exchange.  Measured: 8191 tokens of 56 heads of 128
-// rotated in 42.9 us, 81% of the measured copy bandwidth; 5 x 2000 tokens (8 kv
-// heads, 32 query heads) written in 37 us and read in 10, bound by the
-// quantization's instructions; 64 x 1 written and read in 8.5 us, bound by the
-// chain of dependent loads.  (Query heads in a launch of their own after the
+// rotated in 42.9 us, 81% of the measured copy bandwidth; 5862 tokens of 5
+// sequences (8 kv heads, 32 query heads, e4m3) written in 37.8 us for the 19.9 of
+// their bytes and read back in 9.2 for 5.3, 16 bytes a lane in flight; 64 x 1
+// written in 3.8 us, written and read (1881 tokens) in 8.4.  (Query heads in a launch of their own after the
 // pages': 55 us for 5 x 2000; a warp going through several heads of a page: 50.)
 #include <cuda_fp16.h>
 

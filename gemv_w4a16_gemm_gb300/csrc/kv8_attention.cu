@@ -34,10 +34,14 @@
 // the next tile's K is loaded as soon as this tile's is used up, its V likewise,
 // and the one after it is on its way to L2.  (The same bytes through a ring of
 // cp.async in shared memory: 434 us instead of 347 for 64 x 16000 x 8 heads of
-// 128; without the prefetch to L2 349, with it 319, without spills 311, now 308:
-// 2.1 GB at 6.8 TB/s, the measured copy bandwidth.  Shorter calls are bound by
-// their start, 3 us to the first tile, and by the joins, 4 us after the last:
-// 32 x 4000 takes 34 us for the 22 of its bytes, 1 x 131071 31 for 20.)
+// 128; without the prefetch to L2 349, with it 319, without spills 311, now 303
+// to 308: 2.1 GB at 6.8 TB/s, the measured copy bandwidth.  Shorter calls are
+// bound by their start, 3 us to the first tile, and by the joins, 4 us after the
+// last: 32 x 4000 takes 34 us for the 22 of its bytes, 1 x 131071 31 for 20.
+// More query rows than a tile has go in further units, which read the cache
+// again: 48 x up to 4000, 8 kv heads of 128, 54 us with 16 rows, 88 with 32, 158
+// with 64, for 31 of bytes; the products then run at 120 to 170 TFLOP/s, at the
+// instruction latency of 2 warps a scheduler.)
 //
 // Work.  One chunk = 64 positions (a 16-position tile for each of 4 warps) of
 // one (sequence, kv head, row tile), its unit.  All chunks of a call lie in one
@@ -73,8 +77,8 @@ constexpr float P_SCALE = 128.f;   // 2^7: P <= 2^8 becomes at most 2^15 in f16
 constexpr int W = 4;               // warps of a group
 // With START 3 and 5 in place of 4, 1 x 130 takes 6.8 and 5.8 us instead of 5.8, 16 x 1000 with 2
 // queries 14.6 and 14.9 instead of 15.4, 8 x 6000 with head_dim 256 22.1 and 18.1 instead of 20.9; with
-// SNAP 16 and 24 in place of 20, drafts over a window of 1024 29.5 and 25.9 instead of 26.3, 32 x 4000
-// 33.8 and 34.9 instead of 33.8.
+// SNAP 16 and 24 in place of 20, drafts over a window of 1024 29.6 and 26.6 instead of 26.6 (one of 1280:
+// 32.9 and 30.2 instead of 33.9; 1600: 36.4 and 38.2 instead of 36.8), 32 x 4000 33.8 and 34.9 instead of 33.8.
 constexpr int START = 4;           // a unit's beginning costs about as much as this many chunks
 constexpr int SNAP = 20;           // units up to this many chunks stay in one CTA
 constexpr int JOIN = 16;           // neighbours whose partial sums are joined first, of a unit with more parts
@@ -958,9 +962,10 @@ cudaError_t launch_kv8_attention(const Kv8 &c, const void *q, int64_t q_stride, 
     p.join_count = p.unit_count + sm_count;
     p.part = reinterpret_cast<float *>(static_cast<char *>(workspace) + counter_bytes(sm_count));
 // Groups per CTA: as many as leave every accumulator, query fragment and load in registers (168 a
-// thread with 3 groups, 255 with 2).  One group more spills 10 to 80 words and costs more than its
-// warps bring: head_dim 128, 8 rows, 64 x 16000: 320 us with 4 groups, 311 with 3; 16 rows, 64 x
-// 8000: 242 with 3, 181 with 2; head_dim 64, 32 rows, 64 x 8000: 207 with 3, 165 with 2.
+// thread with 3 groups, 255 with 2; looking for e4m3's NaN spills 4 words at head_dim 128 with 8 rows and
+// 2 at 256, 0.3% of 32 x 4000).  One group more spills 10 to 80 words and costs more than its warps
+// bring: head_dim 128, 8 rows, 64 x 16000: 320 us with 4 groups, 311 with 3; 16 rows, 64 x 8000: 242
+// with 3, 181 with 2; head_dim 64, 32 rows, 64 x 8000: 207 with 3, 165 with 2.
 #define W4Q_ATTN(D, NT, G)                                                        \
     return c.fp8 ? launch_variant<D, NT, true, G>(p, sm_count, stream)           \
                  : launch_variant<D, NT, false, G>(p, sm_count, stream)

@@ -7,7 +7,7 @@
 //
 // What bounds it: the chosen experts' weights, 19/32 bytes each, are read once
 // from HBM; with one token that is a few microseconds, so launches and the
-// depth of dependent loads count more (8 of 128 experts of 2048 x 768: 20.6 us,
+// depth of dependent loads count more (8 of 128 experts of 2048 x 768: 20.8 us,
 // 6.3 of them routing, for 3.4 of bytes).  With more tokens the products' 2.2
 // instructions a weight and lane, at the latency of 3 warps a scheduler, take
 // longer than the bytes (64 tokens, 2 of 16 experts of 6656 x 4096: 183 us for
@@ -46,7 +46,7 @@
 // or 2^123 makes it (q - z) 2^-6, exactly.  The MMAs sum (q - z) x 2^-6 per
 // group of 32 and acc += s * sum in fp32: the weights are never rounded.  h is
 // rounded to bf16, as an activation between two of the library's linear layers
-// is (in two parts where its terms are few, see two_parts).
+// is (in two parts where an output has few terms, see two_parts).
 #include <cooperative_groups.h>
 
 #include "common.cuh"
