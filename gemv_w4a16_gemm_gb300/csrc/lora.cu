@@ -13,8 +13,10 @@
 // of 16 ranks or outputs as their rows and tokens as their columns.  A dot product does
 // not depend on the order of its terms, so k runs in the order in which 16-byte pieces of
 // a row lie in the lanes' registers, and the weights need no rearrangement.  h enters the
-// second product as the sum of two bf16 (16 bits): in one its rounding would add 2^-9 of
-// the addend to the result.
+// second product as the sum of three bf16, which is all of its 24 bits, so that a row is as
+// precise alone as in any batch.  (As two, 16 bits, one result in 600 was another bf16 than the
+// exact sum's, one in 4000 to 11000 so; the third costs nothing for up to 2 tokens of an adapter, 0.3 us in 11 for 16 of
+// rank 32, and 5 in 25 for 64 of rank 256, whose time is the MMAs'.)
 //
 // What bounds it: the used adapters' bytes, read once each, for large ones (64 adapters of
 // rank 64, 6656 to 19968: 220 MB in 45.6 us, 4.9 TB/s with both launches' beginnings, of
@@ -23,6 +25,7 @@
 // weights through a ring of bulk copies in shared memory, so that some 100 KB an SM are in
 // flight whatever the MMAs and their registers need.
 #include <atomic>
+#include <cfloat>
 
 #include "common.cuh"
 #include "decode.h"
@@ -357,22 +360,24 @@ __global__ void __maxnreg__(128) lora_down_kernel(const LoraArgs p)
 // one bulk copy.
 constexpr int COLS = 32;
 constexpr int UP_MAX_STAGES = 8;
-constexpr int UP_SMEM = 110 * 1024;  // for two CTAs an SM
+constexpr int UP_SMEM = 112 * 1024;  // for two CTAs an SM, beside 1 KB of static shared memory
 
 // Warps of a CTA that multiply: fewer for the larger pieces of high ranks.  Beside two of them
-// others help to add up h (rank 256, 33 tokens of one adapter, 4096 to 4096: 21.6 -> 15.2 us);
+// others help to add up h (rank 256, 33 tokens of one adapter, 4096 to 4096: by 6 us, now 16.9);
 // with four it costs more than it saves, since a CTA of both launches then has no room on an SM
 // (32 of rank 128: 19.4 without, 20.1 with).
 constexpr int UP_WARPS = 8;
 __host__ __device__ constexpr int up_warps(int rank) { return rank <= 64 ? UP_WARPS : (rank <= 128 ? 4 : 2); }
 __host__ __device__ constexpr int up_block_warps(int rank) { return rank <= 128 ? up_warps(rank) : UP_WARPS; }
 
-// h lies in shared memory as the MMAs' operand of 8 columns, NT tiles of them: up to 4
-// tokens: 1 tile, the first bf16 of each in columns 0 to 3, the second in 4 to 7; up to 8:
-// 2 tiles, the first and the second; up to 16: 4, two and two.  (mma.sync's rate, a
-// sixteenth of tcgen05's, is what counts here: with the tokens as the 16 rows of the other
-// operand twice as many were needed, and 64 adapters of rank 64 took 49 us.)
-__host__ __device__ constexpr int h_tiles(int count) { return count <= 4 ? 1 : (count <= 8 ? 2 : 4); }
+// h lies in shared memory as the MMAs' operand of 8 columns, NT tiles of them: up to 2
+// tokens: 1 tile, the first bf16 of each in columns 0 and 1, the second in 2 and 3, the third
+// in 4 and 5; up to 4: 2 tiles, the first bf16 in columns 0 to 3 of one, the second in 4 to 7,
+// the third in 0 to 3 of the other; up to 8: 3 tiles, one for each bf16; up to 16: 6.
+// (mma.sync's rate, a sixteenth of tcgen05's, is what counts here: with the tokens as the 16
+// rows of the other operand 64 adapters of rank 64 took 49 us.)
+__host__ __device__ constexpr int h_tiles(int count) { return count <= 2 ? 1 : (count <= 4 ? 2 : (count <= 8 ? 3 : 6)); }
+__host__ __device__ constexpr int h_sums(int nt) { return (nt + 2) / 3; }  // tiles of results
 
 // Bytes from column to column of h: two columns' 16-byte pieces (ranks in 32s), or four
 // columns' 8-byte pieces, lie in different banks.
@@ -381,24 +386,37 @@ __host__ __device__ constexpr int h_pitch(int rank)
     return rank % 32 == 0 ? 2 * rank + (rank % 64 == 0 ? 64 : 0) : 32 * ((rank + 15) / 16 | 1);
 }
 
-// Four ranks from k on of token t's h, as two bf16 each; slots: 4, 8 or 16 tokens' places.
+// Four ranks from k on of token t's h, as three bf16 each; slots: 2, 4, 8 or 16 tokens' places.
 __device__ __forceinline__ void store_h(uint8_t *h, int pitch, int slots, int t, int k, float4 s)
 {
     const float f[4] = {s.x, s.y, s.z, s.w};
-    uint32_t h2[4], l2[4];
+    uint32_t b[3][4];
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-        const __nv_bfloat16 b = __float2bfloat16_rn(f[e]);
-        const float rest = f[e] - __bfloat162float(b);
-        h2[e] = __bfloat16_as_ushort(b);
-        // what is not finite stays as it is in the first part
-        l2[e] = fabsf(f[e]) <= 3.3e38f ? __bfloat16_as_ushort(__float2bfloat16_rn(rest)) : 0u;
+        // the first 8 bits, which stay finite; what is not finite is the first part alone
+        const bool finite = fabsf(f[e]) <= FLT_MAX;
+        b[0][e] = finite ? __float_as_uint(f[e]) >> 16 : __bfloat16_as_ushort(__float2bfloat16_rn(f[e]));
+        float rest = finite ? f[e] - bf16hi_to_f32(__float_as_uint(f[e])) : 0.f;
+#pragma unroll
+        for (int i = 1; i < 3; ++i) {
+            const __nv_bfloat16 v = __float2bfloat16_rn(rest);
+            b[i][e] = __bfloat16_as_ushort(v);
+            rest -= __bfloat162float(v);
+        }
     }
-    const int col = slots == 16 ? t % 8 + t / 8 * 16 : t;
-    *reinterpret_cast<uint2 *>(h + col * pitch + 2 * k) = make_uint2(h2[0] | h2[1] << 16, h2[2] | h2[3] << 16);
-    *reinterpret_cast<uint2 *>(h + (col + (slots == 4 ? 4 : 8)) * pitch + 2 * k) = make_uint2(l2[0] | l2[1] << 16, l2[2] | l2[3] << 16);
+    const int col = slots == 16 ? t % 8 + t / 8 * 24 : t, step = slots == 16 ? 8 : slots;
+#pragma unroll
+    for (int i = 0; i < 3; ++i)
+        *reinterpret_cast<uint2 *>(h + (col + i * step) * pitch + 2 * k) = make_uint2(b[i][0] | b[i][1] << 16, b[i][2] | b[i][3] << 16);
 }
-__device__ __forceinline__ int h_slots(int count) { return count <= 4 ? 4 : (count <= 8 ? 8 : 16); }
+// Zeros, from rank k on, in the columns of a tile that no token has.
+__device__ __forceinline__ void store_h_rest(uint8_t *h, int pitch, int slots, int t, int k)
+{
+    if (slots <= 4)
+        for (int col = 3 * slots + t; col < (slots == 2 ? 8 : 16); col += slots)
+            *reinterpret_cast<uint2 *>(h + col * pitch + 2 * k) = make_uint2(0u, 0u);
+}
+__device__ __forceinline__ int h_slots(int count) { return count <= 2 ? 2 : (count <= 4 ? 4 : (count <= 8 ? 8 : 16)); }
 
 // h of a tile's tokens, the parts added up in their order; zeros in the columns of other
 // tokens and behind the last rank.
@@ -420,6 +438,7 @@ __device__ __forceinline__ void load_h(const LoraArgs &p, const Line &l, int til
                 s.x += v[q].x, s.y += v[q].y, s.z += v[q].z, s.w += v[q].w;
         }
         store_h(h, pitch, slots, t, k, s);
+        store_h_rest(h, pitch, slots, t, k);
     }
 }
 
@@ -430,7 +449,7 @@ __device__ __forceinline__ void load_h(const LoraArgs &p, const Line &l, int til
 // never lie in the same banks.  Else 8-byte pieces, 4 ranks a lane.
 template <bool WIDE, int NT>
 __device__ __forceinline__ void multiply(const LoraArgs &p, const uint8_t *stage, const uint8_t *h, int pitch,
-                                         float (&acc)[2][(NT + 1) / 2][4])
+                                         float (&acc)[2][h_sums(NT)][4])
 {
     const int lane = threadIdx.x & 31, q = lane >> 2, c = lane & 3, row = 2 * p.rank;
     const uint8_t *from = stage + 4 * q * row;
@@ -459,12 +478,12 @@ __device__ __forceinline__ void multiply(const LoraArgs &p, const uint8_t *stage
 #pragma unroll
                         for (int i = 0; i < 2; ++i) {
                             const uint32_t f0[4] = {w[b][i][0].x, w[b][i][1].x, w[b][i][0].y, w[b][i][1].y};
-                            mma_bf16(acc[i][n / 2], f0, v.x, v.y, acc[i][n / 2]);
+                            mma_bf16(acc[i][n / 3], f0, v.x, v.y, acc[i][n / 3]);
                         }
 #pragma unroll
                         for (int i = 0; i < 2; ++i) {
                             const uint32_t f1[4] = {w[b][i][0].z, w[b][i][1].z, w[b][i][0].w, w[b][i][1].w};
-                            mma_bf16(acc[i][n / 2], f1, v.z, v.w, acc[i][n / 2]);
+                            mma_bf16(acc[i][n / 3], f1, v.z, v.w, acc[i][n / 3]);
                         }
                     }
         }
@@ -483,7 +502,7 @@ __device__ __forceinline__ void multiply(const LoraArgs &p, const uint8_t *stage
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
                     const uint32_t f[4] = {w[i][0].x, w[i][1].x, w[i][0].y, w[i][1].y};
-                    mma_bf16(acc[i][n / 2], f, v.x, v.y, acc[i][n / 2]);
+                    mma_bf16(acc[i][n / 3], f, v.x, v.y, acc[i][n / 3]);
                 }
             }
         }
@@ -524,7 +543,7 @@ __device__ __forceinline__ void add_store(const LoraArgs &p, int tok, int n, con
 
 // Units whose y is loaded ahead: a unit of a low rank takes less time than that (with one, 64
 // tokens of as many adapters of rank 8, 2048 to 50000, took 45 us, 34 so, and 33 with four).
-__host__ __device__ constexpr int y_ahead(int nt) { return nt <= 2 ? 2 : 1; }
+__host__ __device__ constexpr int y_ahead(int nt) { return nt <= 3 ? 2 : 1; }
 
 // A warp's ring in the second launch.
 struct UpRing {
@@ -577,13 +596,13 @@ template <bool WIDE, int NT>
 __device__ __forceinline__ void add_units(const LoraArgs &p, UpRing &ring, const __nv_bfloat16 *B, const int *toks, int count, float scale,
                                           int u0, int u1, int step, const uint8_t *h, int pitch)
 {
-    // NT = 1: lane column c adds the halves of one token; else it has two tokens of each 8
-    constexpr int TOKS = NT == 1 ? 1 : NT;
+    // NT = 1 and 2: lane column c adds the parts of one token; else it has two tokens of each 8
+    constexpr int TOKS = NT <= 2 ? 1 : (NT == 3 ? 2 : 4);
     const int lane = threadIdx.x & 31, q = lane >> 2, c = lane & 3;
     int tok[TOKS];
 #pragma unroll
     for (int e = 0; e < TOKS; ++e) {
-        const int t = NT == 1 ? 2 * (c & 1) + (c >> 1) : 8 * (e / 2) + 2 * c + e % 2;
+        const int t = NT == 1 ? (c < 2 ? c : count) : (NT == 2 ? 2 * (c & 1) + (c >> 1) : 8 * (e / 2) + 2 * c + e % 2);
         tok[e] = t < count ? toks[t] : -1;
     }
     constexpr int AHEAD = y_ahead(NT);
@@ -600,25 +619,29 @@ __device__ __forceinline__ void add_units(const LoraArgs &p, UpRing &ring, const
         bases[AHEAD - 1] = load_base<TOKS>(p, tok, v < u1 ? v * COLS + 4 * q : p.N);
         if (!unit_ready(p, ring, u, u1, step))
             continue;
-        float acc[2][(NT + 1) / 2][4];
+        float acc[2][h_sums(NT)][4];
 #pragma unroll
         for (int i = 0; i < 2; ++i)
 #pragma unroll
-            for (int n = 0; n < (NT + 1) / 2; ++n)
+            for (int n = 0; n < h_sums(NT); ++n)
 #pragma unroll
                 for (int e = 0; e < 4; ++e)
                     acc[i][n][e] = 0.f;
         multiply<WIDE, NT>(p, ring.mem + ring.slot * ring.stage_bytes, h, pitch, acc);
         unit_done(p, ring, B, u, u1, step);
         const int n = u * COLS + 4 * q;
-        if (NT == 1) {
-            // columns 2 c and 2 c + 1: the lane two columns on holds the other halves
+        if (NT <= 2) {
             float d[4];
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                const float (&a)[4] = acc[j / 2][0];
-                const float mine = c < 2 ? a[2 * (j & 1)] : a[2 * (j & 1) + 1], give = c < 2 ? a[2 * (j & 1) + 1] : a[2 * (j & 1)];
-                d[j] = mine + __shfl_xor_sync(0xffffffffu, give, 2);
+                const float first = acc[j / 2][0][2 * (j & 1)], second = acc[j / 2][0][2 * (j & 1) + 1];  // columns 2 c and 2 c + 1
+                if (NT == 1) {  // a token's parts are in lane columns 0 to 2: token 0 goes to column 0, token 1 to 1
+                    const float got = __shfl_xor_sync(0xffffffffu, c & 1 ? first : second, 1);
+                    const float sum = c < 2 ? (c ? second : first) + got : (c == 2 ? first : got);
+                    d[j] = sum + __shfl_xor_sync(0xffffffffu, sum, 2);
+                } else {  // the lane two columns on holds the second parts of the same tokens
+                    d[j] = (c < 2 ? first : second) + __shfl_xor_sync(0xffffffffu, c < 2 ? second : first, 2);
+                }
             }
             if (tok[0] >= 0 && n < p.N)
                 add_store(p, tok[0], n, d, scale, base.v[0]);
@@ -633,20 +656,18 @@ __device__ __forceinline__ void add_units(const LoraArgs &p, UpRing &ring, const
     }
 }
 
-// The same for one token and a rank of R: a lane has an output and all of h in registers, which
+// The same for one token and a rank of R: a lane has an output and all of h, in fp32, in registers, which
 // takes a third of the instructions (16 tokens of as many adapters of rank 16, 6656 to 19968: 10.7
 // -> 8.8 us).
 template <int R>
 __device__ __forceinline__ void add_units_one(const LoraArgs &p, UpRing &ring, const __nv_bfloat16 *B, int tok, float scale, int u0, int u1,
-                                              int step, const uint8_t *h, int pitch)
+                                              int step, const uint8_t *h)
 {
     const int lane = threadIdx.x & 31;
     float2 hv[R / 2];
 #pragma unroll
-    for (int k = 0; k < R / 2; ++k) {
-        const uint32_t hi = *reinterpret_cast<const uint32_t *>(h + 4 * k), lo = *reinterpret_cast<const uint32_t *>(h + 4 * pitch + 4 * k);
-        hv[k] = {bf16lo_to_f32(hi) + bf16lo_to_f32(lo), bf16hi_to_f32(hi) + bf16hi_to_f32(lo)};
-    }
+    for (int k = 0; k < R / 2; ++k)
+        hv[k] = reinterpret_cast<const float2 *>(h)[k];
     const __nv_bfloat16 *y = p.y + tok * p.y_stride;
     __nv_bfloat16 *out = p.out + tok * p.out_stride;
     auto load = [&](int u) { return u < u1 && u * COLS + lane < p.N ? y[u * COLS + lane] : __nv_bfloat16(); };
@@ -793,12 +814,14 @@ __global__ void __launch_bounds__(32 * UP_WARPS, 2) lora_up_kernel(const LoraArg
         load_h(p, l, tile, toks, count, pitch, h);
         __syncthreads();
         const float scale = p.scales != nullptr ? __ldg(p.scales + adapter) : 1.f;
-        if (count <= 4)
+        if (count <= 2)
             add_units<WIDE, 1>(p, ring, B, toks, count, scale, u0, u1, warps, h, pitch);
-        else if (count <= 8)
+        else if (count <= 4)
             add_units<WIDE, 2>(p, ring, B, toks, count, scale, u0, u1, warps, h, pitch);
+        else if (count <= 8)
+            add_units<WIDE, 3>(p, ring, B, toks, count, scale, u0, u1, warps, h, pitch);
         else
-            add_units<WIDE, 4>(p, ring, B, toks, count, scale, u0, u1, warps, h, pitch);
+            add_units<WIDE, 6>(p, ring, B, toks, count, scale, u0, u1, warps, h, pitch);
     }
     if (!waited)
         pdl_wait();
@@ -948,7 +971,8 @@ __global__ void __launch_bounds__(32 * UP_WARPS, 2) lora_cluster_kernel(const Lo
         }
         cluster_arrive();
         cluster_wait();
-        const int slots = h_slots(count);
+        const bool one = !WIDE && count == 1 && p.rank <= 16;
+        const int slots = one ? 1 : h_slots(count);
         for (int i = threadIdx.x; i < slots * ranks * 4; i += blockDim.x) {
             const int t = i / (4 * ranks), k = i % (4 * ranks) * 4;
             float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -961,22 +985,29 @@ __global__ void __launch_bounds__(32 * UP_WARPS, 2) lora_cluster_kernel(const Lo
                 for (int d = 0; d < MAX_CLUSTER; ++d)
                     v.x += o[d].x, v.y += o[d].y, v.z += o[d].z, v.w += o[d].w;
             }
-            store_h(h, pitch, slots, t, k, v);
+            if (one) {
+                reinterpret_cast<float4 *>(h)[i] = v;
+            } else {
+                store_h(h, pitch, slots, t, k, v);
+                store_h_rest(h, pitch, slots, t, k);
+            }
         }
         cluster_arrive();
         busy = true;
         __syncthreads();
         const float scale = p.scales != nullptr ? __ldg(p.scales + adapter) : 1.f;
-        if (!WIDE && count == 1 && p.rank == 8)
-            add_units_one<8>(p, ring, B, toks[0], scale, u0, u1, warps, h, pitch);
-        else if (!WIDE && count == 1 && p.rank == 16)
-            add_units_one<16>(p, ring, B, toks[0], scale, u0, u1, warps, h, pitch);
-        else if (count <= 4)
+        if (one && p.rank == 8)
+            add_units_one<8>(p, ring, B, toks[0], scale, u0, u1, warps, h);
+        else if (one)
+            add_units_one<16>(p, ring, B, toks[0], scale, u0, u1, warps, h);
+        else if (count <= 2)
             add_units<WIDE, 1>(p, ring, B, toks, count, scale, u0, u1, warps, h, pitch);
-        else if (count <= 8)
+        else if (count <= 4)
             add_units<WIDE, 2>(p, ring, B, toks, count, scale, u0, u1, warps, h, pitch);
+        else if (count <= 8)
+            add_units<WIDE, 3>(p, ring, B, toks, count, scale, u0, u1, warps, h, pitch);
         else
-            add_units<WIDE, 4>(p, ring, B, toks, count, scale, u0, u1, warps, h, pitch);
+            add_units<WIDE, 6>(p, ring, B, toks, count, scale, u0, u1, warps, h, pitch);
         __syncthreads();  // h is read
     }
     if (busy)
@@ -1054,7 +1085,7 @@ cudaError_t launch_lora(const Lora &a, int sm_count, void *workspace, unsigned *
     const bool wide = a.rank % 32 == 0, fused = a.rank <= 32 && a.rank * a.K <= 32 * 8192;
     const int sums_bytes = fused ? (warps / ranks > 1 ? warps / ranks : 1) * TILE * (16 * ranks + 4) * 4 : 0;
     // as many stages of a warp's ring as two CTAs an SM leave room for
-    const int fit = (UP_SMEM - 2048 - h_bytes - sums_bytes) / (warps * stage);
+    const int fit = (UP_SMEM - h_bytes - sums_bytes) / (warps * stage);
     p.warps = warps;
     p.stages = fit < UP_MAX_STAGES ? fit : UP_MAX_STAGES;
     const int smem = warps * p.stages * stage + h_bytes + sums_bytes;

@@ -593,8 +593,8 @@ size_t moe_workspace_bytes(int64_t tokens, int64_t hidden, int64_t inter,
  *            be y itself (the same address and stride)
  *   workspace  device, >= lora_workspace_bytes(...) bytes; contents are
  *            clobbered
- * (Strides are not looked at for one token.)  Sums in fp32; A_a x enters the
- * second product with 16 bits.  K and rank are multiples of 8, rank <= 256,
+ * (Strides are not looked at for one token.)  Sums in fp32, A_a x with all of
+ * its 24 bits.  K and rank are multiples of 8, rank <= 256,
  * K <= 2^20, N <= 2^24, adapters <= 2^20; an adapter of a lower rank is padded
  * with zeros.  Only the used adapters are read, and a token's NaN or infinity
  * stays with that token.  One or two launches. */
