@@ -13,8 +13,10 @@
 // exp((l - max) / T), a row's vocabulary cut among CTAs.  In the second, every CTA of
 // a sequence joins those, decides which drafts are accepted, and goes over its cut of
 // the one row that matters; the last of them writes the result.  Without drafts the race
-// needs no sum: the largest (l - max) / T - log e is found in the first launch, and the
-// second only joins (256 x 128256: 37 us, 56 with a second pass).
+// needs no sum: the largest l / T - log e is found in the first launch, and the second only
+// joins (256 x 128256: 37 us, 56 with a second pass).  There the best so far is kept as l and
+// log e, not as a score relative to some maximum, and two of them are compared by their
+// difference, as if exactly: equal ones stay equal, and how a row is cut decides nothing.
 //
 // What bounds it: the logits of all rows and, for one row a sequence, q and e, from
 // HBM; for few sequences the chain of dependent loads of two launches.  Loads are 16
@@ -54,8 +56,9 @@ struct VerifyArgs {
     float *logprobs;
     int seqs, queries, vocab, parts1, parts2;
     bool raced;          // no drafts: the first launch does it all but the joins
-    float4 *stats;       // [rows][parts1]: maximum, sum, place of the maximum
-    float2 *best;        // [seqs][parts2]: score and place ([seqs][parts1] where the first launch raced)
+    float4 *stats;       // [rows][parts1]: maximum, sum, place of the maximum (of greedy rows)
+    float2 *best;        // [seqs][parts2]: score and place; [seqs][parts1] where the first launch raced: logit
+                         // and log2 e of the best, whose place stands in stats
     unsigned *arrived;   // [seqs]
 };
 
@@ -235,6 +238,52 @@ __device__ __forceinline__ Pick best_lane(Pick a)
     return a;
 }
 
+// The best of some elements in a race without a sum: the largest x c - log2 e.
+struct Runner {
+    float x, log_e;  // -infinity and 0 where there is none
+    int at;
+};
+// By how much a leads b; exact in its sign but for the last of 45 bits of the terms.
+__device__ __forceinline__ float lead(const Runner &a, const Runner &b, float c)
+{
+    const float dx = a.x - b.x, dl = a.log_e - b.log_e, p = __fmul_rn(dx, c), r = p - dl;
+    if (fabsf(r) >= 0x1p-20f * (fabsf(p) + fabsf(dl)))
+        return r;
+    // r is exact: what the differences and the product were rounded by
+    const float tx = dx - a.x, tl = dl - a.log_e;
+    const float ex = (a.x - (dx - tx)) - (b.x + tx), el = (a.log_e - (dl - tl)) - (b.log_e + tl);
+    return r + ((fmaf(dx, c, -p) + ex * c) - el);
+}
+// The one that leads, the lower place where none does.
+__device__ __forceinline__ Runner better(const Runner &a, const Runner &b, float c)
+{
+    const float d = lead(a, b, c);
+    return d > 0.f || (!(d < 0.f) && (unsigned)a.at < (unsigned)b.at) ? a : b;
+}
+// Below `score` by more than two fp32 scores (x - ref) c - log2 e of equal elements differ, each
+// of whose terms is at most 150 above it and is rounded three times.
+__device__ __forceinline__ float below(float score) { return score - (fabsf(score) * 0x1p-21f + 0x1p-14f); }
+// The best of the lanes, by scores relative to any number `ref`, of which hardly ever two are so near.
+// (All of it by `better` took 0.4 us.)
+__device__ __forceinline__ Runner best_lane(Runner a, float ref, float c)
+{
+    const float score = (a.x - ref) * c - a.log_e;
+    float top = score;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1)
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+    const unsigned near = __ballot_sync(0xffffffffu, score > below(top));
+    if (__popc(near) == 1) {
+        const int from = __ffs(near) - 1;
+        return {__shfl_sync(0xffffffffu, a.x, from), __shfl_sync(0xffffffffu, a.log_e, from), __shfl_sync(0xffffffffu, a.at, from)};
+    }
+    if (top > -INFINITY)
+#pragma unroll 1
+        for (int o = 16; o > 0; o >>= 1)
+            a = better(a, {__shfl_xor_sync(0xffffffffu, a.x, o), __shfl_xor_sync(0xffffffffu, a.log_e, o), __shfl_xor_sync(0xffffffffu, a.at, o)}, c);
+    return a;
+}
+
 // 1 / e enters as -log2 e, so that the race of a whole row needs no sum.
 __device__ __forceinline__ float log2_of(float x)
 {
@@ -243,15 +292,32 @@ __device__ __forceinline__ float log2_of(float x)
     return y;
 }
 
+// A row that is raced over, its noise, and where this CTA's loads of it end.
+struct RaceRow {
+    const void *row;
+    const float *e;
+    int end;
+};
+
+// Element j of consecutive loads.
+template <int N>
+__device__ __forceinline__ float element(const float4 (&e)[N], int j)
+{
+    const float4 f = e[j / 4];
+    return j % 4 == 0 ? f.x : (j % 4 == 1 ? f.y : (j % 4 == 2 ? f.z : f.w));
+}
+
 // Adds U loads of a row, the first of which begins at element `at`, the others `step`
-// elements further on each, to a thread's sums; RACE: and to its race, with the same elements' e.
+// elements further on each, to a thread's sums; RACE: and to its warp's race, with the same
+// elements' e.
 // batch: `at` of the loads with the first of its maxima.  Four to five instructions an element:
 // with every element cleaned by itself there were fifteen, and the pass was bound by them
 // (64 x 5 rows of 151936: 25.5 us).  So a NaN or +infinity is found by what it makes of the
-// sum, and the loads are cleaned only then.
+// sum, and the loads are cleaned only then.  more: many follow, and the lanes of a warp share their
+// best (in every batch, 17 x 50257 took 6.4 us, 5.6 so).
 template <bool F32, int U, bool RACE>
-__device__ __forceinline__ void add_loads(Sum &s, const uint4 (&r)[U], int at, int step, const Heat &heat, int &batch, Pick &best,
-                                          const float4 (&e)[RACE ? U : 1][F32 ? 1 : 2])
+__device__ __forceinline__ void add_loads(Sum &s, const uint4 (&r)[U], int at, int step, bool more, const Heat &heat, int &batch, Runner &best,
+                                          const float4 (&e)[RACE ? U : 1][F32 ? 1 : 2], const RaceRow &race)
 {
     constexpr int W = F32 ? 4 : 8;
     float top = top_of<F32, U>(r);
@@ -260,9 +326,9 @@ __device__ __forceinline__ void add_loads(Sum &s, const uint4 (&r)[U], int at, i
     const float m = fmaxf(s.m, top), ref = m == -INFINITY ? 0.f : m;
     float2 sum[2] = {};
     const float2 minus = {-ref, -ref}, c = {heat.c, heat.c};
-    if (RACE && m > s.m)
-        best.score += (s.m - m) * heat.c;  // relative to the new maximum; -infinity while there was none
-    float score[RACE ? U * W : 1], high = RACE ? best.score : 0.f;
+    // scores relative to the thread's maximum so far, of which those above `bar` may lead the warp's best
+    float score[RACE ? U * W : 1], high = -INFINITY;
+    const float bar = RACE ? below((best.x - ref) * heat.c - best.log_e) : 0.f;
 #pragma unroll
     for (int i = 0; i < U; ++i) {
         float x[W];
@@ -281,9 +347,10 @@ __device__ __forceinline__ void add_loads(Sum &s, const uint4 (&r)[U], int at, i
     }
     const float2 both = add2(sum[0], sum[1]);
     float z = both.x + both.y;
+    bool found = false;
     if (odd || z != z) {
         z = 0.f;
-        high = best.score;
+        found = true;
 #pragma unroll 1
         for (int i = 0; i < U; ++i) {
             uint4 one = r[0];
@@ -296,29 +363,46 @@ __device__ __forceinline__ void add_loads(Sum &s, const uint4 (&r)[U], int at, i
 #pragma unroll
             for (int j = 0; j < W; ++j) {
                 z += exp2_of((x[j] - ref) * heat.c);
-                if constexpr (RACE) {
-                    float f = 0.f;
+            }
+        }
+    }
+    if constexpr (RACE) {
+        // Seldom in a long row, whose warps' lanes share their best: with a thread's own some lane
+        // came in at most batches.
+        if (__any_sync(0xffffffffu, found || high > bar)) {
+            const float least = fmaxf(bar, below(high));
+            Runner top = {-INFINITY, 0.f, -1};
+            unsigned near = 0u;
 #pragma unroll
-                    for (int k = 0; k < U; ++k)
-                        if (i == k)
-                            f = j % 4 == 0 ? e[k][j / 4].x : (j % 4 == 1 ? e[k][j / 4].y : (j % 4 == 2 ? e[k][j / 4].z : e[k][j / 4].w));
-                    const float t = (x[j] - ref) * heat.c - log2_of(f);
-                    if (t > high) {
-                        high = t;
-                        best = {t, at + i * step + j};
+            for (int i = U - 1; i >= 0; --i) {
+                float x[W];
+                raw<F32>(r[i], x);
+#pragma unroll
+                for (int j = W - 1; j >= 0; --j)
+                    if (score[i * W + j] > least) {
+                        near |= 1u << (i * W + j);
+                        top = {x[j], element(e[i], j), at + i * step + j};
+                    }
+            }
+            top.log_e = log2_of(top.log_e);
+            near = found ? (1u << (U * W)) - 1u : (high > bar ? near : 0u);
+            if (__popc(near) == 1 && below(below(high)) > bar) {
+                best = top;
+            } else {  // one by one, loaded again: a short code for what is rare
+#pragma unroll 1
+                for (; near != 0u; near &= near - 1u) {
+                    const int k = __ffs(near) - 1, v = at + k / W * step + k % W;
+                    if (v < race.end) {
+                        const Runner one = {logit<F32>(race.row, v), log2_of(__ldg(race.e + v)), v};
+                        if ((one.x - ref) * heat.c - one.log_e > bar)
+                            best = better(one, best, heat.c);
                     }
                 }
             }
-        }
-    } else if constexpr (RACE) {
-        if (high > best.score) {
-            best.score = high;
-#pragma unroll
-            for (int i = U - 1; i >= 0; --i)
-#pragma unroll
-                for (int j = W - 1; j >= 0; --j)
-                    if (score[i * W + j] == high)
-                        best.at = at + i * step + j;
+            if (more) {
+                const float first = __shfl_sync(0xffffffffu, best.x, 0);
+                best = best_lane(best, first > -INFINITY ? first : 0.f, heat.c);
+            }
         }
     }
     if (m > s.m) {
@@ -362,7 +446,7 @@ __global__ void __launch_bounds__(THREADS, RACE ? race_ctas(F32) : rows_ctas(F32
     constexpr int W = F32 ? 4 : 8, U = RACE ? 2 : 4;         // elements of a load, loads at a time
     constexpr int E = W / 4, L = E + (RACE == RACE_SHIFTED);  // a load's e, and what is loaded for them
     __shared__ Sum part[WARPS];
-    __shared__ Pick part_best[WARPS];
+    __shared__ Runner part_best[WARPS];
     __shared__ int place;
     const int row = blockIdx.x / p.parts1, cut = blockIdx.x % p.parts1;
     const int seq = row / p.queries, query = row % p.queries;
@@ -403,7 +487,8 @@ __global__ void __launch_bounds__(THREADS, RACE ? race_ctas(F32) : rows_ctas(F32
         return;
     Sum s = {-INFINITY, 0.f};
     int batch = 0;
-    Pick best = {-INFINITY, -1};
+    Runner best = {-INFINITY, 0.f, -1};
+    const RaceRow race = {static_cast<const uint8_t *>(p.logits) + begin * (16 / W), p.noise + noise, hi * W - a};
     for (int from = lo; from < hi; from += U * THREADS) {
         uint4 now[U];
         float4 ne[RACE ? U : 1][E];
@@ -427,7 +512,7 @@ __global__ void __launch_bounds__(THREADS, RACE ? race_ctas(F32) : rows_ctas(F32
                 if constexpr (RACE != NO_RACE)
                     place_e<E>(se[i], ne[i], 0);
             }
-            add_loads<F32, N, RACE != NO_RACE>(s, some, at, THREADS * W, heat, batch, best, se);
+            add_loads<F32, N, RACE != NO_RACE>(s, some, at, THREADS * W, hi - from > 5 * U * THREADS, heat, batch, best, se, race);
         };
         if (U > 2 && hi - from > 2 * THREADS)
             add(Int<U>());
@@ -441,22 +526,18 @@ __global__ void __launch_bounds__(THREADS, RACE ? race_ctas(F32) : rows_ctas(F32
     const bool odd = cut == 0 && (int)threadIdx.x < head + tail;  // this thread has one
     const int odd_at = (int)threadIdx.x < head ? threadIdx.x : p.vocab - tail + threadIdx.x - head;
     if (odd) {
-        const float x = logit<F32>(p.logits, begin + odd_at), m = s.m;
+        const float x = logit<F32>(p.logits, begin + odd_at);
         s = joined(s, {x, x == -INFINITY ? 0.f : 1.f}, heat.c);
         if (RACE) {
-            const float t = x == -INFINITY ? x : (x - s.m) * heat.c - log2_of(__ldg(p.noise + noise + odd_at));
-            if (best.at >= 0)
-                best.score += (m - s.m) * heat.c;
-            if (t > -INFINITY)
-                best = better(best, {t, odd_at});
+            const Runner one = {x, log2_of(__ldg(p.noise + noise + odd_at)), odd_at};
+            if (x > -INFINITY && one.log_e < INFINITY)
+                best = better(one, best, heat.c);
         }
     }
     const float m = s.m;
     s = joined_lanes(s, heat.c);
-    if (RACE) {
-        best.score += best.at >= 0 ? (m - s.m) * heat.c : 0.f;
-        best = best_lane(best);
-    }
+    if (RACE)
+        best = best_lane(best, s.m > -INFINITY ? s.m : 0.f, heat.c);
     if ((threadIdx.x & 31) == 0) {
         part[threadIdx.x >> 5] = s;
         part_best[threadIdx.x >> 5] = best;
@@ -493,17 +574,19 @@ __global__ void __launch_bounds__(THREADS, RACE ? race_ctas(F32) : rows_ctas(F32
         }
         __syncthreads();
     }
+    if (RACE && threadIdx.x < 32) {
+        best = threadIdx.x < WARPS ? part_best[threadIdx.x] : Runner{-INFINITY, 0.f, -1};
+        best = best_lane(best, s.m > -INFINITY ? s.m : 0.f, heat.c);
+    }
     if (threadIdx.x == 0) {
         for (int w = 1; w < WARPS; ++w)
             s = joined(s, part[w], heat.c);
-        p.stats[(int64_t)row * p.parts1 + cut] = make_float4(s.m, s.z, __int_as_float(heat.greedy && s.m > -INFINITY ? place : -1), 0.f);
+        int at = heat.greedy && s.m > -INFINITY ? place : -1;
         if (RACE) {
-            best = {-INFINITY, -1};
-            for (int w = 0; w < WARPS; ++w)
-                if (part_best[w].at >= 0)
-                    best = better(best, {part_best[w].score + (part[w].m - s.m) * heat.c, part_best[w].at});
-            p.best[(int64_t)seq * p.parts1 + cut] = make_float2(best.score, __int_as_float(best.at));
+            p.best[(int64_t)seq * p.parts1 + cut] = make_float2(best.x, best.log_e);
+            at = heat.greedy ? at : best.at;
         }
+        p.stats[(int64_t)row * p.parts1 + cut] = make_float4(s.m, s.z, __int_as_float(at), 0.f);
     }
 }
 
@@ -760,14 +843,12 @@ __global__ void __launch_bounds__(THREADS, PICK_CTAS) verify_pick_kernel(const V
     const bool race = !heat.greedy && s.z > 0.f;  // else there is nothing to draw, or nothing to draw from
     const bool rest = taken < count;              // a draft was rejected here
     if (race && p.raced) {
-        Pick best = {-INFINITY, -1};
+        Runner best = {-INFINITY, 0.f, -1};
         if (lane < p.parts1) {
             const float2 v = __ldcg(p.best + (int64_t)seq * p.parts1 + lane);
-            const float m = __ldcg(p.stats + row * p.parts1 + lane).x;
-            if (__float_as_int(v.y) >= 0)
-                best = {v.x + (m - s.m) * heat.c, __float_as_int(v.y)};
+            best = {v.x, v.y, __float_as_int(__ldcg(p.stats + row * p.parts1 + lane).z)};
         }
-        token = best_lane(best).at;
+        token = best_lane(best, s.m, heat.c).at;
     } else if (race) {
         const int64_t q_row = ((int64_t)seq * drafts + taken) * p.vocab;
         const float *q = rest && p.probs != nullptr ? p.probs + q_row : nullptr;
