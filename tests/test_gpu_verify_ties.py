@@ -56,3 +56,22 @@ def test_the_batch_does_not_decide(cuda, dtype):
     score = logits.double()[:, 0] / heat.double()[:, None] - noise.double().log()
     best = score.amax(1, keepdim=True)
     assert torch.equal(want.long(), (score >= best - 1e-9).int().argmax(1))
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("vocab", [40, 4099, 33000, 151936])
+@pytest.mark.parametrize("n", [0, 2])
+def test_a_greedy_sequences_noise_does_not_matter(cuda, dtype, vocab, n):
+    g = torch.Generator(device=cuda).manual_seed(vocab)
+    logits = torch.randint(-30, 20, (6, n + 1, vocab), generator=g, device=cuda).to(dtype)
+    heat = torch.tensor([0.0, 1.0, -1.0, 0.0, 0.5, float("nan")], device=cuda)
+    noise = torch.empty(6, vocab, device=cuda).exponential_(generator=g)
+    drafts, u = torch.zeros(6, n, dtype=torch.int32, device=cuda), torch.ones(6, n, device=cuda)
+    want = w4q.verify_drafts(logits, drafts, u, noise, temperature=heat)
+    greedy = ~(heat > 0)
+    first = want[0][greedy, want[1][greedy].long()]
+    rows = logits[greedy, want[1][greedy].long()].float()
+    assert torch.equal(first.long(), (rows == rows.amax(1, keepdim=True)).int().argmax(1))
+    noise[greedy] = torch.tensor([float("nan"), 0.0, float("inf"), -1.0], device=cuda)[torch.randint(4, (4, vocab), generator=g, device=cuda)]
+    got = w4q.verify_drafts(logits, drafts, u, noise, temperature=heat)
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
