@@ -78,8 +78,11 @@ __device__ __forceinline__ float top_of(const Eight &e)
 // The codes of y under `scale`: 0 where it is 0, infinite or NaN (the scale then says
 // that the values are not finite).  rint(y / scale) as the lowest byte of y * (1 / scale) +
 // 1.5 * 2^23, one rounding: the reciprocal's own is 2^-17 of a step, and |y| <= 127 scale
-// (1 + 2^-23) needs no clamp.  (With the quotients of the activation quantizer, which
-// decide ties as IEEE divisions do, 3001 x 8192 took 39 us, 31 so.)
+// (1 + 2^-23) needs no clamp.  The activation quantizer rounds the quotient, which gives the
+// other code of two where y / scale lies within 2^-16 of their middle, from which both are
+// equally far.  (Its rule with quotients everywhere: 3001 x 8192 by groups 39 us, 30.7 so;
+// with quotients only where a second product with a reciprocal two bits off gives another
+// code: 32.4, without a residual 24.5 instead of 21.9, 700 x 12288 by rows 10.1 instead of 7.0.)
 __device__ __forceinline__ uint2 codes_of(const Eight &y, float scale)
 {
     uint32_t q[2] = {0u, 0u};

@@ -441,7 +441,9 @@ int add_rms_norm(const void *x, int64_t x_stride, const void *residual,
 /* The same norm into the codes of w4a8_gemm_codes: over the row (row_scale != 0)
  * or over each group of 32, in fp32,
  *   scale = max|y| / 127;  code = rint(y * (1 / scale)) in [-127, 127];  where
- *   scale is 0, NaN or infinite the codes are 0.
+ *   scale is 0, NaN or infinite the codes are 0.  (w4a8_quantize_act rounds the
+ *   quotient y / scale: one code may differ where that lies within 2^-16 of the
+ *   middle of two.)
  *   codes   device, int8 [tokens][hidden] (written)
  *   scales  device, f32 [tokens] with row_scale, else [tokens][hidden/32]
  *   out     device, bf16 [tokens][hidden]: y as by add_rms_norm too, or NULL
