@@ -429,10 +429,13 @@ int qk_norm_rope(const void *q, const void *k, int64_t tokens, int q_heads,
  *                with a residual.  It may be x or residual itself (the same
  *                address and stride).
  *   out          device, bf16 [tokens][hidden] (written)
- * hidden a multiple of 8 up to 32768; tokens = 0 launches nothing.  A row that
- * holds a NaN or infinity, whose squares overflow (values from 2^56 on may),
- * or of zeros with eps = 0 gives NaN or unspecified values in that row alone.
- * One launch. */
+ * hidden a multiple of 8 up to 32768; tokens = 0 launches nothing.  The products
+ * s * weight and the squares are formed in fp32, without scaling: a row that holds
+ * a NaN or infinity, whose squares overflow (values from 2^56 on may), a product
+ * of which is 2^128 or more, or, with eps = 0, whose squares are all 0 (zeros, and
+ * values below 2^-75) gives NaN, infinite or unspecified values in that row alone;
+ * products below 2^-126, and with eps = 0 rows whose largest values are below 2^-55,
+ * lose bits.  One launch. */
 int add_rms_norm(const void *x, int64_t x_stride, const void *residual,
                  int64_t residual_stride, const void *weight, float eps,
                  int64_t tokens, int64_t hidden, void *sum_out,
