@@ -1021,18 +1021,18 @@ namespace {
 // Clusters of `cfg` that the device runs at once: not as many as its SMs have room for, since
 // a cluster's CTAs lie together (36 of 8 and 74 of 4 on 152 SMs), and one more takes as long as
 // all of them (64 tokens of rank 16, 6656 to 19968: 16.6 us, 10.7 so).
-cudaError_t clusters_at_once(const cudaLaunchConfig_t &cfg, void (*fn)(LoraArgs), int size, int *n)
+cudaError_t clusters_at_once(const cudaLaunchConfig_t &cfg, bool wide, int size, int *n)
 {
-    static std::atomic<int> known[64][2];
+    static std::atomic<int> known[64][2][2];  // a device's, of each kernel and size
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess)
         return e;
-    std::atomic<int> *slot = dev >= 0 && dev < 64 ? &known[dev][size == MAX_CLUSTER] : nullptr;
+    std::atomic<int> *slot = dev >= 0 && dev < 64 ? &known[dev][wide][size == MAX_CLUSTER] : nullptr;
     *n = slot ? slot->load(std::memory_order_relaxed) : 0;
     if (*n > 0)
         return cudaSuccess;
-    e = cudaOccupancyMaxActiveClusters(n, fn, &cfg);
+    e = cudaOccupancyMaxActiveClusters(n, wide ? lora_cluster_kernel<true> : lora_cluster_kernel<false>, &cfg);
     if (e == cudaSuccess && *n < 1)
         e = cudaErrorInvalidConfiguration;
     if (e == cudaSuccess && slot)
@@ -1114,7 +1114,7 @@ cudaError_t launch_lora(const Lora &a, int sm_count, void *workspace, unsigned *
         cfg.attrs = attr;
         cfg.numAttrs = 1;
         int most = 0;
-        e = clusters_at_once(cfg, fn, p.cluster, &most);
+        e = clusters_at_once(cfg, wide, p.cluster, &most);
         if (e != cudaSuccess)
             return e;
         // 4 of rank 16, 6656 to 19968, 4 tokens: 9.9 us with 36 clusters of 36, 8.0 with 32, 7.3 with
