@@ -623,9 +623,9 @@ struct Race {
     float m, c, inv_z;
     Pick best;
 
-    // N elements, the first at index v, the others `step` further on each
+    // N elements from index v on
     template <int N>
-    __device__ __forceinline__ void run(int v, int step, const float (&x)[N], const float (&q)[N], const float (&e)[N])
+    __device__ __forceinline__ void run(int v, const float (&x)[N], const float (&q)[N], const float (&e)[N])
     {
         float score[N], top = 0.f;
 #pragma unroll
@@ -640,7 +640,7 @@ struct Race {
 #pragma unroll
             for (int j = N - 1; j >= 0; --j)
                 if (score[j] == top)
-                    best.at = v + j * step;
+                    best.at = v + j;
         }
     }
 };
@@ -780,13 +780,13 @@ __device__ Pick row_race(const VerifyArgs &p, const Stat &s, const Heat &heat, i
 #pragma unroll
             for (int j = 0; j < 8; ++j)
                 x[j] = out == v + j ? -INFINITY : x[j];
-        r.run<8>(v, 1, x, qv, ev);
+        r.run<8>(v, x, qv, ev);
     }
     if (!VEC && end_at >= 0) {
         const float x[1] = {end_x}, qv[1] = {end_q}, ev[1] = {end_e};
         const Pick before = r.best;
         r.best = {0.f, -1};
-        r.run<1>(end_at, 1, x, qv, ev);
+        r.run<1>(end_at, x, qv, ev);
         r.best = better(before, r.best);
     }
     Pick best = best_lane(r.best);
