@@ -218,8 +218,11 @@ cudaError_t launch_form(const NormArgs &p, int v, dim3 grid, dim3 block, cudaStr
     }
 }
 
-// Threads of an SM with which the registers of these kernels leave it.
-constexpr int at_once(int chunks, bool codes) { return chunks > 1 ? 1024 : (codes ? 1280 : 2048); }
+// Threads that an SM's 65536 registers hold of these kernels: 28 each with one chunk, 34 with two (40
+// are given out), 40 to 42 for codes (48), 56 to 60 with four (64).  (With 1024 for two chunks and 1280
+// for codes with one, 1500 x 2048 by groups took 5.5 us, 4.2 so, 700 x 4096 in bf16 4.8, now 4.0, 300 x
+// 6656 by rows 3.9, now 3.5; 200 x 16384 in bf16 without a residual 4.1, now 4.8.)
+constexpr int at_once(int chunks, bool codes) { return chunks > 2 ? 1024 : (chunks > 1 ? (codes ? 1344 : 1632) : 2048); }
 
 }  // namespace
 
