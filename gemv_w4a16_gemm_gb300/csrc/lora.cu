@@ -15,11 +15,11 @@
 // a row lie in the lanes' registers, and the weights need no rearrangement.  h enters the
 // second product as the sum of three bf16, which is all of its 24 bits, so that a row is as
 // precise alone as in any batch.  (As two, 16 bits, one result in 600 was another bf16 than the
-// exact sum's, one in 4000 to 11000 so; the third costs nothing for up to 2 tokens of an adapter, 0.3 us in 11 for 16 of
-// rank 32, and 5 in 25 for 64 of rank 256, whose time is the MMAs'.)
+// exact sum's, one in 4000 to 11000 so; the third costs nothing for up to 2 tokens of an adapter, 0.3 us in 11 for 8 of
+// rank 32, and 5 in 25 for 64 of rank 256, where two warps a CTA multiply.)
 //
 // What bounds it: the used adapters' bytes, read once each, for large ones (64 adapters of
-// rank 64, 6656 to 19968: 220 MB in 45.6 us, 4.9 TB/s with both launches' beginnings, of
+// rank 64, 6656 to 19968: 220 MB in 46.0 us, 4.8 TB/s with both launches' beginnings, of
 // which the second product runs at 7); for few the chain of dependent loads (rank 16,
 // 4096 to 4096: 4.8 us).  In the second product every warp streams its own pieces of the
 // weights through a ring of bulk copies in shared memory, so that some 100 KB an SM are in
@@ -374,8 +374,8 @@ __host__ __device__ constexpr int up_block_warps(int rank) { return rank <= 128 
 // tokens: 1 tile, the first bf16 of each in columns 0 and 1, the second in 2 and 3, the third
 // in 4 and 5; up to 4: 2 tiles, the first bf16 in columns 0 to 3 of one, the second in 4 to 7,
 // the third in 0 to 3 of the other; up to 8: 3 tiles, one for each bf16; up to 16: 6.
-// (mma.sync's rate, a sixteenth of tcgen05's, is what counts here: with the tokens as the 16
-// rows of the other operand 64 adapters of rank 64 took 49 us.)
+// (With the tokens as the 16 rows of the other operand, twice the MMAs, 64 adapters of rank 64
+// took 49 us instead of 45.6.)
 __host__ __device__ constexpr int h_tiles(int count) { return count <= 2 ? 1 : (count <= 4 ? 2 : (count <= 8 ? 3 : 6)); }
 __host__ __device__ constexpr int h_sums(int nt) { return (nt + 2) / 3; }  // tiles of results
 

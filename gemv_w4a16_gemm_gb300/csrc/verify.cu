@@ -39,8 +39,8 @@ constexpr int MAX_PARTS = 32;    // cuts of a row: one a lane where they are joi
 constexpr int PART_MIN = 8192;   // elements that a CTA's beginning and end are worth: 64 x 5 rows of 151936 cut in
                                  // 2 (one wave) take 35 us, in 1, 4, 7, 14: 46, 37, 38, 43
 constexpr int MAX_QUERIES = 64;
-// CTAs of an SM in the launches.  (Racing, bf16: 256 x 128256 37 us, 38 and 67 with 3 and 4,
-// which spill; fp32: 64 x 128256 15 us.  Else bf16: 64 x 5 rows of 151936 34.9, 35.7 with 4; fp32,
+// CTAs of an SM in the launches.  (Racing, bf16: 256 x 128256 37 us, 65 with 3, which spills; fp32:
+// 64 x 32000 7.2 us, 256 x 128256 49; 7.8 and 46 with 4, 7.1 and 55 with 2.  Else bf16: 64 x 5 rows of 151936 34.9, 35.7 with 4; fp32,
 // which spills with 5: 64 x 4 rows of 32000 14.3, 16.1 and 14.9 with 3 and 5.)
 constexpr int PICK_CTAS = 3;
 constexpr int rows_ctas(bool f32) { return f32 ? 4 : 5; }
@@ -310,9 +310,9 @@ __device__ __forceinline__ float element(const float4 (&e)[N], int j)
 // Adds U loads of a row, the first of which begins at element `at`, the others `step`
 // elements further on each, to a thread's sums; RACE: and to its warp's race, with the same
 // elements' e.
-// batch: `at` of the loads with the first of its maxima.  Four to five instructions an element:
-// with every element cleaned by itself there were fifteen, and the pass was bound by them
-// (64 x 5 rows of 151936: 25.5 us).  So a NaN or +infinity is found by what it makes of the
+// batch: `at` of the loads with the first of its maxima.  With every element cleaned by itself
+// the pass over 64 x 5 rows of 151936 executed 15 instructions an element and was bound by them
+// (25.5 us); 7.8 so, in 17.  A NaN or +infinity is found by what it makes of the
 // sum, and the loads are cleaned only then.  more: many follow, and the lanes of a warp share their
 // best (in every batch, 17 x 50257 took 6.4 us, 5.6 so).
 template <bool F32, int U, bool RACE>
