@@ -6,7 +6,7 @@
 // same checks made in Python took 25 to 37 us a call on the host.  Here they
 // read the tensors' fields directly: 2.3 to 2.7 us with the launch (4 to 5 with
 // the two of the adapters or the verification, 7 with the four of the experts),
-// 0.8 more for each tensor that the call makes, and 11 for an attention
+// 0.9 more for each tensor that the call makes, and 11 for an attention
 // workspace, which has to be zeroed.
 //
 // Every function takes positional arguments from w4q.py and returns
@@ -135,7 +135,7 @@ bool only_allocates()
            !(torch.deterministicAlgorithms() && torch.deterministicFillUninitializedMemory());
 }
 
-// (Straight from the allocator 0.8 us, 2.0 by at::empty.)
+// (Straight from the allocator 0.9 us, 2.0 by at::empty.)
 Tensor fresh(const Call &c, at::IntArrayRef shape, at::ScalarType type)
 {
     if (!only_allocates())

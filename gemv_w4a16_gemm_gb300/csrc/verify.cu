@@ -40,8 +40,9 @@ constexpr int PART_MIN = 8192;   // elements that a CTA's beginning and end are 
                                  // 2 (one wave) take 35 us, in 1, 4, 7, 14: 46, 37, 38, 43
 constexpr int MAX_QUERIES = 64;
 // CTAs of an SM in the launches.  (Racing, bf16: 256 x 128256 37 us, 65 with 3, which spills; fp32:
-// 64 x 32000 7.2 us, 256 x 128256 49; 7.8 and 46 with 4, 7.1 and 55 with 2.  Else bf16: 64 x 5 rows of 151936 34.9, 35.7 with 4; fp32,
-// which spills with 5: 64 x 4 rows of 32000 14.3, 16.1 and 14.9 with 3 and 5.)
+// 64 x 32000 7.2 us, 256 x 128256 49; 7.8 and 46 with 4, 7.1 and 55 with 2.  Else bf16: 64 x 5 rows
+// of 151936 34.9, 35.7 with 4; fp32, which spills with 5: 64 x 4 rows of 32000 14.3, 16.1 and 14.9
+// with 3 and 5.)
 constexpr int PICK_CTAS = 3;
 constexpr int rows_ctas(bool f32) { return f32 ? 4 : 5; }
 constexpr int race_ctas(bool f32) { return f32 ? 3 : 2; }
