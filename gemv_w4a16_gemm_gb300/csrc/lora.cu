@@ -15,8 +15,9 @@
 // a row lie in the lanes' registers, and the weights need no rearrangement.  h enters the
 // second product as the sum of three bf16, which is all of its 24 bits, so that a row is as
 // precise alone as in any batch.  (As two, 16 bits, one result in 600 was another bf16 than the
-// exact sum's, one in 4000 to 11000 so; the third costs nothing for up to 2 tokens of an adapter, 0.3 us in 11 for 8 of
-// rank 32, and 5 in 25 for 64 of rank 256, where two warps a CTA multiply.)
+// exact sum's, one in 4000 to 11000 so; the third costs nothing for up to 2 tokens of an
+// adapter, 0.3 us in 11 for 8 of rank 32, and 5 in 25 for 64 of rank 256, where two warps a CTA
+// multiply.)
 //
 // What bounds it: the used adapters' bytes, read once each, for large ones (64 adapters of
 // rank 64, 6656 to 19968: 220 MB in 46.0 us, 4.8 TB/s with both launches' beginnings, of

@@ -636,8 +636,8 @@ size_t lora_workspace_bytes(int64_t tokens, int64_t K, int64_t N, int64_t rank,
  *   temperature  device, fp32 [seqs], or NULL: 1.  T <= 0 or NaN: p is 1 at the
  *                largest logit, the lowest of equal ones
  *   uniforms     device, fp32 [seqs][draft_tokens], or NULL with draft_tokens = 0
- *   noise        device, fp32 [seqs][vocab], positive; rows of sequences whose T is 0
- *                do not matter
+ *   noise        device, fp32 [seqs][vocab], positive; what rows of sequences with
+ *                T <= 0 or NaN hold does not matter
  *   tokens       device, int32 [seqs][draft_tokens + 1] (written): the accepted
  *                drafts, the new token, then -1
  *   accepted     device, int32 [seqs] (written): how many were accepted
